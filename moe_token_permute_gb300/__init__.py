@@ -16,7 +16,7 @@ import torch
 from . import _binding as _b
 from ._binding import (MOE_FLAG_BARRIER_TIMEOUT, MOE_FLAG_CAPACITY_OVERFLOW,  # noqa: F401
                        MOE_FLAG_ID_OUT_OF_RANGE, MOE_FLAG_INV_OUT_OF_RANGE,
-                       MOE_FLAG_MAP_OUT_OF_RANGE, MOE_MAX_LOCAL_EXPERTS, MOE_MAX_TOPK,
+                       MOE_FLAG_MAP_OUT_OF_RANGE, MOE_FLAG_OFFSET_OUT_OF_RANGE, MOE_MAX_LOCAL_EXPERTS, MOE_MAX_TOPK,
                        MoeError, library_path)
 
 _DTYPES = {
@@ -208,6 +208,177 @@ def moe_unpermute(permuted_rows, topk_weights, inv_permuted_idx, out, *, workspa
     _b.check("moe_unpermute", _b.lib().moe_unpermute(
         _ptr(permuted_rows), permuted_rows.shape[0], _ptr(topk_weights),
         _ptr(inv_permuted_idx), T, H, K, _ptr(out), _ptr(workspace), _stream(stream)))
+
+
+_ACTIVATIONS = {"none": _b.MOE_ACT_NONE, "silu": _b.MOE_ACT_SILU, "gelu": _b.MOE_ACT_GELU,
+                "relu": _b.MOE_ACT_RELU}
+
+
+def _matrix(t, rows, cols, dtype, what):
+    """A contiguous matrix of `rows` x `cols` of the call's type, or None."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError(f"{what} is {t.dtype}; this call takes {dtype}")
+    if t.dim() < 2 or t.shape[-1] != cols or t.numel() != rows * cols:
+        raise ValueError(f"{what} must hold {rows} rows of {cols}; its shape is "
+                         f"{tuple(t.shape)}")
+
+
+def _expert_sizes(rows, num_rows, weight_shape, dtype, offset, activation):
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("the expert operators take bfloat16 or float16")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
+    E, N, K = weight_shape
+    if offset.dtype != torch.int64:
+        raise ValueError("expert_first_token_offset must be int64")
+    _need(offset, E + 1, "expert_first_token_offset")
+    _matrix(rows, num_rows, K, dtype, "the rows")
+    return E, N, K
+
+
+def _weight_shape(weight, d_weight):
+    t = weight if weight is not None else d_weight
+    if t is None or t.dim() != 3:
+        raise ValueError("the weight (or its gradient) must be [experts, out, in]")
+    return tuple(t.shape)
+
+
+def moe_expert_gated(permuted_rows, weight, expert_first_token_offset, out, *,
+                     activation="silu", preact=None, workspace=None, stream=None) -> None:
+    """out = act(x Wg[e]^T) * (x Wu[e]^T) for every row x of expert e (see
+    include/moe_experts.h).
+
+    permuted_rows [R, H] bf16 or fp16 in moe_permute's order, weight
+    [E_local, 2F, H] (an expert's F gate rows, then its F up rows),
+    expert_first_token_offset int64 [E_local+1], out [R, F], preact [R, 2F] or
+    None (gate and up before the activation, kept for the backward pass);
+    activation "silu", "gelu" (the tanh form), "relu" or "none"; workspace
+    optional (status word only).
+    """
+    R, dtype = permuted_rows.shape[0], weight.dtype
+    E, N, H = _expert_sizes(permuted_rows, R, _weight_shape(weight, None), dtype,
+                            expert_first_token_offset, activation)
+    if N % 2:
+        raise ValueError("weight must hold as many up rows as gate rows")
+    _matrix(out, R, N // 2, dtype, "out")
+    _matrix(preact, R, N, dtype, "preact")
+    _b.check("moe_expert_gated", _b.lib().moe_expert_gated(
+        _ptr(permuted_rows), _ptr(weight), _DTYPES[dtype], _ptr(expert_first_token_offset), R, H,
+        N // 2, E, _ACTIVATIONS[activation], _ptr(out), _ptr(preact), _ptr(workspace),
+        _stream(stream)))
+
+
+def moe_expert_gated_backward(d_out, permuted_rows, weight, expert_first_token_offset, preact,
+                              d_preact, *, activation="silu", d_rows=None, d_weight=None,
+                              workspace=None, stream=None) -> None:
+    """The gradients of moe_expert_gated (see include/moe_experts.h).
+
+    d_out [R, F], preact [R, 2F] as the forward pass wrote it; written:
+    d_preact [R, 2F], d_rows [R, H] and d_weight [E_local, 2F, H] where given.
+    permuted_rows may be None without d_weight, weight without d_rows.
+    """
+    R, dtype = d_out.shape[0], d_out.dtype
+    E, N, H = _expert_sizes(permuted_rows, R, _weight_shape(weight, d_weight), dtype,
+                            expert_first_token_offset, activation)
+    if N % 2:
+        raise ValueError("weight must hold as many up rows as gate rows")
+    for t, cols, what in ((d_out, N // 2, "d_out"), (preact, N, "preact"),
+                          (d_preact, N, "d_preact"), (d_rows, H, "d_rows")):
+        _matrix(t, R, cols, dtype, what)
+    for t, what in ((weight, "weight"), (d_weight, "d_weight")):
+        _matrix(t, E * N, H, dtype, what)
+    if (d_rows is not None and weight is None) or (d_weight is not None and permuted_rows is None):
+        raise ValueError("d_rows needs weight, and d_weight needs permuted_rows")
+    _b.check("moe_expert_gated_backward", _b.lib().moe_expert_gated_backward(
+        _ptr(d_out), _ptr(permuted_rows), _ptr(weight), _DTYPES[dtype],
+        _ptr(expert_first_token_offset), R, H, N // 2, E, _ACTIVATIONS[activation], _ptr(preact),
+        _ptr(d_preact), _ptr(d_rows), _ptr(d_weight), _ptr(workspace), _stream(stream)))
+
+
+def moe_expert_linear(rows, weight, expert_first_token_offset, out, *, bias=None,
+                      activation="none", residual=None, preact=None, workspace=None,
+                      stream=None) -> None:
+    """out = act(x W[e]^T + bias[e]) + residual for every row x of expert e
+    (see include/moe_experts.h).
+
+    rows [R, in], weight [E_local, out, in], bias [E_local, out] or None,
+    residual [R, out] or None (may be out itself), preact [R, out] or None
+    (the activation's argument, kept for the backward pass).
+    """
+    R, dtype = rows.shape[0], weight.dtype
+    E, N, K = _expert_sizes(rows, R, _weight_shape(weight, None), dtype,
+                            expert_first_token_offset, activation)
+    for t, what in ((out, "out"), (residual, "residual"), (preact, "preact")):
+        _matrix(t, R, N, dtype, what)
+    _matrix(bias, E, N, dtype, "bias")
+    _b.check("moe_expert_linear", _b.lib().moe_expert_linear(
+        _ptr(rows), _ptr(weight), _DTYPES[dtype], _ptr(expert_first_token_offset), R, K, N, E,
+        _ptr(bias), _ACTIVATIONS[activation], _ptr(residual), _ptr(out), _ptr(preact),
+        _ptr(workspace), _stream(stream)))
+
+
+def moe_expert_linear_backward(d_out, rows, weight, expert_first_token_offset, *,
+                               activation="none", preact=None, d_preact=None, d_rows=None,
+                               d_weight=None, d_bias=None, workspace=None, stream=None) -> None:
+    """The gradients of moe_expert_linear (see include/moe_experts.h); that of
+    the residual is d_out itself.
+
+    With an activation, preact [R, out] is what the forward pass wrote and
+    d_preact [R, out] is written; without one both are None.  d_rows [R, in],
+    d_weight [E_local, out, in] and d_bias [E_local, out] are written where
+    given; rows may be None without d_weight, weight without d_rows.
+    """
+    R, dtype = d_out.shape[0], d_out.dtype
+    E, N, K = _expert_sizes(rows, R, _weight_shape(weight, d_weight), dtype,
+                            expert_first_token_offset, activation)
+    for t, cols, what in ((d_out, N, "d_out"), (preact, N, "preact"), (d_preact, N, "d_preact"),
+                          (d_rows, K, "d_rows")):
+        _matrix(t, R, cols, dtype, what)
+    for t, what in ((weight, "weight"), (d_weight, "d_weight")):
+        _matrix(t, E * N, K, dtype, what)
+    _matrix(d_bias, E, N, dtype, "d_bias")
+    if (preact is None) != (activation == "none") or (d_preact is None) != (activation == "none"):
+        raise ValueError("preact and d_preact go with an activation, and only with one")
+    if (d_rows is not None and weight is None) or (d_weight is not None and rows is None):
+        raise ValueError("d_rows needs weight, and d_weight needs rows")
+    _b.check("moe_expert_linear_backward", _b.lib().moe_expert_linear_backward(
+        _ptr(d_out), _ptr(rows), _ptr(weight), _DTYPES[dtype], _ptr(expert_first_token_offset),
+        R, K, N, E, _ACTIVATIONS[activation], _ptr(preact), _ptr(d_preact), _ptr(d_rows),
+        _ptr(d_weight), _ptr(d_bias), _ptr(workspace), _stream(stream)))
+
+
+def moe_unpermute_backward(d_out, permuted_rows, topk_weights, inv_permuted_idx, d_rows,
+                           d_topk_weights, *, workspace=None, stream=None) -> None:
+    """The gradients of moe_unpermute (see include/moe_experts.h):
+    d_rows[p] = bf16(w[t,k] * d_out[t]) for p = inv[t*K+k], and
+    d_topk_weights[t,k] = <d_out[t], permuted_rows[p]> in fp32, 0 for a
+    dropped row.
+
+    d_out bf16 [T,H], permuted_rows bf16 [num_rows,H] (None without
+    d_topk_weights), d_rows bf16 [num_rows,H] or None, d_topk_weights fp32
+    [T,K] or None.
+    """
+    T, K = topk_weights.shape
+    H = d_out.shape[1]
+    if d_rows is None and d_topk_weights is None:
+        raise ValueError("nothing to compute: give d_rows or d_topk_weights")
+    if (permuted_rows is None) != (d_topk_weights is None):
+        raise ValueError("permuted_rows goes with d_topk_weights")
+    if topk_weights.dtype != torch.float32 or inv_permuted_idx.dtype != torch.int32:
+        raise ValueError("topk_weights must be float32 and inv_permuted_idx int32")
+    if d_out.dtype != torch.bfloat16:
+        raise ValueError("moe_unpermute_backward takes bf16 rows and writes bf16")
+    _need_rows(d_out, T, "d_out")
+    num_rows = (d_rows if permuted_rows is None else permuted_rows).shape[0]
+    _matrix(permuted_rows, num_rows, H, torch.bfloat16, "permuted_rows")
+    _matrix(d_rows, num_rows, H, torch.bfloat16, "d_rows")
+    _matrix(d_topk_weights, T, K, torch.float32, "d_topk_weights")
+    _need(inv_permuted_idx, T * K, "inv_permuted_idx")
+    _b.check("moe_unpermute_backward", _b.lib().moe_unpermute_backward(
+        _ptr(d_out), _ptr(permuted_rows), num_rows, _ptr(topk_weights), _ptr(inv_permuted_idx),
+        T, H, K, _ptr(d_rows), _ptr(d_topk_weights), _ptr(workspace), _stream(stream)))
 
 
 def moe_read_status(workspace, stream=None) -> int:

@@ -1,4 +1,5 @@
-"""ctypes binding of libmoe_permute.so (include/moe_permute.h).
+"""ctypes binding of libmoe_permute.so (include/moe_permute.h and
+include/moe_experts.h).
 
 Argument marshalling only: every step of permute and unpermute runs in the
 CUDA library.  If the library has not been built this module raises on first
@@ -32,6 +33,12 @@ MOE_FLAG_MAP_OUT_OF_RANGE = 2
 MOE_FLAG_INV_OUT_OF_RANGE = 4
 MOE_FLAG_BARRIER_TIMEOUT = 8
 MOE_FLAG_CAPACITY_OVERFLOW = 16
+MOE_FLAG_OFFSET_OUT_OF_RANGE = 32
+
+MOE_ACT_NONE = 0
+MOE_ACT_SILU = 1
+MOE_ACT_GELU = 2
+MOE_ACT_RELU = 3
 
 MOE_MAX_TOPK = 32
 MOE_MAX_LOCAL_EXPERTS = 1024
@@ -42,7 +49,7 @@ _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 
-# name -> (restype, argtypes); mirrors include/moe_permute.h
+# name -> (restype, argtypes); mirrors include/moe_permute.h and include/moe_experts.h
 SIGNATURES = {
     "moe_permute_supported": (ctypes.c_int, [ctypes.c_int]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -63,6 +70,17 @@ SIGNATURES = {
     "moe_permute_noalloc": (ctypes.c_int, [_P, ctypes.c_int, _P, _I64, _P, ctypes.c_int, _P,
                                            _I64, _I64, _I32, _I32, _I32,
                                            _P, _P, _P, _P, _P, _P]),
+    "moe_expert_gated": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, _I64, _I64, _I64, _I32,
+                                        ctypes.c_int, _P, _P, _P, _P]),
+    "moe_expert_gated_backward": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, _P, _I64, _I64, _I64,
+                                                 _I32, ctypes.c_int, _P, _P, _P, _P, _P, _P]),
+    "moe_expert_linear": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, _I64, _I64, _I64, _I32, _P,
+                                         ctypes.c_int, _P, _P, _P, _P, _P]),
+    "moe_expert_linear_backward": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, _P, _I64, _I64, _I64,
+                                                  _I32, ctypes.c_int, _P, _P, _P, _P, _P, _P,
+                                                  _P]),
+    "moe_unpermute_backward": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I64, _I64, _I32, _P, _P, _P,
+                                              _P]),
 }
 
 MOE_NOALLOC_SCRATCH_BYTES = (1 << 20) + 256

@@ -1,6 +1,9 @@
 """Build libmoe_permute.so (the C-ABI CUDA library) in-tree with nvcc, and
 beside it libmoe_permute_debug.so, the same sources with -DMOE_DEBUG_HOOKS
-(the test hook of include/moe_permute_debug.h).  The two compile in parallel.
+(the test hook of include/moe_permute_debug.h).
+
+Each source compiles to an object of its own, all of them in parallel, and
+each library is linked from its objects.
 
 Usage: python -m moe_token_permute_gb300.build [--verbose]
 Target: sm_103a only (GB300).  The libraries are linked against the shared
@@ -22,7 +25,8 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libmoe_permute.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 DEBUG_LIB_PATH = os.path.join(OUT_DIR, "libmoe_permute_debug.so")
-SOURCES = ["moe_permute_api.cu"]
+EXPERTS = os.path.join(PKG, "csrc_experts")
+SOURCES = [os.path.join(CSRC, "moe_permute_api.cu"), os.path.join(EXPERTS, "moe_experts_api.cu")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -43,8 +47,8 @@ def _cuda_lib_dir(nvcc: str) -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES]
-    files += glob.glob(os.path.join(CSRC, "*.cuh"))
+    files = SOURCES + glob.glob(os.path.join(CSRC, "*.cuh"))
+    files += glob.glob(os.path.join(EXPERTS, "*.cuh"))
     files += glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
     return files
 
@@ -56,36 +60,51 @@ def up_to_date(path: str = LIB_PATH) -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
-def _command(nvcc: str, out: str, defines, verbose: bool):
-    cmd = [nvcc, *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared",
+def _compile_command(nvcc: str, source: str, obj: str, defines, verbose: bool):
+    cmd = [nvcc, *ARCH, "-O3", "-lineinfo", "-std=c++17", "-c",
            "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", *defines,
-           "-I", INCLUDE, "-I", CSRC, "-cudart", "shared",
-           "-Xlinker", "-rpath," + _cuda_lib_dir(nvcc),
-           "-o", out] + [os.path.join(CSRC, s) for s in SOURCES]
+           "-I", INCLUDE, "-I", CSRC, "-o", obj, source]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     return cmd
 
 
+def _link_command(nvcc: str, objs, out: str):
+    return [nvcc, *ARCH, "-shared", "-cudart", "shared",
+            "-Xlinker", "-rpath," + _cuda_lib_dir(nvcc), "-o", out, *objs]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile the libraries that are missing or older than their sources
-    (both nvcc runs in parallel); returns the production library's path."""
+    (every nvcc runs in parallel); returns the production library's path."""
     targets = [(LIB_PATH, []), (DEBUG_LIB_PATH, ["-DMOE_DEBUG_HOOKS"])]
     todo = [(path, d) for path, d in targets if force or not up_to_date(path)]
     if not todo:
         return LIB_PATH
     nvcc = _nvcc()
     os.makedirs(OUT_DIR, exist_ok=True)
-    jobs = []
+    # Only the permute's source knows the debug hooks: the other objects are
+    # compiled once and linked into both libraries.
+    objects, jobs = {}, {}
     for path, defines in todo:
-        tmp = path + f".tmp{os.getpid()}"
-        jobs.append((subprocess.Popen(_command(nvcc, tmp, defines, verbose)), tmp, path))
-    failed = []
-    for proc, tmp, path in jobs:
-        if proc.wait() != 0:
-            failed.append(path)
-        else:
-            os.replace(tmp, path)
+        objects[path] = []
+        for src in SOURCES:
+            d = tuple(defines) if src == SOURCES[0] else ()
+            if (src, d) not in jobs:
+                obj = os.path.join(OUT_DIR, f"{os.path.basename(src)}.{len(jobs)}.{os.getpid()}.o")
+                jobs[src, d] = (subprocess.Popen(_compile_command(nvcc, src, obj, d, verbose)), obj)
+            objects[path].append(jobs[src, d][1])
+    failed = [src for (src, _), (proc, _) in jobs.items() if proc.wait() != 0]
+    if not failed:
+        for path, objs in objects.items():
+            tmp = path + f".tmp{os.getpid()}"
+            if subprocess.call(_link_command(nvcc, objs, tmp)) != 0:
+                failed.append(path)
+            else:
+                os.replace(tmp, path)
+    for _, obj in jobs.values():
+        if os.path.exists(obj):
+            os.remove(obj)
     if failed:
         raise RuntimeError(f"nvcc failed building {', '.join(failed)}")
     return LIB_PATH

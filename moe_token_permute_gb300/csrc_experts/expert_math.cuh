@@ -1,0 +1,106 @@
+// expert_math.cuh -- element types, activations and expert segments shared by
+// the expert operators' kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../csrc/common.cuh"
+#include "moe_experts.h"
+
+namespace moe {
+namespace experts {
+
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+template <>
+__device__ __forceinline__ __half from_f<__half>(float x) {
+  return __float2half_rn(x);
+}
+
+// 16 bytes of a row: 8 elements.
+template <typename T>
+union Vec8 {
+  uint4 v;
+  T e[8];
+};
+
+// 1 / (1 + exp(-z)); 0 and 1 at the infinities.  exp overflows to infinity
+// below z = -88, and the quotient is then 0.
+__device__ __forceinline__ float sigmoid(float z) { return __frcp_rn(1.0f + __expf(-z)); }
+
+constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+
+// 0.5 (1 + tanh(a)) = sigmoid(2a), so both smooth activations are z times one
+// sigmoid: an exponential and a reciprocal each.  Beyond |z| = 16 gelu's
+// sigmoid is 0 or 1 in fp32, so its polynomials take z cut to that range:
+// squares of larger z would overflow against the zero.
+__device__ __forceinline__ float gelu_cut(float z) { return fminf(fmaxf(z, -16.0f), 16.0f); }
+
+__device__ __forceinline__ float gelu_sigmoid(float zc) {
+  return sigmoid(2.0f * kGeluA * zc * (1.0f + kGeluB * zc * zc));
+}
+
+template <int kAct>
+__device__ __forceinline__ float act(float z) {
+  if (kAct == MOE_ACT_SILU) return z * sigmoid(z);
+  if (kAct == MOE_ACT_GELU) return z * gelu_sigmoid(gelu_cut(z));
+  if (kAct == MOE_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
+  return z;
+}
+
+// a = act(z), and its derivative.
+template <int kAct>
+__device__ __forceinline__ float act_grad(float z, float& a) {
+  if (kAct == MOE_ACT_SILU) {
+    const float p = sigmoid(z);
+    a = z * p;
+    return p + a * (1.0f - p);
+  }
+  if (kAct == MOE_ACT_GELU) {
+    const float zc = gelu_cut(z);
+    const float p = gelu_sigmoid(zc);
+    a = z * p;
+    return p + a * (1.0f - p) * (2.0f * kGeluA * (1.0f + 3.0f * kGeluB * zc * zc));
+  }
+  if (kAct == MOE_ACT_RELU) {
+    a = z > 0.0f ? z : (z != z ? z : 0.0f);
+    return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+  }
+  a = z;
+  return 1.0f;
+}
+
+// Rows of expert e, cut to [0, num_rows] whatever the offsets hold.
+struct Segment {
+  int lo, hi;
+};
+
+__device__ __forceinline__ Segment segment(const int64_t* offset, int e, int64_t num_rows,
+                                           bool* bad = nullptr) {
+  const int64_t a = __ldg(offset + e), b = __ldg(offset + e + 1);
+  const int64_t lo = a < 0 ? 0 : (a > num_rows ? num_rows : a);
+  const int64_t hi = b < lo ? lo : (b > num_rows ? num_rows : b);
+  if (bad != nullptr) *bad = lo != a || hi != b;
+  return {static_cast<int>(lo), static_cast<int>(hi)};
+}
+
+// Rows that belong to an expert at all.
+__device__ __forceinline__ int64_t rows_in_use(const int64_t* offset, int num_experts,
+                                               int64_t num_rows) {
+  const int64_t n = __ldg(offset + num_experts);
+  return n < 0 ? 0 : (n > num_rows ? num_rows : n);
+}
+
+}  // namespace experts
+}  // namespace moe

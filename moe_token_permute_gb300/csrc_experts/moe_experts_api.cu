@@ -1,0 +1,314 @@
+// moe_experts_api.cu -- host side of the C ABI declared in include/moe_experts.h.
+//
+// Argument checks happen before any device is touched; nothing allocates or
+// synchronises.  Each entry point is one launch, or for the backward passes
+// one launch per gradient.
+#include "moe_experts.h"
+
+#include <algorithm>
+
+#include "../csrc/common.cuh"
+#include "expert_grad.cuh"
+#include "expert_math.cuh"
+#include "expert_product.cuh"
+#include "host_util.cuh"
+#include "unpermute_grad.cuh"
+
+namespace moe {
+namespace experts {
+namespace {
+
+bool is_type(moe_dtype_t dt) { return dt == MOE_DTYPE_BF16 || dt == MOE_DTYPE_FP16; }
+bool is_act(moe_activation_t a) { return a >= MOE_ACT_NONE && a <= MOE_ACT_RELU; }
+
+// Sizes of a [E, N, K] weight and its rows.
+bool sizes_ok(int64_t num_rows, int64_t K, int64_t N, int32_t E) {
+  return num_rows >= 0 && num_rows <= INT32_MAX && K >= 8 && N >= 8 && K % 8 == 0 && N % 8 == 0 &&
+         K <= INT32_MAX / 2 && N <= INT32_MAX / 2 && E >= 1 && E <= MOE_MAX_LOCAL_EXPERTS;
+}
+
+bool base_ok(const void* p) { return p != nullptr && aligned(p, 16); }
+bool base_or_null(const void* p) { return p == nullptr || aligned(p, 16); }
+
+unsigned* status_of(void* workspace) {
+  return workspace == nullptr ? nullptr : &static_cast<WsHeader*>(workspace)->status;
+}
+
+template <typename T, int kUse, int kAct>
+cudaError_t launch_product(const ProductArgs& a, cudaStream_t s) {
+  const int64_t jn = kUse == kForward ? a.N : kUse == kGated ? a.N / 2 : a.K;
+  const int64_t tiles = kUse == kWeightGrad ? a.E * ceil_div(a.N, kTile)
+                                            : a.num_rows / kTile + std::min<int64_t>(a.E, a.num_rows);
+  const int64_t cols = ceil_div(jn, kTile);
+  if (tiles > INT32_MAX || cols > 65535) return cudaErrorInvalidConfiguration;
+  return launch(k_expert_product<T, kUse, kAct>,
+                dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(cols)), 256, 0, s, a);
+}
+
+template <typename T, int kUse>
+cudaError_t launch_forward(const ProductArgs& a, moe_activation_t act, cudaStream_t s) {
+  switch (act) {
+    case MOE_ACT_SILU: return launch_product<T, kUse, MOE_ACT_SILU>(a, s);
+    case MOE_ACT_GELU: return launch_product<T, kUse, MOE_ACT_GELU>(a, s);
+    case MOE_ACT_RELU: return launch_product<T, kUse, MOE_ACT_RELU>(a, s);
+    default: return launch_product<T, kUse, MOE_ACT_NONE>(a, s);
+  }
+}
+
+template <typename T, bool kGatedForm>
+cudaError_t launch_act_grad(const void* d_out, const void* z, void* dz, const int64_t* offset,
+                            int E, int64_t num_rows, int64_t W, moe_activation_t act, int sms,
+                            cudaStream_t s) {
+  auto kern = k_act_grad<T, kGatedForm, MOE_ACT_NONE>;
+  if (act == MOE_ACT_SILU) kern = k_act_grad<T, kGatedForm, MOE_ACT_SILU>;
+  if (act == MOE_ACT_GELU) kern = k_act_grad<T, kGatedForm, MOE_ACT_GELU>;
+  if (act == MOE_ACT_RELU) kern = k_act_grad<T, kGatedForm, MOE_ACT_RELU>;
+  const int64_t warps = num_rows * ceil_div(W / 8, 32);
+  const int64_t grid = std::min<int64_t>(ceil_div(warps, kGradWarps), 8 * static_cast<int64_t>(sms));
+  return launch(kern, dim3(static_cast<unsigned>(grid)), kGradThreads, 0, s,
+                static_cast<const T*>(d_out), static_cast<const T*>(z), static_cast<T*>(dz),
+                offset, E, num_rows, W);
+}
+
+template <typename T>
+cudaError_t launch_bias_grad(const void* dz, const int64_t* offset, int E, int64_t num_rows,
+                             int64_t N, void* d_bias, cudaStream_t s) {
+  return launch(k_bias_grad<T>, dim3(static_cast<unsigned>(ceil_div(N, 64)), E), kGradThreads, 0,
+                s, static_cast<const T*>(dz), offset, num_rows, N, static_cast<T*>(d_bias));
+}
+
+// d_rows and d_weight of z = x W^T from dz.
+template <typename T>
+cudaError_t product_gradients(const void* dz, const void* rows, const void* weight,
+                              const int64_t* offset, int64_t num_rows, int64_t K, int64_t N,
+                              int E, void* d_rows, void* d_weight, unsigned* status,
+                              cudaStream_t s) {
+  ProductArgs a = {};
+  a.offset = offset;
+  a.num_rows = num_rows;
+  a.K = K;
+  a.N = N;
+  a.E = E;
+  a.status = status;
+  if (d_rows != nullptr && num_rows > 0) {
+    a.x = dz;
+    a.w = weight;
+    a.out = d_rows;
+    const cudaError_t err = launch_product<T, kRowsGrad, MOE_ACT_NONE>(a, s);
+    if (err != cudaSuccess) return err;
+  }
+  if (d_weight != nullptr) {
+    a.x = rows;
+    a.w = dz;
+    a.out = d_weight;
+    return launch_product<T, kWeightGrad, MOE_ACT_NONE>(a, s);
+  }
+  return cudaSuccess;
+}
+
+template <typename VecT>
+cudaError_t launch_unpermute_backward(const void* d_out, const void* rows, int64_t num_rows,
+                                      int64_t H, const float* w, const int32_t* inv, int64_t T,
+                                      int K, void* d_rows, float* d_w, unsigned* status,
+                                      cudaStream_t s) {
+  constexpr int V = 4;
+  const int64_t vecs = H * 2 / static_cast<int64_t>(sizeof(VecT));
+  const int64_t warps = std::min<int64_t>(kCombineMaxWarps, ceil_div(vecs, 32));
+  return launch(k_unpermute_backward<VecT, V>, dim3(static_cast<unsigned>(T)),
+                static_cast<unsigned>(warps * 32), 0, s, static_cast<const VecT*>(d_out),
+                static_cast<const VecT*>(rows), num_rows, vecs, w, inv, K,
+                static_cast<VecT*>(d_rows), d_w, status);
+}
+
+int finish(cudaError_t err) {
+  if (err == cudaSuccess) return MOE_OK;
+  cudaGetLastError();
+  return MOE_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace experts
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::experts;
+
+extern "C" {
+
+int moe_expert_gated(const void* permuted_rows, const void* weight, moe_dtype_t dtype,
+                     const int64_t* expert_first_token_offset, int64_t num_rows,
+                     int64_t hidden_size, int64_t ffn_size, int32_t num_local_experts,
+                     moe_activation_t activation, void* out, void* preact, void* workspace,
+                     moe_stream_t stream) {
+  if (!is_type(dtype) || !is_act(activation) || ffn_size < 8 || ffn_size > INT32_MAX / 4 ||
+      ffn_size % 8 != 0 || !sizes_ok(num_rows, hidden_size, 2 * ffn_size, num_local_experts))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
+  if (num_rows == 0) return MOE_OK;
+  if (expert_first_token_offset == nullptr || !aligned(expert_first_token_offset, 8) ||
+      !base_ok(permuted_rows) || !base_ok(weight) || !base_ok(out) || !base_or_null(preact))
+    return MOE_ERR_INVALID_ARG;
+  if (supported_sm_count() == 0) return MOE_ERR_UNSUPPORTED_DEVICE;
+  ProductArgs a = {};
+  a.x = permuted_rows;
+  a.w = weight;
+  a.offset = expert_first_token_offset;
+  a.num_rows = num_rows;
+  a.K = hidden_size;
+  a.N = 2 * ffn_size;
+  a.E = num_local_experts;
+  a.out = out;
+  a.preact = preact;
+  a.status = status_of(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return finish(dtype == MOE_DTYPE_BF16 ? launch_forward<__nv_bfloat16, kGated>(a, activation, s)
+                                        : launch_forward<__half, kGated>(a, activation, s));
+}
+
+int moe_expert_gated_backward(const void* d_out, const void* permuted_rows, const void* weight,
+                              moe_dtype_t dtype, const int64_t* expert_first_token_offset,
+                              int64_t num_rows, int64_t hidden_size, int64_t ffn_size,
+                              int32_t num_local_experts, moe_activation_t activation,
+                              const void* preact, void* d_preact, void* d_rows, void* d_weight,
+                              void* workspace, moe_stream_t stream) {
+  if (!is_type(dtype) || !is_act(activation) || ffn_size < 8 || ffn_size > INT32_MAX / 4 ||
+      ffn_size % 8 != 0 || !sizes_ok(num_rows, hidden_size, 2 * ffn_size, num_local_experts))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
+  if (expert_first_token_offset == nullptr || !aligned(expert_first_token_offset, 8))
+    return MOE_ERR_INVALID_ARG;
+  if (!base_or_null(d_rows) || !base_or_null(d_weight)) return MOE_ERR_INVALID_ARG;
+  if (num_rows > 0) {
+    if (!base_ok(d_out) || !base_ok(preact) || !base_ok(d_preact)) return MOE_ERR_INVALID_ARG;
+    if (d_rows != nullptr && !base_ok(weight)) return MOE_ERR_INVALID_ARG;
+    if (d_weight != nullptr && !base_ok(permuted_rows)) return MOE_ERR_INVALID_ARG;
+  }
+  const int sms = supported_sm_count();
+  if (sms == 0) return MOE_ERR_UNSUPPORTED_DEVICE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf = dtype == MOE_DTYPE_BF16;
+  if (num_rows > 0) {
+    const cudaError_t err =
+        bf ? launch_act_grad<__nv_bfloat16, true>(d_out, preact, d_preact,
+                                                  expert_first_token_offset, num_local_experts,
+                                                  num_rows, ffn_size, activation, sms, s)
+           : launch_act_grad<__half, true>(d_out, preact, d_preact, expert_first_token_offset,
+                                           num_local_experts, num_rows, ffn_size, activation, sms, s);
+    if (err != cudaSuccess) return finish(err);
+  }
+  auto gradients = bf ? product_gradients<__nv_bfloat16> : product_gradients<__half>;
+  return finish(gradients(d_preact, permuted_rows, weight, expert_first_token_offset, num_rows,
+                          hidden_size, 2 * ffn_size, num_local_experts, d_rows, d_weight,
+                          status_of(workspace), s));
+}
+
+int moe_expert_linear(const void* rows, const void* weight, moe_dtype_t dtype,
+                      const int64_t* expert_first_token_offset, int64_t num_rows, int64_t in_size,
+                      int64_t out_size, int32_t num_local_experts, const void* bias,
+                      moe_activation_t activation, const void* residual, void* out, void* preact,
+                      void* workspace, moe_stream_t stream) {
+  if (!is_type(dtype) || !is_act(activation) ||
+      !sizes_ok(num_rows, in_size, out_size, num_local_experts))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
+  if (num_rows == 0) return MOE_OK;
+  if (expert_first_token_offset == nullptr || !aligned(expert_first_token_offset, 8) ||
+      !base_ok(rows) || !base_ok(weight) || !base_ok(out) || !base_or_null(bias) ||
+      !base_or_null(residual) || !base_or_null(preact))
+    return MOE_ERR_INVALID_ARG;
+  if (supported_sm_count() == 0) return MOE_ERR_UNSUPPORTED_DEVICE;
+  ProductArgs a = {};
+  a.x = rows;
+  a.w = weight;
+  a.offset = expert_first_token_offset;
+  a.num_rows = num_rows;
+  a.K = in_size;
+  a.N = out_size;
+  a.E = num_local_experts;
+  a.bias = bias;
+  a.residual = residual;
+  a.out = out;
+  a.preact = preact;
+  a.status = status_of(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return finish(dtype == MOE_DTYPE_BF16 ? launch_forward<__nv_bfloat16, kForward>(a, activation, s)
+                                        : launch_forward<__half, kForward>(a, activation, s));
+}
+
+int moe_expert_linear_backward(const void* d_out, const void* rows, const void* weight,
+                               moe_dtype_t dtype, const int64_t* expert_first_token_offset,
+                               int64_t num_rows, int64_t in_size, int64_t out_size,
+                               int32_t num_local_experts, moe_activation_t activation,
+                               const void* preact, void* d_preact, void* d_rows, void* d_weight,
+                               void* d_bias, void* workspace, moe_stream_t stream) {
+  if (!is_type(dtype) || !is_act(activation) ||
+      !sizes_ok(num_rows, in_size, out_size, num_local_experts))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
+  if (expert_first_token_offset == nullptr || !aligned(expert_first_token_offset, 8))
+    return MOE_ERR_INVALID_ARG;
+  if (!base_or_null(d_rows) || !base_or_null(d_weight) || !base_or_null(d_bias))
+    return MOE_ERR_INVALID_ARG;
+  const bool with_act = activation != MOE_ACT_NONE;
+  if (!with_act && (preact != nullptr || d_preact != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (num_rows > 0) {
+    if (!base_ok(d_out)) return MOE_ERR_INVALID_ARG;
+    if (with_act && (!base_ok(preact) || !base_ok(d_preact))) return MOE_ERR_INVALID_ARG;
+    if (d_rows != nullptr && !base_ok(weight)) return MOE_ERR_INVALID_ARG;
+    if (d_weight != nullptr && !base_ok(rows)) return MOE_ERR_INVALID_ARG;
+  }
+  const int sms = supported_sm_count();
+  if (sms == 0) return MOE_ERR_UNSUPPORTED_DEVICE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf = dtype == MOE_DTYPE_BF16;
+  const void* dz = d_out;
+  cudaError_t err = cudaSuccess;
+  if (with_act && num_rows > 0) {
+    auto grad = bf ? launch_act_grad<__nv_bfloat16, false> : launch_act_grad<__half, false>;
+    err = grad(d_out, preact, d_preact, expert_first_token_offset, num_local_experts, num_rows,
+               out_size, activation, sms, s);
+    dz = d_preact;
+  }
+  if (err == cudaSuccess && d_bias != nullptr) {
+    auto grad = bf ? launch_bias_grad<__nv_bfloat16> : launch_bias_grad<__half>;
+    err = grad(dz, expert_first_token_offset, num_local_experts, num_rows, out_size, d_bias, s);
+  }
+  if (err != cudaSuccess) return finish(err);
+  auto gradients = bf ? product_gradients<__nv_bfloat16> : product_gradients<__half>;
+  return finish(gradients(dz, rows, weight, expert_first_token_offset, num_rows, in_size, out_size,
+                          num_local_experts, d_rows, d_weight, status_of(workspace), s));
+}
+
+int moe_unpermute_backward(const void* d_out, const void* permuted_rows, int64_t num_rows,
+                           const float* topk_weights, const int32_t* inv_permuted_idx,
+                           int64_t num_tokens, int64_t hidden_size, int32_t topk, void* d_rows,
+                           float* d_topk_weights, void* workspace, moe_stream_t stream) {
+  const int64_t T = num_tokens, H = hidden_size;
+  if (T < 0 || H < 1 || topk < 1 || topk > MOE_MAX_TOPK || num_rows < 0) return MOE_ERR_INVALID_ARG;
+  if (T > INT32_MAX / topk || num_rows > INT32_MAX || H > INT64_MAX / 32)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (d_out == nullptr || topk_weights == nullptr || inv_permuted_idx == nullptr ||
+      !aligned(d_out, 2) || !aligned(permuted_rows, 2) || !aligned(topk_weights, 4) ||
+      !aligned(inv_permuted_idx, 4) || !aligned(d_rows, 2) || !aligned(d_topk_weights, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (num_rows > 0 && (permuted_rows == nullptr) != (d_topk_weights == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (d_rows == nullptr && d_topk_weights == nullptr) return MOE_ERR_INVALID_ARG;
+  if (supported_sm_count() == 0) return MOE_ERR_UNSUPPORTED_DEVICE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  unsigned* status = status_of(workspace);
+  size_t vb = 16;
+  while (vb > 2 && (H * 2 % static_cast<int64_t>(vb) != 0 || !aligned(d_out, vb) ||
+                    !aligned(permuted_rows, vb) || !aligned(d_rows, vb)))
+    vb /= 2;
+  auto run = vb == 16  ? launch_unpermute_backward<uint4>
+             : vb == 8 ? launch_unpermute_backward<uint2>
+             : vb == 4 ? launch_unpermute_backward<uint32_t>
+                       : launch_unpermute_backward<uint16_t>;
+  return finish(run(d_out, permuted_rows, num_rows, H, topk_weights, inv_permuted_idx, T, topk,
+                    d_rows, d_topk_weights, status, s));
+}
+
+}  // extern "C"
