@@ -6,6 +6,7 @@
 #include "moe_experts.h"
 
 #include <algorithm>
+#include <type_traits>
 
 #include "../csrc/common.cuh"
 #include "expert_grad.cuh"
@@ -34,25 +35,76 @@ unsigned* status_of(void* workspace) {
   return workspace == nullptr ? nullptr : &static_cast<WsHeader*>(workspace)->status;
 }
 
-template <typename T, int kUse, int kAct>
-cudaError_t launch_product(const ProductArgs& a, cudaStream_t s) {
-  const int64_t jn = kUse == kForward ? a.N : kUse == kGated ? a.N / 2 : a.K;
-  const int64_t tiles = kUse == kWeightGrad ? a.E * ceil_div(a.N, kTile)
-                                            : a.num_rows / kTile + std::min<int64_t>(a.E, a.num_rows);
-  const int64_t cols = ceil_div(jn, kTile);
-  if (tiles > INT32_MAX || cols > 65535) return cudaErrorInvalidConfiguration;
-  return launch(k_expert_product<T, kUse, kAct>,
-                dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(cols)), 256, 0, s, a);
+// cuTensorMapEncodeTiled, looked up once: the library is not linked against
+// the driver.
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
 }
 
+// A TMA map over [planes, rows, cols] (two dimensions with planes = 0), tiles
+// of box_rows rows by 64 columns: 128 bytes, in the 128-byte swizzle.  What a
+// tile reaches outside reads as zero.
+template <typename T>
+bool make_map(CUtensorMap* map, const void* base, int64_t planes, int64_t rows, int64_t cols,
+              int box_rows) {
+  const EncodeFn encode = encode_fn();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(planes)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2,
+                                 static_cast<cuuint64_t>(cols) * 2 * static_cast<cuuint64_t>(rows)};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  return encode(map, kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                planes > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// lhs: the weight, or dz for d_weight; rhs: the rows, or dz for d_rows.
 template <typename T, int kUse>
-cudaError_t launch_forward(const ProductArgs& a, moe_activation_t act, cudaStream_t s) {
-  switch (act) {
-    case MOE_ACT_SILU: return launch_product<T, kUse, MOE_ACT_SILU>(a, s);
-    case MOE_ACT_GELU: return launch_product<T, kUse, MOE_ACT_GELU>(a, s);
-    case MOE_ACT_RELU: return launch_product<T, kUse, MOE_ACT_RELU>(a, s);
-    default: return launch_product<T, kUse, MOE_ACT_NONE>(a, s);
+cudaError_t launch_product(const ProductArgs& a, const void* lhs, const void* rhs, int sms,
+                           cudaStream_t s) {
+  CUtensorMap map_a, map_b;
+  bool ok;
+  if (kUse == kWeightGrad) {
+    // Without rows the products are empty and the maps are never used.
+    const int64_t rows = std::max<int64_t>(1, a.num_rows);
+    const void* any = a.out;
+    ok = make_map<T>(&map_a, lhs != nullptr ? lhs : any, 0, rows, a.N, kSlice) &&
+         make_map<T>(&map_b, rhs != nullptr ? rhs : any, 0, rows, a.K, kSlice);
+  } else {
+    ok = make_map<T>(&map_a, lhs, a.E, a.N, a.K, kUse == kRowsGrad ? kSlice : 128) &&
+         make_map<T>(&map_b, rhs, 0, a.num_rows, kUse == kRowsGrad ? a.N : a.K, kBoxRows);
   }
+  if (!ok) return cudaErrorInvalidValue;
+  const int64_t m = kUse == kForward || kUse == kWeightGrad ? a.N : kUse == kGated ? a.N / 2 : a.K;
+  const int64_t m_blocks = ceil_div(m, kUse == kGated ? 128 : 256);
+  const int64_t tiles =
+      m_blocks * (kUse == kWeightGrad ? a.E * ceil_div(a.K, kMaxN)
+                                      : a.num_rows / kMaxN + std::min<int64_t>(a.E, a.num_rows));
+  if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
+  return launch(k_expert_product<T, kUse>,
+                dim3(static_cast<unsigned>(std::min<int64_t>(tiles, sms))), kProductThreads,
+                product_smem(a.E), s, map_a, map_b, a);
 }
 
 template <typename T, bool kGatedForm>
@@ -81,7 +133,7 @@ cudaError_t launch_bias_grad(const void* dz, const int64_t* offset, int E, int64
 template <typename T>
 cudaError_t product_gradients(const void* dz, const void* rows, const void* weight,
                               const int64_t* offset, int64_t num_rows, int64_t K, int64_t N,
-                              int E, void* d_rows, void* d_weight, unsigned* status,
+                              int E, void* d_rows, void* d_weight, unsigned* status, int sms,
                               cudaStream_t s) {
   ProductArgs a = {};
   a.offset = offset;
@@ -91,17 +143,13 @@ cudaError_t product_gradients(const void* dz, const void* rows, const void* weig
   a.E = E;
   a.status = status;
   if (d_rows != nullptr && num_rows > 0) {
-    a.x = dz;
-    a.w = weight;
     a.out = d_rows;
-    const cudaError_t err = launch_product<T, kRowsGrad, MOE_ACT_NONE>(a, s);
+    const cudaError_t err = launch_product<T, kRowsGrad>(a, weight, dz, sms, s);
     if (err != cudaSuccess) return err;
   }
   if (d_weight != nullptr) {
-    a.x = rows;
-    a.w = dz;
     a.out = d_weight;
-    return launch_product<T, kWeightGrad, MOE_ACT_NONE>(a, s);
+    return launch_product<T, kWeightGrad>(a, dz, rows, sms, s);
   }
   return cudaSuccess;
 }
@@ -148,21 +196,21 @@ int moe_expert_gated(const void* permuted_rows, const void* weight, moe_dtype_t 
   if (expert_first_token_offset == nullptr || !aligned(expert_first_token_offset, 8) ||
       !base_ok(permuted_rows) || !base_ok(weight) || !base_ok(out) || !base_or_null(preact))
     return MOE_ERR_INVALID_ARG;
-  if (supported_sm_count() == 0) return MOE_ERR_UNSUPPORTED_DEVICE;
+  const int sms = supported_sm_count();
+  if (sms == 0) return MOE_ERR_UNSUPPORTED_DEVICE;
   ProductArgs a = {};
-  a.x = permuted_rows;
-  a.w = weight;
   a.offset = expert_first_token_offset;
   a.num_rows = num_rows;
   a.K = hidden_size;
   a.N = 2 * ffn_size;
   a.E = num_local_experts;
+  a.act = activation;
   a.out = out;
   a.preact = preact;
   a.status = status_of(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return finish(dtype == MOE_DTYPE_BF16 ? launch_forward<__nv_bfloat16, kGated>(a, activation, s)
-                                        : launch_forward<__half, kGated>(a, activation, s));
+  return finish(dtype == MOE_DTYPE_BF16 ? launch_product<__nv_bfloat16, kGated>(a, weight, permuted_rows, sms, s)
+                                        : launch_product<__half, kGated>(a, weight, permuted_rows, sms, s));
 }
 
 int moe_expert_gated_backward(const void* d_out, const void* permuted_rows, const void* weight,
@@ -199,7 +247,7 @@ int moe_expert_gated_backward(const void* d_out, const void* permuted_rows, cons
   auto gradients = bf ? product_gradients<__nv_bfloat16> : product_gradients<__half>;
   return finish(gradients(d_preact, permuted_rows, weight, expert_first_token_offset, num_rows,
                           hidden_size, 2 * ffn_size, num_local_experts, d_rows, d_weight,
-                          status_of(workspace), s));
+                          status_of(workspace), sms, s));
 }
 
 int moe_expert_linear(const void* rows, const void* weight, moe_dtype_t dtype,
@@ -216,23 +264,23 @@ int moe_expert_linear(const void* rows, const void* weight, moe_dtype_t dtype,
       !base_ok(rows) || !base_ok(weight) || !base_ok(out) || !base_or_null(bias) ||
       !base_or_null(residual) || !base_or_null(preact))
     return MOE_ERR_INVALID_ARG;
-  if (supported_sm_count() == 0) return MOE_ERR_UNSUPPORTED_DEVICE;
+  const int sms = supported_sm_count();
+  if (sms == 0) return MOE_ERR_UNSUPPORTED_DEVICE;
   ProductArgs a = {};
-  a.x = rows;
-  a.w = weight;
   a.offset = expert_first_token_offset;
   a.num_rows = num_rows;
   a.K = in_size;
   a.N = out_size;
   a.E = num_local_experts;
+  a.act = activation;
   a.bias = bias;
   a.residual = residual;
   a.out = out;
   a.preact = preact;
   a.status = status_of(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return finish(dtype == MOE_DTYPE_BF16 ? launch_forward<__nv_bfloat16, kForward>(a, activation, s)
-                                        : launch_forward<__half, kForward>(a, activation, s));
+  return finish(dtype == MOE_DTYPE_BF16 ? launch_product<__nv_bfloat16, kForward>(a, weight, rows, sms, s)
+                                        : launch_product<__half, kForward>(a, weight, rows, sms, s));
 }
 
 int moe_expert_linear_backward(const void* d_out, const void* rows, const void* weight,
@@ -276,7 +324,7 @@ int moe_expert_linear_backward(const void* d_out, const void* rows, const void* 
   if (err != cudaSuccess) return finish(err);
   auto gradients = bf ? product_gradients<__nv_bfloat16> : product_gradients<__half>;
   return finish(gradients(dz, rows, weight, expert_first_token_offset, num_rows, in_size, out_size,
-                          num_local_experts, d_rows, d_weight, status_of(workspace), s));
+                          num_local_experts, d_rows, d_weight, status_of(workspace), sms, s));
 }
 
 int moe_unpermute_backward(const void* d_out, const void* permuted_rows, int64_t num_rows,
