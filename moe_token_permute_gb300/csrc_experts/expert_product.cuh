@@ -8,13 +8,19 @@
 // which goes in steps of 16: a segment costs its own rows rounded up to 16,
 // not to 128, and a single row costs one 16-column product.
 //
-// A block computes 256 x (up to 256) outputs: two A tiles of 128 rows (forward
-// gated: the gate rows and the up rows of the same 128 features, so that the
-// activation and the product happen in registers; else 256 consecutive ones)
-// against one B tile, accumulated in all 512 columns of tensor memory.
+// A pair of blocks (two SMs, cta_group::2) computes 512 x (up to 256) outputs:
+// four A tiles of 128 rows, two in each block, against one B tile of which each
+// block holds half the columns.  Gated: a block's two A tiles are the gate and
+// the up rows of the same 128 features, so that the activation and the product
+// happen in registers; else the pair's tiles are consecutive.  The accumulators
+// take all 512 columns of tensor memory, or, up to 128 columns wide, half of
+// them, and then the epilogue of one tile overlaps the products of the next.
 //   warps 0-7  epilogue: tensor memory -> registers -> shared -> rows
-//   warp 8     TMA producer: 64-deep slices into kStages stages of 64 KB
-//   warp 9     tcgen05.mma issue, and tensor memory allocation
+//   warp 8     TMA producer: 64-deep slices into kStages stages of 48 KB
+//   warp 9     tcgen05.mma issue (first block), tensor memory allocation
+// The pair shape is what shared memory and L2 bandwidth ask for: a 64-deep
+// slice feeds 1024 cycles of products with 48 KB per SM, where a single block's
+// 256 x 256 tile reads 64 KB, and its operands a third more of shared memory.
 // The grid is persistent; tiles are numbered expert by expert, the row blocks
 // of one weight tile next to each other so that they share it in L2.
 #pragma once
@@ -29,9 +35,9 @@ enum Use { kForward, kGated, kRowsGrad, kWeightGrad };
 
 constexpr int kMaxN = 256;     // columns of one accumulator
 constexpr int kSlice = 64;     // contraction depth of one stage: 128 bytes
-constexpr int kStages = 3;
+constexpr int kStages = 4;
 constexpr int kTileABytes = 128 * kSlice * 2;
-constexpr int kTileBBytes = kMaxN * kSlice * 2;
+constexpr int kTileBBytes = kMaxN / 2 * kSlice * 2;
 constexpr int kStageBytes = 2 * kTileABytes + kTileBBytes;
 constexpr int kBoxRows = 32;   // rows of one TMA box of a k-contiguous B
 constexpr int kEpiWarps = 8;
@@ -54,10 +60,15 @@ struct ProductArgs {
   unsigned* status;
 };
 
-// Dynamic shared memory: stages (1024-byte aligned), staging, tile numbers.
+// Dynamic shared memory: stages (1024-byte aligned), staging, then each
+// expert's rows and its first tile.
 inline size_t product_smem(int E) {
-  return 1024 + kStages * kStageBytes + kStagingBytes + static_cast<size_t>(E + 1) * 4;
+  return 1024 + kStages * kStageBytes + kStagingBytes + static_cast<size_t>(E) * 12 + 4;
 }
+
+static_assert(1024 + kStages * kStageBytes + kStagingBytes + MOE_MAX_LOCAL_EXPERTS * 12 + 4 + 1024 <=
+                  227 * 1024,
+              "shared memory of one block");
 
 struct Tile {
   int e, lo, rows;  // expert; first row and row count (d_weight: all of e's rows)
@@ -70,33 +81,33 @@ __device__ __forceinline__ int block_rows(int rows, int blocks) {
   return ((rows + blocks - 1) / blocks + 15) / 16 * 16;
 }
 
-// Output features of one tile.
+// Output features of one tile of the pair.
 template <int kUse>
-__device__ __forceinline__ int m_step() { return kUse == kGated ? 128 : 256; }
+__host__ __device__ constexpr int m_step() { return kUse == kGated ? 256 : 512; }
 
 template <int kUse>
-__device__ __forceinline__ Tile find_tile(const ProductArgs& a, const int* first, int t,
+__device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const int* first, int t,
                                           int m_blocks, int n_blocks) {
   Tile r;
   if (kUse == kWeightGrad) {
     const int per = m_blocks * n_blocks;
     r.e = t / per;
     const int local = t - r.e * per;
-    const Segment s = segment(a.offset, r.e, a.num_rows);
+    const Segment s = segments[r.e];
     r.lo = s.lo;
     r.rows = s.hi - s.lo;
     r.m0 = local / n_blocks * m_step<kUse>();
     r.n0 = local % n_blocks * kMaxN;
     return r;
   }
-  int lo = 0, hi = a.E;  // first[lo] <= t < first[hi]
+  int lo = 0, hi = E;  // first[lo] <= t < first[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (first[mid] <= t) lo = mid;
     else hi = mid;
   }
   r.e = lo;
-  const Segment s = segment(a.offset, lo, a.num_rows);
+  const Segment s = segments[lo];
   const int rows = s.hi - s.lo;
   const int blocks = row_blocks(rows), step = block_rows(rows, blocks);
   const int local = t - first[lo];
@@ -179,30 +190,40 @@ __device__ __forceinline__ void write_block(const float (&v)[32], float* stage, 
 // map_a, map_b: the operands as TMA tiles of 64 contiguous values (128 bytes,
 // 128-byte swizzle) by 128 (forward A), 64 (MN-major) or kBoxRows rows.
 template <typename T, int kUse>
-__global__ void __launch_bounds__(kProductThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 k_expert_product(const __grid_constant__ CUtensorMap map_a,
                  const __grid_constant__ CUtensorMap map_b, const ProductArgs a) {
   constexpr bool kBf16 = sizeof(T) == 2 && !__is_same(T, __half);
   constexpr bool kAMn = kUse == kRowsGrad || kUse == kWeightGrad;
   constexpr bool kBMn = kUse == kWeightGrad;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_done, s_free;
+  // s_full, s_free and s_peer are used in the pair's first block only, s_tail in
+  // its second.
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_done[2], s_free[2],
+      s_peer[kStages], s_tail[kStages];
   __shared__ uint32_t s_tmem;
   __shared__ int s_gave_up, s_scan[32];
 
   uint8_t* stages = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float* staging = reinterpret_cast<float*>(stages + kStages * kStageBytes);
-  int* first = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(staging) + kStagingBytes);
+  Segment* segments = reinterpret_cast<Segment*>(reinterpret_cast<uint8_t*>(staging) + kStagingBytes);
+  int* first = reinterpret_cast<int*>(segments + a.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_addr(&s_full[i]), 1);
       mbar_init(smem_addr(&s_empty[i]), 1);
+      mbar_init(smem_addr(&s_peer[i]), 1);
+      mbar_init(smem_addr(&s_tail[i]), 1);
     }
-    mbar_init(smem_addr(&s_done), 1);
-    mbar_init(smem_addr(&s_free), kEpiWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&s_done[i]), 1);
+      mbar_init(smem_addr(&s_free[i]), 2 * kEpiWarps);
+    }
     mbar_init_fence();
     s_gave_up = 0;
     tma_prefetch_map(&map_a);
@@ -226,6 +247,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       bool b;
       const Segment s = segment(a.offset, e, a.num_rows, &b);
       bad |= b;
+      segments[e] = s;
       n = row_blocks(s.hi - s.lo) * m_blocks;
     }
     int part;
@@ -239,6 +261,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     atomicOr(a.status, MOE_FLAG_OFFSET_OUT_OF_RANGE);
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // both blocks' barriers exist before either's loads or arrivals
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* gave_up = &s_gave_up;
@@ -248,36 +271,71 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   auto slices = [&](const Tile& t) {
     return ((kUse == kWeightGrad ? t.rows : k_size) + kSlice - 1) / kSlice;
   };
-  // Columns of the tile, and whether its second A tile holds anything.
+  // Columns of the tile, those of the product (each block holds half of B), and
+  // whether the second A tiles hold anything.
   auto columns = [&](const Tile& t) {
     return kUse == kWeightGrad ? min(kMaxN, static_cast<int>(a.K) - t.n0) : t.rows;
   };
-  auto two = [&](const Tile& t) { return kUse == kGated || t.m0 + 128 < m_size; };
+  auto mma_n = [](int cols) { return (cols + 15) / 16 * 16; };
+  auto two = [&](const Tile& t) { return kUse == kGated || t.m0 + 256 < m_size; };
+  // First feature of the block's i-th A tile.
+  auto feature = [&](const Tile& t, int i) {
+    return t.m0 + rank * 128 + (kUse == kGated ? i * F : i * 256);
+  };
+  // Whether slice s of a d_weight tile runs past the expert's rows.
+  auto is_tail = [&](const Tile& t, int s) {
+    return kUse == kWeightGrad && t.rows - s * kSlice < kSlice;
+  };
+  // A slice that runs past the expert's rows: what follows belongs to another
+  // expert or to none and may be infinite or NaN, so it is overwritten in both
+  // operands rather than multiplied by zeros.
+  auto clear_tail = [&](int st, int left) {
+    const int rows = (left + 15) / 16 * 16 - left;
+    for (int i = lane; i < rows * 48; i += 32) {
+      const int box = i / 8 % 6, r = left + i / 48;
+      *reinterpret_cast<uint4*>(stages + st * kStageBytes + box * (kTileABytes / 2) + r * 128 +
+                                (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_async_shared();
+    __syncwarp();
+  };
+  // Tensor memory of a tile: a wide one takes all of it, narrow ones take
+  // turns with its halves.
+  auto narrow = [](int cols) { return cols <= kMaxN / 2; };
 
   if (warp == kEpiWarps) {
-    if (lane == 0) {
-      uint32_t step = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        const Tile tile = find_tile<kUse>(a, first, t, m_blocks, n_blocks);
-        const int n_slices = slices(tile), cols = columns(tile);
-        const int a_tiles = two(tile) ? 2 : 1;
-        const int b_boxes = kBMn ? (cols + 63) / 64 : (cols + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = a_tiles * kTileABytes +
-                               b_boxes * (kBMn ? 64 * kSlice * 2 : kBoxRows * kSlice * 2);
-        for (int s = 0; s < n_slices; ++s, ++step) {
-          const int st = step % kStages;
-          const uint32_t full = smem_addr(&s_full[st]);
-          if (!mbar_wait(smem_addr(&s_empty[st]), (step / kStages & 1) ^ 1, gave_up)) {
-            ok = false;
-            break;
+    uint32_t step = 0;
+    bool ok = true;
+    for (int t = pair; t < total && ok; t += pairs) {
+      const Tile tile = find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks);
+      const int n_slices = slices(tile), half_n = mma_n(columns(tile)) / 2;
+      const int a_tiles = two(tile) ? 2 : 1;
+      const int b_boxes = kBMn ? (half_n + 63) / 64 : (half_n + kBoxRows - 1) / kBoxRows;
+      const uint32_t bytes = a_tiles * kTileABytes +
+                             b_boxes * (kBMn ? 64 * kSlice * 2 : kBoxRows * kSlice * 2);
+      for (int s = 0; s < n_slices; ++s, ++step) {
+        const int st = step % kStages;
+        if (!warp_wait(smem_addr(&s_empty[st]), (step / kStages & 1) ^ 1, gave_up)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          // Both blocks' loads report to the first block's barrier; a tail
+          // slice of the second block to its own, as it is cleared there.
+          uint32_t full = smem_addr(&s_full[st]);
+          if (is_tail(tile, s)) {
+            if (rank != 0) full = smem_addr(&s_tail[st]);
+            mbar_expect(full, bytes);
+          } else if (rank == 0) {
+            mbar_expect(full, 2 * bytes);
+          } else {
+            full = cluster_addr(full, 0);
           }
-          mbar_expect(full, bytes);
           const uint32_t sa = smem_addr(stages + st * kStageBytes);
           const uint32_t sb = sa + 2 * kTileABytes;
           const int k = s * kSlice;
           for (int i = 0; i < a_tiles; ++i) {
-            const int m = tile.m0 + (kUse == kGated ? i * F : i * 128);
+            const int m = feature(tile, i);
             const uint32_t dst = sa + i * kTileABytes;
             if (kUse == kForward || kUse == kGated) {
               tma_load_3d(dst, &map_a, k, m, tile.e, full);
@@ -291,38 +349,46 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           }
           for (int i = 0; i < b_boxes; ++i) {
             if (kBMn)
-              tma_load_2d(sb + i * 64 * kSlice * 2, &map_b, tile.n0 + i * 64, tile.lo + k, full);
+              tma_load_2d(sb + i * 64 * kSlice * 2, &map_b, tile.n0 + rank * half_n + i * 64,
+                          tile.lo + k, full);
             else
-              tma_load_2d(sb + i * kBoxRows * kSlice * 2, &map_b, k, tile.lo + i * kBoxRows, full);
+              tma_load_2d(sb + i * kBoxRows * kSlice * 2, &map_b, k,
+                          tile.lo + rank * half_n + i * kBoxRows, full);
           }
         }
+        __syncwarp();
       }
-      // Nothing of this block may still be in flight when it ends.  After an
-      // ordinary run the MMA warp has seen every load; after a wait gave up,
-      // the loads are given the time of one wait to land.
-      if (*gave_up != 0) {
-        const unsigned long long t0 = now_ns();
-        for (int i = 0; i < kStages && step > 0; ++i) {
-          const uint32_t last = step - 1 - i;  // the newest load of its stage
-          if (static_cast<int>(last) < 0) break;
-          while (!mbar_try(smem_addr(&s_full[last % kStages]), last / kStages & 1) &&
-                 now_ns() - t0 < kWaitNs) {
-          }
+    }
+    // Nothing of this block may still be in flight when it ends.  After an
+    // ordinary run every load was seen; after a wait gave up, the loads are
+    // given the time of one wait to be used.
+    if (*gave_up != 0 && lane == 0) {
+      const unsigned long long t0 = now_ns();
+      for (uint32_t i = 1; i <= kStages && i <= step; ++i) {
+        const uint32_t last = step - i;  // the newest load of its stage
+        while (!mbar_try(smem_addr(&s_empty[last % kStages]), last / kStages & 1) &&
+               now_ns() - t0 < kWaitNs) {
         }
       }
     }
     __syncwarp();
-  } else if (warp == kEpiWarps + 1) {
-    uint32_t step = 0, done = 0;
+  } else if (warp == kEpiWarps + 1 && rank == 0) {
+    uint32_t step = 0, used[2] = {0, 0};
+    uint32_t tails = 0;  // bit st: parity of the stage's tail slices so far
+    int next = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const Tile tile = find_tile<kUse>(a, first, t, m_blocks, n_blocks);
+    for (int t = pair; t < total && ok; t += pairs) {
+      const Tile tile = find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks);
       const int n_slices = slices(tile);
       if (n_slices == 0) continue;
-      const int n = (columns(tile) + 15) / 16 * 16;
-      const bool both = two(tile);
-      const uint32_t idesc = instr_desc(kBf16, kAMn, kBMn, 128, n);
-      if (!warp_wait(smem_addr(&s_free), (done & 1) ^ 1, gave_up)) break;
+      const int cols = columns(tile), n = mma_n(cols);
+      const bool both = two(tile), half = narrow(cols);
+      const uint32_t idesc = instr_desc(kBf16, kAMn, kBMn, 256, n);
+      const int buf = half ? next : 0;
+      next = half ? next ^ 1 : 0;
+      const uint32_t acc0 = tmem + buf * kMaxN, acc1 = acc0 + (half ? kMaxN / 2 : kMaxN);
+      if (!warp_wait(smem_addr(&s_free[buf]), (used[buf]++ & 1) ^ 1, gave_up)) break;
+      if (!half && !warp_wait(smem_addr(&s_free[1]), (used[1]++ & 1) ^ 1, gave_up)) break;
       tc_fence_after();
       for (int s = 0; s < n_slices; ++s, ++step) {
         const int st = step % kStages;
@@ -330,81 +396,94 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           ok = false;
           break;
         }
-        uint8_t* sa = stages + st * kStageBytes;
-        uint8_t* sb = sa + 2 * kTileABytes;
-        int depth = 4;  // products of 16 k-values each
-        if (kUse == kWeightGrad) {
+        const uint32_t pa = smem_addr(stages + st * kStageBytes);
+        const uint32_t pb = pa + 2 * kTileABytes;
+        int depth = kSlice / 16;
+        if (is_tail(tile, s)) {
           const int left = tile.rows - s * kSlice;
-          if (left < kSlice) {
-            // The slice runs past the expert's rows.  What follows belongs to
-            // another expert or to none and may be infinite or NaN, so it is
-            // overwritten in both operands rather than multiplied by zeros.
-            depth = (left + 15) / 16;
-            const int rows = depth * 16 - left;
-            for (int i = lane; i < rows * 64; i += 32) {
-              const int box = i / 8 & 7, r = left + i / 64;
-              uint8_t* at = box < 4 ? sa + box * (kTileABytes / 2)
-                                    : sb + (box - 4) * (kTileBBytes / 4);
-              *reinterpret_cast<uint4*>(at + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_async_shared();
-            __syncwarp();
+          depth = (left + 15) / 16;
+          clear_tail(st, left);
+          if (!warp_wait(smem_addr(&s_peer[st]), tails >> st & 1, gave_up)) {
+            ok = false;
+            break;
           }
+          tails ^= 1u << st;
         }
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           constexpr uint32_t kStepA = kAMn ? 2048 : 32, kStepB = kBMn ? 2048 : 32;
-          const uint32_t pa = smem_addr(sa), pb = smem_addr(sb);
           for (int i = 0; i < depth; ++i) {
             const uint64_t db = smem_desc(pb + i * kStepB, kBMn ? 8192 : 16, 1024);
             const bool acc = s > 0 || i > 0;
-            tc_mma(tmem, smem_desc(pa + i * kStepA, kAMn ? 8192 : 16, 1024), db, idesc, acc);
+            tc_mma(acc0, smem_desc(pa + i * kStepA, kAMn ? 8192 : 16, 1024), db, idesc, acc);
             if (both)
-              tc_mma(tmem + kMaxN,
-                     smem_desc(pa + kTileABytes + i * kStepA, kAMn ? 8192 : 16, 1024), db, idesc,
-                     acc);
+              tc_mma(acc1, smem_desc(pa + kTileABytes + i * kStepA, kAMn ? 8192 : 16, 1024), db,
+                     idesc, acc);
           }
           tc_commit(smem_addr(&s_empty[st]));
-          if (s == n_slices - 1) tc_commit(smem_addr(&s_done));
+          if (s == n_slices - 1) tc_commit(smem_addr(&s_done[buf]));
         }
         __syncwarp();
       }
-      ++done;
     }
     // The products are over before the memory they read and write is given up.
     if (*gave_up != 0 && lane == 0) {
       const unsigned long long t0 = now_ns();
-      for (int i = 0; i < kStages; ++i) {
-        const uint32_t last = step - 1 - i;
-        if (static_cast<int>(last) < 0) break;
+      for (uint32_t i = 1; i <= kStages && i <= step; ++i) {
+        const uint32_t last = step - i;
         while (!mbar_try(smem_addr(&s_empty[last % kStages]), last / kStages & 1) &&
                now_ns() - t0 < kWaitNs) {
         }
       }
     }
     __syncwarp();
-  } else {
-    const int quad = warp & 3, half = warp >> 2;
+  } else if (warp == kEpiWarps + 1) {
+    if (kUse == kWeightGrad) {
+      // The second block's tail slices: clear, then tell the first block.
+      uint32_t step = 0, tails = 0;
+      for (int t = pair; t < total; t += pairs) {
+        const Tile tile = find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks);
+        const int n_slices = slices(tile);
+        if (n_slices > 0 && is_tail(tile, n_slices - 1)) {
+          const int st = (step + n_slices - 1) % kStages;
+          if (!warp_wait(smem_addr(&s_tail[st]), tails >> st & 1, gave_up)) break;
+          tails ^= 1u << st;
+          clear_tail(st, tile.rows - (n_slices - 1) * kSlice);
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&s_peer[st]), 0));
+        }
+        step += n_slices;
+      }
+      __syncwarp();
+    }
+  } else if (warp < kEpiWarps) {
+    const int quad = warp & 3;
     float* stage = staging + warp * kStageFloats;
     T* out = static_cast<T*>(a.out);
     T* preact = static_cast<T*>(a.preact);
     const T* residual = static_cast<const T*>(a.residual);
-    uint32_t done = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
-      const Tile tile = find_tile<kUse>(a, first, t, m_blocks, n_blocks);
+    uint32_t fin[2] = {0, 0};
+    int next = 0;
+    const uint32_t free0 = cluster_addr(smem_addr(&s_free[0]), 0);
+    const uint32_t free1 = cluster_addr(smem_addr(&s_free[1]), 0);
+    for (int t = pair; t < total; t += pairs) {
+      const Tile tile = find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks);
       const int cols = columns(tile);
-      const bool any = slices(tile) > 0;
+      const bool any = slices(tile) > 0, half = narrow(cols);
+      int buf = 0;
       if (any) {
-        if (!warp_wait(smem_addr(&s_done), done & 1, gave_up)) break;
+        buf = half ? next : 0;
+        next = half ? next ^ 1 : 0;
+        if (!warp_wait(smem_addr(&s_done[buf]), fin[buf]++ & 1, gave_up)) break;
         tc_fence_after();
       }
-      const uint32_t base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-      for (int c = half * 32; c < cols; c += 64) {
-        const int64_t m = tile.m0 + quad * 32;  // the warp's first feature
+      const uint32_t acc0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kMaxN;
+      const uint32_t acc1 = acc0 + (half ? kMaxN / 2 : kMaxN);
+      for (int c = warp / 4 * 32; c < cols; c += 64) {
         if (kUse == kGated) {
+          const int64_t m = tile.m0 + rank * 128 + quad * 32;  // the warp's first feature
           float g[32], u[32];
-          tmem_load32(base + c, g);
-          tmem_load32(base + kMaxN + c, u);
+          tmem_load32(acc0 + c, g);
+          tmem_load32(acc1 + c, u);
           tmem_wait_load(g);
           tmem_wait_load(u);
           if (preact != nullptr) {
@@ -418,33 +497,33 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
         } else {
           const int parts = two(tile) ? 2 : 1;
           for (int i = 0; i < parts; ++i) {
-            const int64_t mi = m + i * 128;
+            const int64_t m = feature(tile, i) + quad * 32;
             float z[32];
             if (any) {
-              tmem_load32(base + i * kMaxN + c, z);
+              tmem_load32((i == 0 ? acc0 : acc1) + c, z);
               tmem_wait_load(z);
             } else {
 #pragma unroll
               for (int j = 0; j < 32; ++j) z[j] = 0.f;
             }
             if (kUse == kForward) {
-              if (a.bias != nullptr && mi + lane < a.N) {
+              if (a.bias != nullptr && m + lane < a.N) {
                 const float bias = to_f(static_cast<const T*>(
-                    a.bias)[static_cast<int64_t>(tile.e) * a.N + mi + lane]);
+                    a.bias)[static_cast<int64_t>(tile.e) * a.N + m + lane]);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) z[j] += bias;
               }
               if (preact != nullptr)
-                write_block<T, true>(z, stage, preact, nullptr, a.N, tile.lo + c, cols - c, mi,
+                write_block<T, true>(z, stage, preact, nullptr, a.N, tile.lo + c, cols - c, m,
                                      a.N);
               apply_act(a.act, z);
-              write_block<T, true>(z, stage, out, residual, a.N, tile.lo + c, cols - c, mi, a.N);
+              write_block<T, true>(z, stage, out, residual, a.N, tile.lo + c, cols - c, m, a.N);
             } else if (kUse == kRowsGrad) {
-              write_block<T, true>(z, stage, out, nullptr, a.K, tile.lo + c, cols - c, mi, a.K);
+              write_block<T, true>(z, stage, out, nullptr, a.K, tile.lo + c, cols - c, m, a.K);
             } else {
-              const int64_t left = a.N - mi;
+              const int64_t left = a.N - m;
               write_block<T, false>(z, stage, out, nullptr, a.K,
-                                    static_cast<int64_t>(tile.e) * a.N + mi,
+                                    static_cast<int64_t>(tile.e) * a.N + m,
                                     static_cast<int>(left < 32 ? (left < 0 ? 0 : left) : 32),
                                     tile.n0 + c, a.K);
             }
@@ -454,13 +533,16 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       if (any) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&s_free));
-        ++done;
+        if (lane == 0) {
+          mbar_arrive_cluster(buf == 0 ? free0 : free1);
+          if (!half) mbar_arrive_cluster(free1);
+        }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // the pair's products, loads and arrivals are over in both blocks
   tc_fence_after();
   if (threadIdx.x == 0 && *gave_up != 0 && a.status != nullptr)
     atomicOr(a.status, MOE_FLAG_BARRIER_TIMEOUT);

@@ -97,13 +97,13 @@ cudaError_t launch_product(const ProductArgs& a, const void* lhs, const void* rh
   }
   if (!ok) return cudaErrorInvalidValue;
   const int64_t m = kUse == kForward || kUse == kWeightGrad ? a.N : kUse == kGated ? a.N / 2 : a.K;
-  const int64_t m_blocks = ceil_div(m, kUse == kGated ? 128 : 256);
+  const int64_t m_blocks = ceil_div(m, m_step<kUse>());
   const int64_t tiles =
       m_blocks * (kUse == kWeightGrad ? a.E * ceil_div(a.K, kMaxN)
                                       : a.num_rows / kMaxN + std::min<int64_t>(a.E, a.num_rows));
   if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
   return launch(k_expert_product<T, kUse>,
-                dim3(static_cast<unsigned>(std::min<int64_t>(tiles, sms))), kProductThreads,
+                dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, sms / 2))), kProductThreads,
                 product_smem(a.E), s, map_a, map_b, a);
 }
 
