@@ -18,6 +18,7 @@
 //   warps 0-7  epilogue: tensor memory -> registers -> shared -> rows
 //   warp 8     TMA producer: 64-deep slices into kStages stages of 48 KB
 //   warp 9     tcgen05.mma issue (first block), tensor memory allocation
+//   warp 10    d_weight: clears what a slice holds beyond the expert's rows
 // The pair shape is what shared memory and L2 bandwidth ask for: a 64-deep
 // slice feeds 1024 cycles of products with 48 KB per SM, where a single block's
 // 256 x 256 tile reads 64 KB, and its operands a third more of shared memory.
@@ -41,7 +42,7 @@ constexpr int kTileBBytes = kMaxN / 2 * kSlice * 2;
 constexpr int kStageBytes = 2 * kTileABytes + kTileBBytes;
 constexpr int kBoxRows = 32;   // rows of one TMA box of a k-contiguous B
 constexpr int kEpiWarps = 8;
-constexpr int kProductThreads = (kEpiWarps + 2) * 32;
+constexpr int kProductThreads = (kEpiWarps + 3) * 32;
 // Staging of 16 columns of a warp's block: 16 rows of 32 values transposed, or
 // 32 rows of 16, each padded by 4 against bank conflicts.
 constexpr int kStageFloats = 32 * (16 + 4);
@@ -197,8 +198,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   constexpr bool kAMn = kUse == kRowsGrad || kUse == kWeightGrad;
   constexpr bool kBMn = kUse == kWeightGrad;
   extern __shared__ uint8_t smem_raw[];
-  // s_full, s_free and s_peer are used in the pair's first block only, s_tail in
-  // its second.
+  // s_full, s_free and s_peer are used in the pair's first block only.
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_done[2], s_free[2],
       s_peer[kStages], s_tail[kStages];
   __shared__ uint32_t s_tmem;
@@ -304,27 +304,27 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   auto narrow = [](int cols) { return cols <= kMaxN / 2; };
 
   if (warp == kEpiWarps) {
-    uint32_t step = 0;
-    bool ok = true;
-    for (int t = pair; t < total && ok; t += pairs) {
-      const Tile tile = find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks);
-      const int n_slices = slices(tile), half_n = mma_n(columns(tile)) / 2;
-      const int a_tiles = two(tile) ? 2 : 1;
-      const int b_boxes = kBMn ? (half_n + 63) / 64 : (half_n + kBoxRows - 1) / kBoxRows;
-      const uint32_t bytes = a_tiles * kTileABytes +
-                             b_boxes * (kBMn ? 64 * kSlice * 2 : kBoxRows * kSlice * 2);
-      for (int s = 0; s < n_slices; ++s, ++step) {
-        const int st = step % kStages;
-        if (!warp_wait(smem_addr(&s_empty[st]), (step / kStages & 1) ^ 1, gave_up)) {
-          ok = false;
-          break;
-        }
-        if (elect_one()) {
-          // Both blocks' loads report to the first block's barrier; a tail
-          // slice of the second block to its own, as it is cleared there.
+    if (lane == 0) {  // one lane alone: a warp-wide wait per slice costs a quarter of the rate
+      uint32_t step = 0;
+      bool ok = true;
+      for (int t = pair; t < total && ok; t += pairs) {
+        const Tile tile = find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks);
+        const int n_slices = slices(tile), half_n = mma_n(columns(tile)) / 2;
+        const int a_tiles = two(tile) ? 2 : 1;
+        const int b_boxes = kBMn ? (half_n + 63) / 64 : (half_n + kBoxRows - 1) / kBoxRows;
+        const uint32_t bytes = a_tiles * kTileABytes +
+                               b_boxes * (kBMn ? 64 * kSlice * 2 : kBoxRows * kSlice * 2);
+        for (int s = 0; s < n_slices; ++s, ++step) {
+          const int st = step % kStages;
+          if (!mbar_wait(smem_addr(&s_empty[st]), (step / kStages & 1) ^ 1, gave_up)) {
+            ok = false;
+            break;
+          }
+          // Both blocks' loads report to the first block's barrier; those of a
+          // tail slice to their own block's, where it is cleared first.
           uint32_t full = smem_addr(&s_full[st]);
           if (is_tail(tile, s)) {
-            if (rank != 0) full = smem_addr(&s_tail[st]);
+            full = smem_addr(&s_tail[st]);
             mbar_expect(full, bytes);
           } else if (rank == 0) {
             mbar_expect(full, 2 * bytes);
@@ -356,62 +356,50 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
                           tile.lo + rank * half_n + i * kBoxRows, full);
           }
         }
-        __syncwarp();
       }
-    }
-    // Nothing of this block may still be in flight when it ends.  After an
-    // ordinary run every load was seen; after a wait gave up, the loads are
-    // given the time of one wait to be used.
-    if (*gave_up != 0 && lane == 0) {
-      const unsigned long long t0 = now_ns();
-      for (uint32_t i = 1; i <= kStages && i <= step; ++i) {
-        const uint32_t last = step - i;  // the newest load of its stage
-        while (!mbar_try(smem_addr(&s_empty[last % kStages]), last / kStages & 1) &&
-               now_ns() - t0 < kWaitNs) {
+      // Nothing of this block may still be in flight when it ends.  After an
+      // ordinary run every load was seen; after a wait gave up, the loads are
+      // given the time of one wait to be used.
+      if (*gave_up != 0) {
+        const unsigned long long t0 = now_ns();
+        for (uint32_t i = 1; i <= kStages && i <= step; ++i) {
+          const uint32_t last = step - i;  // the newest load of its stage
+          while (!mbar_try(smem_addr(&s_empty[last % kStages]), last / kStages & 1) &&
+                 now_ns() - t0 < kWaitNs) {
+          }
         }
       }
     }
     __syncwarp();
-  } else if (warp == kEpiWarps + 1 && rank == 0) {
-    uint32_t step = 0, used[2] = {0, 0};
-    uint32_t tails = 0;  // bit st: parity of the stage's tail slices so far
-    int next = 0;
-    bool ok = true;
-    for (int t = pair; t < total && ok; t += pairs) {
-      const Tile tile = find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks);
-      const int n_slices = slices(tile);
-      if (n_slices == 0) continue;
-      const int cols = columns(tile), n = mma_n(cols);
-      const bool both = two(tile), half = narrow(cols);
-      const uint32_t idesc = instr_desc(kBf16, kAMn, kBMn, 256, n);
-      const int buf = half ? next : 0;
-      next = half ? next ^ 1 : 0;
-      const uint32_t acc0 = tmem + buf * kMaxN, acc1 = acc0 + (half ? kMaxN / 2 : kMaxN);
-      if (!warp_wait(smem_addr(&s_free[buf]), (used[buf]++ & 1) ^ 1, gave_up)) break;
-      if (!half && !warp_wait(smem_addr(&s_free[1]), (used[1]++ & 1) ^ 1, gave_up)) break;
-      tc_fence_after();
-      for (int s = 0; s < n_slices; ++s, ++step) {
-        const int st = step % kStages;
-        if (!warp_wait(smem_addr(&s_full[st]), step / kStages & 1, gave_up)) {
-          ok = false;
-          break;
-        }
-        const uint32_t pa = smem_addr(stages + st * kStageBytes);
-        const uint32_t pb = pa + 2 * kTileABytes;
-        int depth = kSlice / 16;
-        if (is_tail(tile, s)) {
-          const int left = tile.rows - s * kSlice;
-          depth = (left + 15) / 16;
-          clear_tail(st, left);
-          if (!warp_wait(smem_addr(&s_peer[st]), tails >> st & 1, gave_up)) {
+  } else if (warp == kEpiWarps + 1) {
+    if (rank == 0 && elect_one()) {
+      uint32_t step = 0, used[2] = {0, 0};
+      int next = 0;
+      bool ok = true;
+      for (int t = pair; t < total && ok; t += pairs) {
+        const Tile tile = find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks);
+        const int n_slices = slices(tile);
+        if (n_slices == 0) continue;
+        const int cols = columns(tile), n = mma_n(cols);
+        const bool both = two(tile), half = narrow(cols);
+        const uint32_t idesc = instr_desc(kBf16, kAMn, kBMn, 256, n);
+        const int buf = half ? next : 0;
+        next = half ? next ^ 1 : 0;
+        const uint32_t acc0 = tmem + buf * kMaxN, acc1 = acc0 + (half ? kMaxN / 2 : kMaxN);
+        if (!mbar_wait(smem_addr(&s_free[buf]), (used[buf]++ & 1) ^ 1, gave_up)) break;
+        if (!half && !mbar_wait(smem_addr(&s_free[1]), (used[1]++ & 1) ^ 1, gave_up)) break;
+        tc_fence_after();
+        for (int s = 0; s < n_slices; ++s, ++step) {
+          const int st = step % kStages;
+          if (!mbar_wait(smem_addr(&s_full[st]), step / kStages & 1, gave_up)) {
             ok = false;
             break;
           }
-          tails ^= 1u << st;
-        }
-        tc_fence_after();
-        if (elect_one()) {
+          tc_fence_after();
+          const uint32_t pa = smem_addr(stages + st * kStageBytes);
+          const uint32_t pb = pa + 2 * kTileABytes;
           constexpr uint32_t kStepA = kAMn ? 2048 : 32, kStepB = kBMn ? 2048 : 32;
+          const int depth = is_tail(tile, s) ? (tile.rows - s * kSlice + 15) / 16 : kSlice / 16;
           for (int i = 0; i < depth; ++i) {
             const uint64_t db = smem_desc(pb + i * kStepB, kBMn ? 8192 : 16, 1024);
             const bool acc = s > 0 || i > 0;
@@ -423,39 +411,46 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           tc_commit(smem_addr(&s_empty[st]));
           if (s == n_slices - 1) tc_commit(smem_addr(&s_done[buf]));
         }
-        __syncwarp();
       }
-    }
-    // The products are over before the memory they read and write is given up.
-    if (*gave_up != 0 && lane == 0) {
-      const unsigned long long t0 = now_ns();
-      for (uint32_t i = 1; i <= kStages && i <= step; ++i) {
-        const uint32_t last = step - i;
-        while (!mbar_try(smem_addr(&s_empty[last % kStages]), last / kStages & 1) &&
-               now_ns() - t0 < kWaitNs) {
+      // The products are over before the memory they read and write is given up.
+      if (*gave_up != 0) {
+        const unsigned long long t0 = now_ns();
+        for (uint32_t i = 1; i <= kStages && i <= step; ++i) {
+          const uint32_t last = step - i;
+          while (!mbar_try(smem_addr(&s_empty[last % kStages]), last / kStages & 1) &&
+                 now_ns() - t0 < kWaitNs) {
+          }
         }
       }
     }
     __syncwarp();
-  } else if (warp == kEpiWarps + 1) {
+  } else if (warp == kEpiWarps + 2) {
     if (kUse == kWeightGrad) {
-      // The second block's tail slices: clear, then tell the first block.
-      uint32_t step = 0, tails = 0;
+      // Tail slices: both blocks clear theirs, the second tells the first, and
+      // the first releases the slice to the products.
+      uint32_t step = 0;
+      uint32_t tails = 0;  // bit st: parity of the stage's tail slices so far
       for (int t = pair; t < total; t += pairs) {
         const Tile tile = find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks);
         const int n_slices = slices(tile);
         if (n_slices > 0 && is_tail(tile, n_slices - 1)) {
           const int st = (step + n_slices - 1) % kStages;
-          if (!warp_wait(smem_addr(&s_tail[st]), tails >> st & 1, gave_up)) break;
+          const uint32_t parity = tails >> st & 1;
           tails ^= 1u << st;
+          if (!warp_wait(smem_addr(&s_tail[st]), parity, gave_up)) break;
           clear_tail(st, tile.rows - (n_slices - 1) * kSlice);
-          if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&s_peer[st]), 0));
+          if (rank != 0) {
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&s_peer[st]), 0));
+          } else {
+            if (!warp_wait(smem_addr(&s_peer[st]), parity, gave_up)) break;
+            if (lane == 0) mbar_arrive(smem_addr(&s_full[st]));
+          }
         }
         step += n_slices;
       }
       __syncwarp();
     }
-  } else if (warp < kEpiWarps) {
+  } else {
     const int quad = warp & 3;
     float* stage = staging + warp * kStageFloats;
     T* out = static_cast<T*>(a.out);
