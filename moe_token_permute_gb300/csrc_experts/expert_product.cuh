@@ -529,8 +529,8 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_cluster(buf == 0 ? free0 : free1);
-          if (!half) mbar_arrive_cluster(free1);
+          mbar_arrive_relaxed_cluster(buf == 0 ? free0 : free1);
+          if (!half) mbar_arrive_relaxed_cluster(free1);
         }
       }
     }

@@ -9,6 +9,7 @@
 #include <type_traits>
 
 #include "../csrc/common.cuh"
+#include "expert_decode.cuh"
 #include "expert_grad.cuh"
 #include "expert_math.cuh"
 #include "expert_product.cuh"
@@ -79,6 +80,35 @@ bool make_map(CUtensorMap* map, const void* base, int64_t planes, int64_t rows, 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The weight [E, N, K] as [E, K/64, N, 64], tiles of blocks x rows x 64.
+template <typename T>
+bool make_decode_map(CUtensorMap* map, const void* base, int64_t E, int64_t N, int64_t K,
+                     int rows) {
+  const EncodeFn encode = encode_fn();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(K / 64),
+                              static_cast<cuuint64_t>(E)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(K) * 2, 128,
+                                 static_cast<cuuint64_t>(N) * static_cast<cuuint64_t>(K) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), kDecodeBlocks, 1};
+  const cuuint32_t steps[4] = {1, 1, 1, 1};
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  return encode(map, kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The most tiles a product may have.
+template <int kUse>
+int64_t most_tiles(const ProductArgs& a) {
+  const int64_t m = kUse == kForward || kUse == kWeightGrad ? a.N : kUse == kGated ? a.N / 2 : a.K;
+  const int64_t columns = kUse == kWeightGrad
+                              ? a.E * ceil_div(a.K, kMaxN)
+                              : a.num_rows / kMaxN + std::min<int64_t>(a.E, a.num_rows);
+  return ceil_div(m, m_step<kUse>()) * columns;
+}
+
 // lhs: the weight, or dz for d_weight; rhs: the rows, or dz for d_rows.
 template <typename T, int kUse>
 cudaError_t launch_product(const ProductArgs& a, const void* lhs, const void* rhs, int sms,
@@ -96,15 +126,30 @@ cudaError_t launch_product(const ProductArgs& a, const void* lhs, const void* rh
          make_map<T>(&map_b, rhs, 0, a.num_rows, kUse == kRowsGrad ? a.N : a.K, kBoxRows);
   }
   if (!ok) return cudaErrorInvalidValue;
-  const int64_t m = kUse == kForward || kUse == kWeightGrad ? a.N : kUse == kGated ? a.N / 2 : a.K;
-  const int64_t m_blocks = ceil_div(m, m_step<kUse>());
-  const int64_t tiles =
-      m_blocks * (kUse == kWeightGrad ? a.E * ceil_div(a.K, kMaxN)
-                                      : a.num_rows / kMaxN + std::min<int64_t>(a.E, a.num_rows));
+  const int64_t tiles = most_tiles<kUse>(a);
   if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
   return launch(k_expert_product<T, kUse>,
                 dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, sms / 2))), kProductThreads,
                 product_smem(a.E), s, map_a, map_b, a);
+}
+
+template <typename T, int kUse>
+cudaError_t launch_forward(const ProductArgs& a, const void* weight, const void* rows, int sms,
+                           cudaStream_t s) {
+  if (!decode_pays(a.num_rows, a.K, most_tiles<kUse>(a), sms / 2))
+    return launch_product<T, kUse>(a, weight, rows, sms, s);
+  constexpr bool kGatedForm = kUse == kGated;
+  // Tasks at most: every expert with rows has one group, and each further
+  // kDecodeGroup rows one more.
+  const int64_t groups = std::min<int64_t>(a.E, a.num_rows) + a.num_rows / kDecodeGroup;
+  const int64_t tasks = groups * ((kGatedForm ? a.N / 2 : a.N) / kDecodeFeatures);
+  if (tasks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  CUtensorMap map;
+  if (!make_decode_map<T>(&map, weight, a.E, a.N, a.K, kDecodeFeatures))
+    return cudaErrorInvalidValue;
+  return launch(k_expert_decode<T, kGatedForm>,
+                dim3(static_cast<unsigned>(std::min<int64_t>(tasks, sms))), kDecodeThreads,
+                DecodeShape<kGatedForm>::kSmem, s, map, static_cast<const T*>(rows), a);
 }
 
 template <typename T, bool kGatedForm>
@@ -209,8 +254,8 @@ int moe_expert_gated(const void* permuted_rows, const void* weight, moe_dtype_t 
   a.preact = preact;
   a.status = status_of(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return finish(dtype == MOE_DTYPE_BF16 ? launch_product<__nv_bfloat16, kGated>(a, weight, permuted_rows, sms, s)
-                                        : launch_product<__half, kGated>(a, weight, permuted_rows, sms, s));
+  return finish(dtype == MOE_DTYPE_BF16 ? launch_forward<__nv_bfloat16, kGated>(a, weight, permuted_rows, sms, s)
+                                        : launch_forward<__half, kGated>(a, weight, permuted_rows, sms, s));
 }
 
 int moe_expert_gated_backward(const void* d_out, const void* permuted_rows, const void* weight,
@@ -279,8 +324,8 @@ int moe_expert_linear(const void* rows, const void* weight, moe_dtype_t dtype,
   a.preact = preact;
   a.status = status_of(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return finish(dtype == MOE_DTYPE_BF16 ? launch_product<__nv_bfloat16, kForward>(a, weight, rows, sms, s)
-                                        : launch_product<__half, kForward>(a, weight, rows, sms, s));
+  return finish(dtype == MOE_DTYPE_BF16 ? launch_forward<__nv_bfloat16, kForward>(a, weight, rows, sms, s)
+                                        : launch_forward<__half, kForward>(a, weight, rows, sms, s));
 }
 
 int moe_expert_linear_backward(const void* d_out, const void* rows, const void* weight,
