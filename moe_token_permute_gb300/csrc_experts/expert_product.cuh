@@ -43,10 +43,8 @@ constexpr int kStageBytes = 2 * kTileABytes + kTileBBytes;
 constexpr int kBoxRows = 32;   // rows of one TMA box of a k-contiguous B
 constexpr int kEpiWarps = 8;
 constexpr int kProductThreads = (kEpiWarps + 3) * 32;
-// Staging of 16 columns of a warp's block: 16 rows of 32 values transposed, or
-// 32 rows of 16, each padded by 4 against bank conflicts.
-constexpr int kStageFloats = 32 * (16 + 4);
-constexpr int kStagingBytes = kEpiWarps * kStageFloats * 4;
+constexpr int kStagingWarpBytes = 32 * 64;  // 32 x 32 outputs of 16 bits
+constexpr int kStagingBytes = kEpiWarps * kStagingWarpBytes;
 
 struct ProductArgs {
   const int64_t* offset;
@@ -120,15 +118,6 @@ __device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const 
   return r;
 }
 
-// Eight consecutive outputs of a row, rounded and stored as 16 bytes.
-template <typename T>
-__device__ __forceinline__ void store8(T* dst, const float* v) {
-  Vec8<T> o;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) o.e[i] = from_f<T>(v[i]);
-  *reinterpret_cast<uint4*>(dst) = o.v;
-}
-
 template <int kAct>
 __device__ __forceinline__ void apply_act(float (&v)[32]) {
 #pragma unroll
@@ -140,50 +129,91 @@ __device__ __forceinline__ void apply_act(int a, float (&v)[32]) {
   else if (a == MOE_ACT_RELU) apply_act<MOE_ACT_RELU>(v);
 }
 
-// A warp's 32 x 32 values, lane l holding v[j] = value (l, j), to the matrix
-// `out` of row pitch `pitch`: transposed, value (l, j) goes to row r0 + j,
-// column c0 + l; else to row r0 + l, column c0 + j.  Rows and columns from
-// `rows` and `cols` on are left out (cols is a multiple of 8).  Through shared
-// memory, so that neighbouring lanes write consecutive bytes of a row (64
-// transposed, 32 not: whole sectors).
-template <typename T, bool kTranspose>
-__device__ __forceinline__ void write_block(const float (&v)[32], float* stage, T* out,
-                                            const T* residual, int64_t pitch, int64_t r0, int rows,
-                                            int64_t c0, int64_t cols) {
-  constexpr int kPitch = kTranspose ? 36 : 20;
-  constexpr int kLanesPerRow = kTranspose ? 4 : 2;
-  const int lane = threadIdx.x & 31;
+// A warp's 32 x 32 block of a matrix in memory: rows r0 + [0, rows) and columns
+// c0 + [0, 32) below `cols` (a multiple of 8).  Its shared memory copy has rows
+// of 64 bytes, the 16-byte chunks of two rows exchanged so that neither the
+// fragments' accesses (8 rows of a chunk) nor the rows' (2 rows) meet in a bank.
+template <typename T>
+struct Block {
+  T* at;            // the lane's first 8 values: row lane / 4, chunk lane % 4
+  int64_t step;     // 8 rows
+  int rows;         // of the lane's rows lane / 4 + 8 i, those below `rows` exist
+  uint32_t line;    // shared memory address of those 8 values
+  uint32_t matrix;  // and of the row the lane gives for fragments: lane % 8, chunk lane / 8
+
+  __device__ __forceinline__ Block(T* base, int64_t pitch, int64_t r0, int n_rows, int64_t c0,
+                                   int64_t cols, uint32_t stage) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    at = base + (r0 + r) * pitch + c0 + c * 8;
+    step = 8 * pitch;
+    rows = c0 + c * 8 < cols ? n_rows - r : 0;
+    line = stage + r * 64 + ((c ^ (r >> 1 & 3)) << 4);
+    const int m = lane & 7, k = lane >> 3;
+    matrix = stage + m * 64 + ((k ^ (m >> 1 & 3)) << 4);
+  }
+};
+
+__device__ __forceinline__ uint4 shared_load16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void shared_store16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// v, as tmem_load_32x32 gives it, rounded and written to the block.
+// kTranspose: tensor memory lanes are the block's columns; else its rows.
+template <bool kTranspose, typename T>
+__device__ __forceinline__ void write_block(const float (&v)[32], const Block<T>& b) {
+  uint32_t p[16];
 #pragma unroll
-  for (int h = 0; h < 32; h += 16) {
-    __syncwarp();
-    if (kTranspose) {
+  for (int i = 0; i < 16; ++i) p[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+  __syncwarp();  // the block before this one is read
 #pragma unroll
-      for (int j = 0; j < 16; ++j) stage[j * kPitch + lane] = v[h + j];
-    } else {
+  for (int j = 0; j < 4; ++j) {
+    // p[8 h + 2 i + s]: lanes 16 h + 8 s + [0, 8), columns 8 i + [0, 8)
+    if (kTranspose)
+      store_matrices<true>(b.matrix + j * 512, p[2 * j], p[2 * j + 1], p[8 + 2 * j],
+                           p[8 + 2 * j + 1]);
+    else
+      store_matrices<false>(b.matrix + j * 512, p[j / 2 * 8 + j % 2], p[j / 2 * 8 + 2 + j % 2],
+                            p[j / 2 * 8 + 4 + j % 2], p[j / 2 * 8 + 6 + j % 2]);
+  }
+  __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 16; j += 4)
-        *reinterpret_cast<float4*>(stage + lane * kPitch + j) =
-            make_float4(v[h + j], v[h + j + 1], v[h + j + 2], v[h + j + 3]);
-    }
-    __syncwarp();
-    const int seg = lane % kLanesPerRow * 8;
-    const int64_t col = c0 + seg + (kTranspose ? 0 : h);
+  for (int j = 0; j < 4; ++j) {
+    const uint4 x = shared_load16(b.line + j * 512);
+    if (8 * j < b.rows) *reinterpret_cast<uint4*>(b.at + j * b.step) = x;
+  }
+}
+
+// v += the block (transposed); what lies outside the matrix counts as zero.
+template <typename T>
+__device__ __forceinline__ void add_block(float (&v)[32], const Block<T>& b) {
+  uint4 x[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = i * (32 / kLanesPerRow) + lane / kLanesPerRow;
-      const int row = r + (kTranspose ? h : 0);
-      if (row >= rows || col >= cols) continue;
-      const float4* src = reinterpret_cast<const float4*>(stage + r * kPitch + seg);
-      const float4 p = src[0], q = src[1];
-      float w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-      const int64_t at = (r0 + row) * pitch + col;
-      if (residual != nullptr) {
-        Vec8<T> x;
-        x.v = *reinterpret_cast<const uint4*>(residual + at);
+  for (int j = 0; j < 4; ++j)
+    x[j] = 8 * j < b.rows ? *reinterpret_cast<const uint4*>(b.at + j * b.step)
+                          : make_uint4(0, 0, 0, 0);
+  __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] += to_f(x.e[k]);
-      }
-      store8(out + at, w);
+  for (int j = 0; j < 4; ++j) shared_store16(b.line + j * 512, x[j]);
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t r[4];
+    load_matrices_transposed(b.matrix + j * 512, r[0], r[1], r[2], r[3]);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const float2 f = unpack2<T>(r[m]);
+      v[m / 2 * 16 + 4 * j + m % 2 * 2] += f.x;
+      v[m / 2 * 16 + 4 * j + m % 2 * 2 + 1] += f.y;
     }
   }
 }
@@ -206,8 +236,8 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
 
   uint8_t* stages = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float* staging = reinterpret_cast<float*>(stages + kStages * kStageBytes);
-  Segment* segments = reinterpret_cast<Segment*>(reinterpret_cast<uint8_t*>(staging) + kStagingBytes);
+  uint8_t* staging = stages + kStages * kStageBytes;
+  Segment* segments = reinterpret_cast<Segment*>(staging + kStagingBytes);
   int* first = reinterpret_cast<int*>(segments + a.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
@@ -452,10 +482,10 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     }
   } else {
     const int quad = warp & 3;
-    float* stage = staging + warp * kStageFloats;
+    const uint32_t stage = smem_addr(staging + warp * kStagingWarpBytes);
     T* out = static_cast<T*>(a.out);
     T* preact = static_cast<T*>(a.preact);
-    const T* residual = static_cast<const T*>(a.residual);
+    T* residual = static_cast<T*>(const_cast<void*>(a.residual));
     uint32_t fin[2] = {0, 0};
     int next = 0;
     const uint32_t free0 = cluster_addr(smem_addr(&s_free[0]), 0);
@@ -474,53 +504,60 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       const uint32_t acc0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kMaxN;
       const uint32_t acc1 = acc0 + (half ? kMaxN / 2 : kMaxN);
       for (int c = warp / 4 * 32; c < cols; c += 64) {
+        // The block: features m + [0, 32) of rows tile.lo + c + [0, 32).
+        const int64_t row = tile.lo + c;
         if (kUse == kGated) {
-          const int64_t m = tile.m0 + rank * 128 + quad * 32;  // the warp's first feature
+          const int64_t m = tile.m0 + rank * 128 + quad * 32;
           float g[32], u[32];
-          tmem_load32(acc0 + c, g);
-          tmem_load32(acc1 + c, u);
+          tmem_load_32x32(acc0 + c, g);
+          tmem_load_32x32(acc1 + c, u);
           tmem_wait_load(g);
           tmem_wait_load(u);
           if (preact != nullptr) {
-            write_block<T, true>(g, stage, preact, nullptr, a.N, tile.lo + c, cols - c, m, F);
-            write_block<T, true>(u, stage, preact + F, nullptr, a.N, tile.lo + c, cols - c, m, F);
+            write_block<true>(g, Block<T>(preact, a.N, row, cols - c, m, F, stage));
+            write_block<true>(u, Block<T>(preact + F, a.N, row, cols - c, m, F, stage));
           }
           apply_act(a.act, g);
 #pragma unroll
           for (int i = 0; i < 32; ++i) g[i] *= u[i];
-          write_block<T, true>(g, stage, out, nullptr, F, tile.lo + c, cols - c, m, F);
+          write_block<true>(g, Block<T>(out, F, row, cols - c, m, F, stage));
         } else {
           const int parts = two(tile) ? 2 : 1;
           for (int i = 0; i < parts; ++i) {
             const int64_t m = feature(tile, i) + quad * 32;
             float z[32];
             if (any) {
-              tmem_load32((i == 0 ? acc0 : acc1) + c, z);
+              tmem_load_32x32((i == 0 ? acc0 : acc1) + c, z);
               tmem_wait_load(z);
             } else {
 #pragma unroll
               for (int j = 0; j < 32; ++j) z[j] = 0.f;
             }
             if (kUse == kForward) {
-              if (a.bias != nullptr && m + lane < a.N) {
-                const float bias = to_f(static_cast<const T*>(
-                    a.bias)[static_cast<int64_t>(tile.e) * a.N + m + lane]);
+              if (a.bias != nullptr) {
+                const T* bias = static_cast<const T*>(a.bias) + static_cast<int64_t>(tile.e) * a.N;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) z[j] += bias;
+                for (int j = 0; j < 4; ++j) {  // z[16 h + 4 i + 2 s + b]: feature 16 h + 8 s + g
+                  const int64_t f = m + j * 8 + (lane >> 2);
+                  const float x = f < a.N ? to_f(bias[f]) : 0.f;
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) z[j / 2 * 16 + k / 2 * 4 + j % 2 * 2 + k % 2] += x;
+                }
               }
               if (preact != nullptr)
-                write_block<T, true>(z, stage, preact, nullptr, a.N, tile.lo + c, cols - c, m,
-                                     a.N);
+                write_block<true>(z, Block<T>(preact, a.N, row, cols - c, m, a.N, stage));
               apply_act(a.act, z);
-              write_block<T, true>(z, stage, out, residual, a.N, tile.lo + c, cols - c, m, a.N);
+              if (residual != nullptr)
+                add_block(z, Block<T>(residual, a.N, row, cols - c, m, a.N, stage));
+              write_block<true>(z, Block<T>(out, a.N, row, cols - c, m, a.N, stage));
             } else if (kUse == kRowsGrad) {
-              write_block<T, true>(z, stage, out, nullptr, a.K, tile.lo + c, cols - c, m, a.K);
+              write_block<true>(z, Block<T>(out, a.K, row, cols - c, m, a.K, stage));
             } else {
               const int64_t left = a.N - m;
-              write_block<T, false>(z, stage, out, nullptr, a.K,
-                                    static_cast<int64_t>(tile.e) * a.N + m,
-                                    static_cast<int>(left < 32 ? (left < 0 ? 0 : left) : 32),
-                                    tile.n0 + c, a.K);
+              write_block<false>(
+                  z, Block<T>(out, a.K, static_cast<int64_t>(tile.e) * a.N + m,
+                              static_cast<int>(left < 32 ? (left < 0 ? 0 : left) : 32),
+                              tile.n0 + c, a.K, stage));
             }
           }
         }

@@ -207,21 +207,25 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
       : "memory");
 }
 
-// 32 columns of the warp's 32 lanes: v[j] = D[lane][col + j].
-__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
-  uint32_t r[32];
+// 32 columns of 16 of the warp's 32 lanes, as the fragments of mma.sync: lane
+// (g, q) gets v[kAt + 4 i + 2 s + b] = D[lane 8 s + g][column 8 i + 2 q + b].
+template <int kAt>
+__device__ __forceinline__ void tmem_load_16x32(uint32_t addr, float (&v)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, "
+      "%8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[kAt + 0]), "=f"(v[kAt + 1]), "=f"(v[kAt + 2]), "=f"(v[kAt + 3]),
+        "=f"(v[kAt + 4]), "=f"(v[kAt + 5]), "=f"(v[kAt + 6]), "=f"(v[kAt + 7]),
+        "=f"(v[kAt + 8]), "=f"(v[kAt + 9]), "=f"(v[kAt + 10]), "=f"(v[kAt + 11]),
+        "=f"(v[kAt + 12]), "=f"(v[kAt + 13]), "=f"(v[kAt + 14]), "=f"(v[kAt + 15])
       : "r"(addr));
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 32 columns of the warp's 32 lanes: v[16 h + 4 i + 2 s + b] =
+// D[lane 16 h + 8 s + g][column 8 i + 2 q + b].
+__device__ __forceinline__ void tmem_load_32x32(uint32_t addr, float (&v)[32]) {
+  tmem_load_16x32<0>(addr, v);
+  tmem_load_16x32<16>(addr + (16u << 16), v);
 }
 // The loaded values pass through the wait, so that no use of them can be moved
 // in front of it.
@@ -233,6 +237,30 @@ __device__ __forceinline__ void tmem_wait_load(float (&v)[32]) {
                  "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
                  "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
                  "+f"(v[30]), "+f"(v[31])::"memory");
+}
+
+// Four 8 x 8 matrices of 16-bit values, in fragments, to or from the rows whose
+// addresses the lanes give (lane l: row l % 8 of matrix l / 8); transposed,
+// what a fragment holds as row and column is column and row in memory.
+template <bool kTranspose>
+__device__ __forceinline__ void store_matrices(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                               uint32_t d) {
+  if (kTranspose)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                     addr),
+                 "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+  else
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void load_matrices_transposed(uint32_t addr, uint32_t& a, uint32_t& b,
+                                                         uint32_t& c, uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(addr)
+               : "memory");
 }
 
 // Shared memory descriptor of a 128-byte-swizzled operand tile.
