@@ -201,10 +201,10 @@ k_expert_decode(const __grid_constant__ CUtensorMap map, const T* __restrict__ x
           const uint32_t bytes = min(kDecodeSlice, K - k) * 2;
           mbar_expect(full, Shape::kTiles * kDecodeTileBytes + task.rows * bytes);
           uint32_t dst = smem_addr(ring + st * Shape::kStageBytes);
-          tma_load_4d(dst, &map, 0, f0, s * kDecodeBlocks, task.e, full);
+          tma_load_4d_single(dst, &map, 0, f0, s * kDecodeBlocks, task.e, full);
           dst += kDecodeTileBytes;
           if (kGatedForm) {
-            tma_load_4d(dst, &map, 0, F + f0, s * kDecodeBlocks, task.e, full);
+            tma_load_4d_single(dst, &map, 0, F + f0, s * kDecodeBlocks, task.e, full);
             dst += kDecodeTileBytes;
           }
           for (int i = 0; i < task.rows; ++i, dst += kDecodePitch)

@@ -36,11 +36,10 @@ enum Use { kForward, kGated, kRowsGrad, kWeightGrad };
 
 constexpr int kMaxN = 256;     // columns of one accumulator
 constexpr int kSlice = 64;     // contraction depth of one stage: 128 bytes
-constexpr int kStages = 4;
 constexpr int kTileABytes = 128 * kSlice * 2;
 constexpr int kTileBBytes = kMaxN / 2 * kSlice * 2;
-constexpr int kStageBytes = 2 * kTileABytes + kTileBBytes;
-constexpr int kBoxRows = 32;   // rows of one TMA box of a k-contiguous B
+constexpr int kRingBytes = 192 * 1024;  // stages
+constexpr int kBoxRows = 32;   // rows of the small TMA box of a k-contiguous B; the large: 128
 constexpr int kEpiWarps = 8;
 constexpr int kProductThreads = (kEpiWarps + 3) * 32;
 constexpr int kStagingWarpBytes = 32 * 64;  // 32 x 32 outputs of 16 bits
@@ -62,10 +61,10 @@ struct ProductArgs {
 // Dynamic shared memory: stages (1024-byte aligned), staging, then each
 // expert's rows and its first tile.
 inline size_t product_smem(int E) {
-  return 1024 + kStages * kStageBytes + kStagingBytes + static_cast<size_t>(E) * 12 + 4;
+  return 1024 + kRingBytes + kStagingBytes + static_cast<size_t>(E) * 12 + 4;
 }
 
-static_assert(1024 + kStages * kStageBytes + kStagingBytes + MOE_MAX_LOCAL_EXPERTS * 12 + 4 + 1024 <=
+static_assert(1024 + kRingBytes + kStagingBytes + MOE_MAX_LOCAL_EXPERTS * 12 + 4 + 1024 <=
                   227 * 1024,
               "shared memory of one block");
 
@@ -80,11 +79,13 @@ __device__ __forceinline__ int block_rows(int rows, int blocks) {
   return ((rows + blocks - 1) / blocks + 15) / 16 * 16;
 }
 
-// Output features of one tile of the pair.
+// Output features of one A tile of the pair, and of the pair's kMt A tiles.
 template <int kUse>
-__host__ __device__ constexpr int m_step() { return kUse == kGated ? 256 : 512; }
+__host__ __device__ constexpr int m_unit() { return kUse == kGated ? 128 : 256; }
+template <int kUse, int kMt>
+__host__ __device__ constexpr int m_step() { return m_unit<kUse>() * kMt; }
 
-template <int kUse>
+template <int kUse, int kMt>
 __device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const int* first, int t,
                                           int m_blocks, int n_blocks) {
   Tile r;
@@ -95,7 +96,7 @@ __device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const 
     const Segment s = segments[r.e];
     r.lo = s.lo;
     r.rows = s.hi - s.lo;
-    r.m0 = local / n_blocks * m_step<kUse>();
+    r.m0 = local / n_blocks * m_step<kUse, kMt>();
     r.n0 = local % n_blocks * kMaxN;
     return r;
   }
@@ -113,43 +114,52 @@ __device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const 
   const int b = local % blocks;
   r.lo = s.lo + b * step;
   r.rows = min(step, rows - b * step);
-  r.m0 = local / blocks * m_step<kUse>();
+  r.m0 = local / blocks * m_step<kUse, kMt>();
   r.n0 = 0;
   return r;
 }
 
-template <int kAct>
-__device__ __forceinline__ void apply_act(float (&v)[32]) {
+template <int kCount, int kAct>
+__device__ __forceinline__ void apply_act(float* v) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = act<kAct>(v[i]);
+  for (int i = 0; i < kCount; ++i) v[i] = act<kAct>(v[i]);
 }
-__device__ __forceinline__ void apply_act(int a, float (&v)[32]) {
-  if (a == MOE_ACT_SILU) apply_act<MOE_ACT_SILU>(v);
-  else if (a == MOE_ACT_GELU) apply_act<MOE_ACT_GELU>(v);
-  else if (a == MOE_ACT_RELU) apply_act<MOE_ACT_RELU>(v);
+template <int kCount>
+__device__ __forceinline__ void apply_act(int a, float* v) {
+  if (a == MOE_ACT_SILU) apply_act<kCount, MOE_ACT_SILU>(v);
+  else if (a == MOE_ACT_GELU) apply_act<kCount, MOE_ACT_GELU>(v);
+  else if (a == MOE_ACT_RELU) apply_act<kCount, MOE_ACT_RELU>(v);
 }
 
-// A warp's 32 x 32 block of a matrix in memory: rows r0 + [0, rows) and columns
-// c0 + [0, 32) below `cols` (a multiple of 8).  Its shared memory copy has rows
-// of 64 bytes, the 16-byte chunks of two rows exchanged so that neither the
-// fragments' accesses (8 rows of a chunk) nor the rows' (2 rows) meet in a bank.
-template <typename T>
+// A warp's block of a matrix in memory: rows r0 + [0, rows), at most 32, and
+// columns c0 + [0, kCols) below `cols` (a multiple of 8).  Its shared memory copy
+// has rows of kCols values, the 16-byte chunks of some rows exchanged so that
+// neither the fragments' accesses (8 rows of a chunk) nor the rows' (128 bytes)
+// meet in a bank.
+template <typename T, int kCols = 32>
 struct Block {
-  T* at;            // the lane's first 8 values: row lane / 4, chunk lane % 4
-  int64_t step;     // 8 rows
-  int rows;         // of the lane's rows lane / 4 + 8 i, those below `rows` exist
+  static constexpr int kChunks = kCols / 8;          // 16 bytes each, of a row
+  static constexpr int kLaneRows = 32 / kChunks;     // rows the warp reads at once
+  T* at;            // the lane's first 8 values: row lane / kChunks, chunk lane % kChunks
+  int64_t step;     // kLaneRows rows
+  int rows;         // of the lane's rows lane / kChunks + kLaneRows i, those below `rows` exist
   uint32_t line;    // shared memory address of those 8 values
-  uint32_t matrix;  // and of the row the lane gives for fragments: lane % 8, chunk lane / 8
+  uint32_t matrix;  // and of the row the lane gives for fragments
 
+  static __device__ __forceinline__ uint32_t place(int row, int chunk) {
+    return row * (kCols * 2) + ((chunk ^ (kCols == 32 ? row >> 1 & 3 : row >> 2 & 1)) << 4);
+  }
   __device__ __forceinline__ Block(T* base, int64_t pitch, int64_t r0, int n_rows, int64_t c0,
                                    int64_t cols, uint32_t stage) {
-    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const int lane = threadIdx.x & 31, r = lane / kChunks, c = lane % kChunks;
     at = base + (r0 + r) * pitch + c0 + c * 8;
-    step = 8 * pitch;
+    step = kLaneRows * pitch;
     rows = c0 + c * 8 < cols ? n_rows - r : 0;
-    line = stage + r * 64 + ((c ^ (r >> 1 & 3)) << 4);
-    const int m = lane & 7, k = lane >> 3;
-    matrix = stage + m * 64 + ((k ^ (m >> 1 & 3)) << 4);
+    line = stage + place(r, c);
+    // 32 columns: lane l row l % 8 of chunk l / 8; 16: chunk l / 8 % 2 of row
+    // l % 8, the upper lanes of row 8 + l % 8.
+    const int k = lane >> 3;
+    matrix = stage + (kCols == 32 ? place(lane & 7, k) : place((k >> 1) * 8 + (lane & 7), k & 1));
   }
 };
 
@@ -193,6 +203,24 @@ __device__ __forceinline__ void write_block(const float (&v)[32], const Block<T>
   }
 }
 
+// The transposed block of 16 tensor memory lanes: v[4 i + 2 s + b].
+template <typename T>
+__device__ __forceinline__ void write_half_block(const float* v, const Block<T, 16>& b) {
+  uint32_t p[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+  __syncwarp();  // the block before this one is read
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    store_matrices<true>(b.matrix + j * 512, p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint4 x = shared_load16(b.line + j * 512);
+    if (16 * j < b.rows) *reinterpret_cast<uint4*>(b.at + j * b.step) = x;
+  }
+}
+
 // v += the block (transposed); what lies outside the matrix counts as zero.
 template <typename T>
 __device__ __forceinline__ void add_block(float (&v)[32], const Block<T>& b) {
@@ -220,10 +248,13 @@ __device__ __forceinline__ void add_block(float (&v)[32], const Block<T>& b) {
 
 // map_a, map_b: the operands as TMA tiles of 64 contiguous values (128 bytes,
 // 128-byte swizzle) by 128 (forward A), 64 (MN-major) or kBoxRows rows.
-template <typename T, int kUse>
+template <typename T, int kUse, int kMt>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 k_expert_product(const __grid_constant__ CUtensorMap map_a,
-                 const __grid_constant__ CUtensorMap map_b, const ProductArgs a) {
+                 const __grid_constant__ CUtensorMap map_b,
+                 const __grid_constant__ CUtensorMap map_b_large, const ProductArgs a) {
+  constexpr int kStageBytes = kMt * kTileABytes + kTileBBytes;
+  constexpr int kStages = kRingBytes / kStageBytes;
   constexpr bool kBf16 = sizeof(T) == 2 && !__is_same(T, __half);
   constexpr bool kAMn = kUse == kRowsGrad || kUse == kWeightGrad;
   constexpr bool kBMn = kUse == kWeightGrad;
@@ -258,6 +289,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     s_gave_up = 0;
     tma_prefetch_map(&map_a);
     tma_prefetch_map(&map_b);
+    if (!kBMn) tma_prefetch_map(&map_b_large);
   }
   if (warp == kEpiWarps + 1) tmem_alloc(smem_addr(&s_tmem), 512);
   pdl_wait();
@@ -266,7 +298,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   const int F = static_cast<int>(a.N / 2);
   const int m_size = static_cast<int>(kUse == kForward ? a.N : kUse == kGated ? F
                                       : kUse == kRowsGrad ? a.K : a.N);
-  const int m_blocks = (m_size + m_step<kUse>() - 1) / m_step<kUse>();
+  const int m_blocks = (m_size + m_step<kUse, kMt>() - 1) / m_step<kUse, kMt>();
   const int n_blocks = static_cast<int>((a.K + kMaxN - 1) / kMaxN);  // d_weight
   int total = 0;
   bool bad = false;
@@ -307,10 +339,10 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     return kUse == kWeightGrad ? min(kMaxN, static_cast<int>(a.K) - t.n0) : t.rows;
   };
   auto mma_n = [](int cols) { return (cols + 15) / 16 * 16; };
-  auto two = [&](const Tile& t) { return kUse == kGated || t.m0 + 256 < m_size; };
+  auto two = [&](const Tile& t) { return kMt == 2 && t.m0 + m_unit<kUse>() < m_size; };
   // First feature of the block's i-th A tile.
   auto feature = [&](const Tile& t, int i) {
-    return t.m0 + rank * 128 + (kUse == kGated ? i * F : i * 256);
+    return t.m0 + i * m_unit<kUse>() + rank * (m_unit<kUse>() / 2);
   };
   // Whether slice s of a d_weight tile runs past the expert's rows.
   auto is_tail = [&](const Tile& t, int s) {
@@ -320,30 +352,33 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   // expert or to none and may be infinite or NaN, so it is overwritten in both
   // operands rather than multiplied by zeros.
   auto clear_tail = [&](int st, int left) {
+    constexpr int kBoxes = kStageBytes / (kTileABytes / 2);  // 64 values x 64 rows each
     const int rows = (left + 15) / 16 * 16 - left;
-    for (int i = lane; i < rows * 48; i += 32) {
-      const int box = i / 8 % 6, r = left + i / 48;
+    for (int i = lane; i < rows * kBoxes * 8; i += 32) {
+      const int box = i / 8 % kBoxes, r = left + i / 8 / kBoxes;
       *reinterpret_cast<uint4*>(stages + st * kStageBytes + box * (kTileABytes / 2) + r * 128 +
                                 (i & 7) * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_async_shared();
     __syncwarp();
   };
-  // Tensor memory of a tile: a wide one takes all of it, narrow ones take
-  // turns with its halves.
-  auto narrow = [](int cols) { return cols <= kMaxN / 2; };
+  // Tensor memory of a tile: half of it in turn, or, with two A tiles of more
+  // than half the columns, all of it.
+  auto narrow = [](int cols) { return kMt == 1 || cols <= kMaxN / 2; };
 
   if (warp == kEpiWarps) {
     if (lane == 0) {  // one lane alone: a warp-wide wait per slice costs a quarter of the rate
       uint32_t step = 0;
       bool ok = true;
       for (int t = pair; t < total && ok; t += pairs) {
-        const Tile tile = find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks);
+        const Tile tile = find_tile<kUse, kMt>(a.E, segments, first, t, m_blocks, n_blocks);
         const int n_slices = slices(tile), half_n = mma_n(columns(tile)) / 2;
         const int a_tiles = two(tile) ? 2 : 1;
-        const int b_boxes = kBMn ? (half_n + 63) / 64 : (half_n + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = a_tiles * kTileABytes +
-                               b_boxes * (kBMn ? 64 * kSlice * 2 : kBoxRows * kSlice * 2);
+        const bool large = !kBMn && half_n > 64;
+        const int b_boxes = kBMn ? (half_n + 63) / 64
+                            : large ? 1 : (half_n + kBoxRows - 1) / kBoxRows;
+        const int box_rows = kBMn ? 64 : large ? 128 : kBoxRows;
+        const uint32_t bytes = a_tiles * kTileABytes + b_boxes * box_rows * kSlice * 2;
         for (int s = 0; s < n_slices; ++s, ++step) {
           const int st = step % kStages;
           if (!mbar_wait(smem_addr(&s_empty[st]), (step / kStages & 1) ^ 1, gave_up)) {
@@ -362,12 +397,20 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
             full = cluster_addr(full, 0);
           }
           const uint32_t sa = smem_addr(stages + st * kStageBytes);
-          const uint32_t sb = sa + 2 * kTileABytes;
+          const uint32_t sb = sa + kMt * kTileABytes;
           const int k = s * kSlice;
           for (int i = 0; i < a_tiles; ++i) {
             const int m = feature(tile, i);
             const uint32_t dst = sa + i * kTileABytes;
-            if (kUse == kForward || kUse == kGated) {
+            if (kUse == kGated) {
+              if (F % 16 == 0) {  // a tile in one load (make_gated_map)
+                tma_load_5d(dst, &map_a, k, 0, 0, m / 16, tile.e, full);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  tma_load_4d(dst + j * (kTileABytes / 4), &map_a, k, m + j * 16, 0, tile.e, full);
+              }
+            } else if (kUse == kForward) {
               tma_load_3d(dst, &map_a, k, m, tile.e, full);
             } else if (kUse == kRowsGrad) {
               tma_load_3d(dst, &map_a, m, k, tile.e, full);
@@ -382,7 +425,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
               tma_load_2d(sb + i * 64 * kSlice * 2, &map_b, tile.n0 + rank * half_n + i * 64,
                           tile.lo + k, full);
             else
-              tma_load_2d(sb + i * kBoxRows * kSlice * 2, &map_b, k,
+              tma_load_2d(sb + i * kBoxRows * kSlice * 2, large ? &map_b_large : &map_b, k,
                           tile.lo + rank * half_n + i * kBoxRows, full);
           }
         }
@@ -407,7 +450,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       int next = 0;
       bool ok = true;
       for (int t = pair; t < total && ok; t += pairs) {
-        const Tile tile = find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks);
+        const Tile tile = find_tile<kUse, kMt>(a.E, segments, first, t, m_blocks, n_blocks);
         const int n_slices = slices(tile);
         if (n_slices == 0) continue;
         const int cols = columns(tile), n = mma_n(cols);
@@ -427,7 +470,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           }
           tc_fence_after();
           const uint32_t pa = smem_addr(stages + st * kStageBytes);
-          const uint32_t pb = pa + 2 * kTileABytes;
+          const uint32_t pb = pa + kMt * kTileABytes;
           constexpr uint32_t kStepA = kAMn ? 2048 : 32, kStepB = kBMn ? 2048 : 32;
           const int depth = is_tail(tile, s) ? (tile.rows - s * kSlice + 15) / 16 : kSlice / 16;
           for (int i = 0; i < depth; ++i) {
@@ -461,7 +504,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       uint32_t step = 0;
       uint32_t tails = 0;  // bit st: parity of the stage's tail slices so far
       for (int t = pair; t < total; t += pairs) {
-        const Tile tile = find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks);
+        const Tile tile = find_tile<kUse, kMt>(a.E, segments, first, t, m_blocks, n_blocks);
         const int n_slices = slices(tile);
         if (n_slices > 0 && is_tail(tile, n_slices - 1)) {
           const int st = (step + n_slices - 1) % kStages;
@@ -491,7 +534,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     const uint32_t free0 = cluster_addr(smem_addr(&s_free[0]), 0);
     const uint32_t free1 = cluster_addr(smem_addr(&s_free[1]), 0);
     for (int t = pair; t < total; t += pairs) {
-      const Tile tile = find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks);
+      const Tile tile = find_tile<kUse, kMt>(a.E, segments, first, t, m_blocks, n_blocks);
       const int cols = columns(tile);
       const bool any = slices(tile) > 0, half = narrow(cols);
       int buf = 0;
@@ -507,20 +550,23 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
         // The block: features m + [0, 32) of rows tile.lo + c + [0, 32).
         const int64_t row = tile.lo + c;
         if (kUse == kGated) {
-          const int64_t m = tile.m0 + rank * 128 + quad * 32;
-          float g[32], u[32];
-          tmem_load_32x32(acc0 + c, g);
-          tmem_load_32x32(acc1 + c, u);
-          tmem_wait_load(g);
-          tmem_wait_load(u);
-          if (preact != nullptr) {
-            write_block<true>(g, Block<T>(preact, a.N, row, cols - c, m, F, stage));
-            write_block<true>(u, Block<T>(preact + F, a.N, row, cols - c, m, F, stage));
-          }
-          apply_act(a.act, g);
+          // The warp's 32 lanes: 16 gate rows, then the up rows of the same
+          // features; a thread holds both of a value in z[i] and z[16 + i].
+          const int parts = two(tile) ? 2 : 1;
+          for (int i = 0; i < parts; ++i) {
+            const int64_t m = feature(tile, i) + quad * 16;
+            float z[32];
+            tmem_load_32x32((i == 0 ? acc0 : acc1) + c, z);
+            tmem_wait_load(z);
+            if (preact != nullptr) {
+              write_half_block(z, Block<T, 16>(preact, a.N, row, cols - c, m, F, stage));
+              write_half_block(z + 16, Block<T, 16>(preact + F, a.N, row, cols - c, m, F, stage));
+            }
+            apply_act<16>(a.act, z);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) g[i] *= u[i];
-          write_block<true>(g, Block<T>(out, F, row, cols - c, m, F, stage));
+            for (int j = 0; j < 16; ++j) z[j] *= z[16 + j];
+            write_half_block(z, Block<T, 16>(out, F, row, cols - c, m, F, stage));
+          }
         } else {
           const int parts = two(tile) ? 2 : 1;
           for (int i = 0; i < parts; ++i) {
@@ -546,7 +592,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
               }
               if (preact != nullptr)
                 write_block<true>(z, Block<T>(preact, a.N, row, cols - c, m, a.N, stage));
-              apply_act(a.act, z);
+              apply_act<32>(a.act, z);
               if (residual != nullptr)
                 add_block(z, Block<T>(residual, a.N, row, cols - c, m, a.N, stage));
               write_block<true>(z, Block<T>(out, a.N, row, cols - c, m, a.N, stage));
