@@ -8,20 +8,21 @@
 // which goes in steps of 16: a segment costs its own rows rounded up to 16,
 // not to 128, and a single row costs one 16-column product.
 //
-// A pair of blocks (two SMs, cta_group::2) computes 512 x (up to 256) outputs:
-// four A tiles of 128 rows, two in each block, against one B tile of which each
-// block holds half the columns.  Gated: a block's two A tiles are the gate and
-// the up rows of the same 128 features, so that the activation and the product
-// happen in registers; else the pair's tiles are consecutive.  The accumulators
-// take all 512 columns of tensor memory, or, up to 128 columns wide, half of
-// them, and then the epilogue of one tile overlaps the products of the next.
+// A pair of blocks (two SMs, cta_group::2) computes 256 or 512 x (up to 256)
+// outputs: one or two A tiles of 128 rows in each block against one B tile of
+// which each block holds half the columns.  Gated: an A tile holds 16 gate rows
+// and the 16 up rows of the same features in turns, so that both of an output meet
+// in one thread's registers.  Tensor memory (512 columns) holds two accumulator
+// sets, and then the epilogue of one tile overlaps the products of the next, but
+// only one set of two A tiles by more than 128 columns.
 //   warps 0-7  epilogue: tensor memory -> registers -> shared -> rows
-//   warp 8     TMA producer: 64-deep slices into kStages stages of 48 KB
+//   warp 8     TMA producer: 64-deep slices into a ring of 192 KB
 //   warp 9     tcgen05.mma issue (first block), tensor memory allocation
 //   warp 10    d_weight: clears what a slice holds beyond the expert's rows
-// The pair shape is what shared memory and L2 bandwidth ask for: a 64-deep
-// slice feeds 1024 cycles of products with 48 KB per SM, where a single block's
-// 256 x 256 tile reads 64 KB, and its operands a third more of shared memory.
+// What bounds it: a slice of two A tiles by 256 columns is 1024 cycles of
+// products, for which a block loads 48 KB and tcgen05 reads 64 KB of shared
+// memory: 112 of 128 bytes a cycle.  One A tile loads 64 KB for the same work; a
+// block on its own, without the pair, 64 KB, and reads 96.
 // The grid is persistent; tiles are numbered expert by expert, the row blocks
 // of one weight tile next to each other so that they share it in L2.
 #pragma once
@@ -38,7 +39,8 @@ constexpr int kMaxN = 256;     // columns of one accumulator
 constexpr int kSlice = 64;     // contraction depth of one stage: 128 bytes
 constexpr int kTileABytes = 128 * kSlice * 2;
 constexpr int kTileBBytes = kMaxN / 2 * kSlice * 2;
-constexpr int kRingBytes = 192 * 1024;  // stages
+constexpr int kRingBytes = 192 * 1024;
+constexpr int kMaxStages = kRingBytes / (kTileABytes + kTileBBytes);
 constexpr int kBoxRows = 32;   // rows of the small TMA box of a k-contiguous B; the large: 128
 constexpr int kEpiWarps = 8;
 constexpr int kProductThreads = (kEpiWarps + 3) * 32;
@@ -51,6 +53,7 @@ struct ProductArgs {
   int64_t K, N;  // in_size and out_size of the weight [E, N, K]
   int E;
   int act;
+  int a_tiles;  // d_weight: A tiles per block
   const void* bias;
   const void* residual;
   void* out;
@@ -74,20 +77,40 @@ struct Tile {
 };
 
 // Row blocks of a segment: as few as fit, of even size (a multiple of 16).
-__device__ __forceinline__ int row_blocks(int rows) { return (rows + kMaxN - 1) / kMaxN; }
+__device__ __forceinline__ int row_blocks(int rows, int most) { return (rows + most - 1) / most; }
 __device__ __forceinline__ int block_rows(int rows, int blocks) {
   return ((rows + blocks - 1) / blocks + 15) / 16 * 16;
 }
 
-// Output features of one A tile of the pair, and of the pair's kMt A tiles.
+// Output features of one A tile of the pair.
 template <int kUse>
 __host__ __device__ constexpr int m_unit() { return kUse == kGated ? 128 : 256; }
-template <int kUse, int kMt>
-__host__ __device__ constexpr int m_step() { return m_unit<kUse>() * kMt; }
 
-template <int kUse, int kMt>
+// How a product over ragged rows is cut: A tiles per block, most columns.  The
+// choice weighs, for the rows there are, full waves of tiles against the cost of
+// a tile; `tiles` counts the column blocks, each with m_size / (a_tiles * unit)
+// tiles.  Cycles, from measured slices and epilogues: a slice is bound by the
+// products (2 per column and A tile), by shared memory (the bytes loaded and read
+// at 128 a cycle), or by L2 (48 bytes a cycle); an epilogue of 700 per 64 columns and
+// A tile is exposed where one accumulator set fills tensor memory.
+constexpr int kCaps = 9;  // most columns: 256, 240, ..., 128
+__device__ __forceinline__ int cap_of(int i) { return kMaxN - 16 * i; }
+
+__device__ __forceinline__ float plan_cost(int a_tiles, int cap, int blocks, int m_size, int unit,
+                                           int slices, int pairs) {
+  const int m_blocks = (m_size + a_tiles * unit - 1) / (a_tiles * unit);
+  const float waves = static_cast<float>((static_cast<int64_t>(blocks) * m_blocks + pairs - 1) / pairs);
+  const float loaded = a_tiles * 16384.f + cap * 64.f;
+  const float read = a_tiles * (16384.f + cap * 64.f);
+  const float slice = fmaxf(2.f * a_tiles * cap, fmaxf((loaded + read) / 128.f, loaded / 48.f));
+  const float products = slices * slice, epilogue = 700.f * a_tiles * ((cap + 63) / 64);
+  const bool overlapped = a_tiles == 1 || cap <= kMaxN / 2;
+  return waves * (products + (overlapped ? fmaxf(0.f, epilogue - products) + 500.f : epilogue + 2000.f));
+}
+
+template <int kUse>
 __device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const int* first, int t,
-                                          int m_blocks, int n_blocks) {
+                                          int m_step, int m_blocks, int n_blocks, int cap) {
   Tile r;
   if (kUse == kWeightGrad) {
     const int per = m_blocks * n_blocks;
@@ -96,7 +119,7 @@ __device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const 
     const Segment s = segments[r.e];
     r.lo = s.lo;
     r.rows = s.hi - s.lo;
-    r.m0 = local / n_blocks * m_step<kUse, kMt>();
+    r.m0 = local / n_blocks * m_step;
     r.n0 = local % n_blocks * kMaxN;
     return r;
   }
@@ -109,12 +132,12 @@ __device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const 
   r.e = lo;
   const Segment s = segments[lo];
   const int rows = s.hi - s.lo;
-  const int blocks = row_blocks(rows), step = block_rows(rows, blocks);
+  const int blocks = row_blocks(rows, cap), step = block_rows(rows, blocks);
   const int local = t - first[lo];
   const int b = local % blocks;
   r.lo = s.lo + b * step;
   r.rows = min(step, rows - b * step);
-  r.m0 = local / blocks * m_step<kUse, kMt>();
+  r.m0 = local / blocks * m_step;
   r.n0 = 0;
   return r;
 }
@@ -221,14 +244,17 @@ __device__ __forceinline__ void write_half_block(const float* v, const Block<T, 
   }
 }
 
-// v += the block (transposed); what lies outside the matrix counts as zero.
+// v += the block (transposed), in two steps, as its loads take long; what lies
+// outside the matrix counts as zero.
 template <typename T>
-__device__ __forceinline__ void add_block(float (&v)[32], const Block<T>& b) {
-  uint4 x[4];
+__device__ __forceinline__ void load_block(uint4 (&x)[4], const Block<T>& b) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     x[j] = 8 * j < b.rows ? *reinterpret_cast<const uint4*>(b.at + j * b.step)
                           : make_uint4(0, 0, 0, 0);
+}
+template <typename T>
+__device__ __forceinline__ void add_block(float (&v)[32], const uint4 (&x)[4], const Block<T>& b) {
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < 4; ++j) shared_store16(b.line + j * 512, x[j]);
@@ -247,27 +273,27 @@ __device__ __forceinline__ void add_block(float (&v)[32], const Block<T>& b) {
 }
 
 // map_a, map_b: the operands as TMA tiles of 64 contiguous values (128 bytes,
-// 128-byte swizzle) by 128 (forward A), 64 (MN-major) or kBoxRows rows.
-template <typename T, int kUse, int kMt>
+// 128-byte swizzle) by 128 (forward A), 64 (MN-major) or kBoxRows rows; map_b_large
+// by 128.  map_a of the gated product: make_gated_map.
+template <typename T, int kUse>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 k_expert_product(const __grid_constant__ CUtensorMap map_a,
                  const __grid_constant__ CUtensorMap map_b,
                  const __grid_constant__ CUtensorMap map_b_large, const ProductArgs a) {
-  constexpr int kStageBytes = kMt * kTileABytes + kTileBBytes;
-  constexpr int kStages = kRingBytes / kStageBytes;
   constexpr bool kBf16 = sizeof(T) == 2 && !__is_same(T, __half);
   constexpr bool kAMn = kUse == kRowsGrad || kUse == kWeightGrad;
   constexpr bool kBMn = kUse == kWeightGrad;
+  constexpr int kUnit = m_unit<kUse>();
   extern __shared__ uint8_t smem_raw[];
   // s_full, s_free and s_peer are used in the pair's first block only.
-  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_done[2], s_free[2],
-      s_peer[kStages], s_tail[kStages];
+  __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_done[2], s_free[2],
+      s_peer[kMaxStages], s_tail[kMaxStages];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_gave_up, s_scan[32];
+  __shared__ int s_gave_up, s_scan[32], s_blocks[kCaps], s_plan;
 
   uint8_t* stages = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* staging = stages + kStages * kStageBytes;
+  uint8_t* staging = stages + kRingBytes;
   Segment* segments = reinterpret_cast<Segment*>(staging + kStagingBytes);
   int* first = reinterpret_cast<int*>(segments + a.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -275,7 +301,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(smem_addr(&s_full[i]), 1);
       mbar_init(smem_addr(&s_empty[i]), 1);
       mbar_init(smem_addr(&s_peer[i]), 1);
@@ -291,45 +317,110 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     tma_prefetch_map(&map_b);
     if (!kBMn) tma_prefetch_map(&map_b_large);
   }
+  if (threadIdx.x < kCaps) s_blocks[threadIdx.x] = 0;
   if (warp == kEpiWarps + 1) tmem_alloc(smem_addr(&s_tmem), 512);
   pdl_wait();
+  __syncthreads();
 
-  // Tiles of each expert, and the sum before it.
   const int F = static_cast<int>(a.N / 2);
   const int m_size = static_cast<int>(kUse == kForward ? a.N : kUse == kGated ? F
                                       : kUse == kRowsGrad ? a.K : a.N);
-  const int m_blocks = (m_size + m_step<kUse, kMt>() - 1) / m_step<kUse, kMt>();
   const int n_blocks = static_cast<int>((a.K + kMaxN - 1) / kMaxN);  // d_weight
-  int total = 0;
+  const int k_size = static_cast<int>(kUse == kRowsGrad ? a.N : a.K);
+
+  // The experts' rows, and in how many blocks of each size they are cut.
   bool bad = false;
   for (int e0 = 0; e0 < a.E; e0 += kProductThreads) {
     const int e = e0 + threadIdx.x;
-    int n = 0;
+    int rows = 0;
     if (e < a.E) {
       bool b;
       const Segment s = segment(a.offset, e, a.num_rows, &b);
       bad |= b;
       segments[e] = s;
-      n = row_blocks(s.hi - s.lo) * m_blocks;
+      rows = s.hi - s.lo;
     }
-    int part;
-    const int before = block_exclusive_sum(n, s_scan, &part);
-    if (e < a.E) first[e] = total + before;
-    total += part;
+    if (kUse != kWeightGrad && __any_sync(kFullMask, rows > 0)) {
+#pragma unroll
+      for (int i = 0; i < kCaps; ++i) {
+        const int n = __reduce_add_sync(kFullMask, row_blocks(rows, cap_of(i)));
+        if (lane == 0) atomicAdd(&s_blocks[i], n);
+      }
+    }
   }
-  if (threadIdx.x == 0) first[a.E] = total;
-  if (kUse == kWeightGrad) total = a.E * m_blocks * n_blocks;
   if (a.status != nullptr && blockIdx.x == 0 && bad)
     atomicOr(a.status, MOE_FLAG_OFFSET_OUT_OF_RANGE);
+  __syncthreads();
+  int a_tiles = a.a_tiles, cap = kMaxN;
+  if (kUse != kWeightGrad) {
+    if (warp == 0) {
+      float cost = INFINITY;
+      if (lane < 2 * kCaps)
+        cost = plan_cost(2 - lane / kCaps, cap_of(lane % kCaps), s_blocks[lane % kCaps], m_size, kUnit,
+                         (k_size + kSlice - 1) / kSlice, pairs);
+      float best = cost;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) best = fminf(best, __shfl_xor_sync(kFullMask, best, d));
+      const unsigned at = __ballot_sync(kFullMask, cost == best);
+      if (lane == 0) s_plan = __ffs(at) - 1;
+    }
+    __syncthreads();
+    a_tiles = 2 - s_plan / kCaps;
+    cap = cap_of(s_plan % kCaps);
+#ifdef FORCE_MT
+    a_tiles = FORCE_MT;
+    cap = FORCE_CAP;
+#endif
+  }
+  const int m_step = a_tiles * kUnit;
+  const int m_blocks = (m_size + m_step - 1) / m_step;
+  // Tiles of each expert, and the sum before it.
+  int total = 0;
+  if (kUse == kWeightGrad) {
+    total = a.E * m_blocks * n_blocks;
+  } else {
+    for (int e0 = 0; e0 < a.E; e0 += kProductThreads) {
+      const int e = e0 + threadIdx.x;
+      const int n = e < a.E ? row_blocks(segments[e].hi - segments[e].lo, cap) * m_blocks : 0;
+      int part;
+      const int before = block_exclusive_sum(n, s_scan, &part);
+      if (e < a.E) first[e] = total + before;
+      total += part;
+    }
+    if (threadIdx.x == 0) first[a.E] = total;
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both blocks' barriers exist before either's loads or arrivals
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* gave_up = &s_gave_up;
+  const int stage_bytes = a_tiles * kTileABytes + kTileBBytes;
+  const int n_stages = a_tiles == 1 ? kMaxStages : kRingBytes / (2 * kTileABytes + kTileBBytes);
 
+  // A place in the ring of stages: stage and parity of the pass through them.
+  struct Ring {
+    int at = 0;
+    uint32_t pass = 0;
+    __device__ __forceinline__ void advance(int n) {
+      if (++at == n) at = 0, pass ^= 1;
+    }
+  };
+  // After a wait gave up: what was issued last at each stage is given the time of
+  // one wait to be used up, so that nothing is in flight when the block ends.
+  auto drain = [&](Ring r, uint32_t issued) {
+    const unsigned long long t0 = now_ns();
+    for (int i = 0; i < n_stages && static_cast<uint32_t>(i) < issued; ++i) {
+      if (r.at == 0) r.at = n_stages, r.pass ^= 1;
+      --r.at;
+      while (!mbar_try(smem_addr(&s_empty[r.at]), r.pass) && now_ns() - t0 < kWaitNs) {
+      }
+    }
+  };
+  auto tile_at = [&](int t) {
+    return find_tile<kUse>(a.E, segments, first, t, m_step, m_blocks, n_blocks, cap);
+  };
   // Slices of the contraction (d_weight: of the expert's rows).
-  const int k_size = static_cast<int>(kUse == kRowsGrad ? a.N : a.K);
   auto slices = [&](const Tile& t) {
     return ((kUse == kWeightGrad ? t.rows : k_size) + kSlice - 1) / kSlice;
   };
@@ -339,11 +430,9 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     return kUse == kWeightGrad ? min(kMaxN, static_cast<int>(a.K) - t.n0) : t.rows;
   };
   auto mma_n = [](int cols) { return (cols + 15) / 16 * 16; };
-  auto two = [&](const Tile& t) { return kMt == 2 && t.m0 + m_unit<kUse>() < m_size; };
+  auto two = [&](const Tile& t) { return a_tiles == 2 && t.m0 + kUnit < m_size; };
   // First feature of the block's i-th A tile.
-  auto feature = [&](const Tile& t, int i) {
-    return t.m0 + i * m_unit<kUse>() + rank * (m_unit<kUse>() / 2);
-  };
+  auto feature = [&](const Tile& t, int i) { return t.m0 + i * kUnit + rank * (kUnit / 2); };
   // Whether slice s of a d_weight tile runs past the expert's rows.
   auto is_tail = [&](const Tile& t, int s) {
     return kUse == kWeightGrad && t.rows - s * kSlice < kSlice;
@@ -352,54 +441,54 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   // expert or to none and may be infinite or NaN, so it is overwritten in both
   // operands rather than multiplied by zeros.
   auto clear_tail = [&](int st, int left) {
-    constexpr int kBoxes = kStageBytes / (kTileABytes / 2);  // 64 values x 64 rows each
+    const int boxes = stage_bytes / (kTileABytes / 2);  // 64 values x 64 rows each
     const int rows = (left + 15) / 16 * 16 - left;
-    for (int i = lane; i < rows * kBoxes * 8; i += 32) {
-      const int box = i / 8 % kBoxes, r = left + i / 8 / kBoxes;
-      *reinterpret_cast<uint4*>(stages + st * kStageBytes + box * (kTileABytes / 2) + r * 128 +
-                                (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-    }
+    for (int box = 0; box < boxes; ++box)
+      for (int i = lane; i < rows * 8; i += 32)
+        *reinterpret_cast<uint4*>(stages + st * stage_bytes + box * (kTileABytes / 2) +
+                                  (left + i / 8) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
     fence_async_shared();
     __syncwarp();
   };
-  // Tensor memory of a tile: half of it in turn, or, with two A tiles of more
-  // than half the columns, all of it.
-  auto narrow = [](int cols) { return kMt == 1 || cols <= kMaxN / 2; };
+  // Whether a tile's accumulators take half of tensor memory, the halves in turn;
+  // else all of it.
+  auto narrow = [&](int cols) { return a_tiles == 1 || cols <= kMaxN / 2; };
 
   if (warp == kEpiWarps) {
-    if (lane == 0) {  // one lane alone: a warp-wide wait per slice costs a quarter of the rate
-      uint32_t step = 0;
+    if (elect_one()) {  // one lane alone: a warp-wide wait per slice costs a quarter of the rate
+      Ring ring;
+      uint32_t issued = 0;
       bool ok = true;
+      const uint32_t full0 = cluster_addr(smem_addr(&s_full[0]), 0);  // the first block's
       for (int t = pair; t < total && ok; t += pairs) {
-        const Tile tile = find_tile<kUse, kMt>(a.E, segments, first, t, m_blocks, n_blocks);
+        const Tile tile = tile_at(t);
         const int n_slices = slices(tile), half_n = mma_n(columns(tile)) / 2;
-        const int a_tiles = two(tile) ? 2 : 1;
+        const int parts = two(tile) ? 2 : 1;
         const bool large = !kBMn && half_n > 64;
         const int b_boxes = kBMn ? (half_n + 63) / 64
                             : large ? 1 : (half_n + kBoxRows - 1) / kBoxRows;
         const int box_rows = kBMn ? 64 : large ? 128 : kBoxRows;
-        const uint32_t bytes = a_tiles * kTileABytes + b_boxes * box_rows * kSlice * 2;
-        for (int s = 0; s < n_slices; ++s, ++step) {
-          const int st = step % kStages;
-          if (!mbar_wait(smem_addr(&s_empty[st]), (step / kStages & 1) ^ 1, gave_up)) {
+        const uint32_t bytes = parts * kTileABytes + b_boxes * box_rows * kSlice * 2;
+        for (int s = 0; s < n_slices; ++s, ++issued) {
+          const int st = ring.at;
+          if (!mbar_wait(smem_addr(&s_empty[st]), ring.pass ^ 1, gave_up)) {
             ok = false;
             break;
           }
+          ring.advance(n_stages);
           // Both blocks' loads report to the first block's barrier; those of a
           // tail slice to their own block's, where it is cleared first.
-          uint32_t full = smem_addr(&s_full[st]);
+          uint32_t full = full0 + st * 8;
           if (is_tail(tile, s)) {
             full = smem_addr(&s_tail[st]);
             mbar_expect(full, bytes);
           } else if (rank == 0) {
-            mbar_expect(full, 2 * bytes);
-          } else {
-            full = cluster_addr(full, 0);
+            mbar_expect(smem_addr(&s_full[st]), 2 * bytes);
           }
-          const uint32_t sa = smem_addr(stages + st * kStageBytes);
-          const uint32_t sb = sa + kMt * kTileABytes;
+          const uint32_t sa = smem_addr(stages + st * stage_bytes);
+          const uint32_t sb = sa + a_tiles * kTileABytes;
           const int k = s * kSlice;
-          for (int i = 0; i < a_tiles; ++i) {
+          for (int i = 0; i < parts; ++i) {
             const int m = feature(tile, i);
             const uint32_t dst = sa + i * kTileABytes;
             if (kUse == kGated) {
@@ -430,47 +519,38 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           }
         }
       }
-      // Nothing of this block may still be in flight when it ends.  After an
-      // ordinary run every load was seen; after a wait gave up, the loads are
-      // given the time of one wait to be used.
-      if (*gave_up != 0) {
-        const unsigned long long t0 = now_ns();
-        for (uint32_t i = 1; i <= kStages && i <= step; ++i) {
-          const uint32_t last = step - i;  // the newest load of its stage
-          while (!mbar_try(smem_addr(&s_empty[last % kStages]), last / kStages & 1) &&
-                 now_ns() - t0 < kWaitNs) {
-          }
-        }
-      }
+      if (*gave_up != 0) drain(ring, issued);
     }
     __syncwarp();
   } else if (warp == kEpiWarps + 1) {
     if (rank == 0 && elect_one()) {
-      uint32_t step = 0, used[2] = {0, 0};
+      Ring ring;
+      uint32_t issued = 0, used0 = 0, used1 = 0;  // uses of the accumulator halves
       int next = 0;
       bool ok = true;
       for (int t = pair; t < total && ok; t += pairs) {
-        const Tile tile = find_tile<kUse, kMt>(a.E, segments, first, t, m_blocks, n_blocks);
+        const Tile tile = tile_at(t);
         const int n_slices = slices(tile);
         if (n_slices == 0) continue;
-        const int cols = columns(tile), n = mma_n(cols);
+        const int cols = columns(tile);
         const bool both = two(tile), half = narrow(cols);
-        const uint32_t idesc = instr_desc(kBf16, kAMn, kBMn, 256, n);
+        const uint32_t idesc = instr_desc(kBf16, kAMn, kBMn, 256, mma_n(cols));
         const int buf = half ? next : 0;
         next = half ? next ^ 1 : 0;
         const uint32_t acc0 = tmem + buf * kMaxN, acc1 = acc0 + (half ? kMaxN / 2 : kMaxN);
-        if (!mbar_wait(smem_addr(&s_free[buf]), (used[buf]++ & 1) ^ 1, gave_up)) break;
-        if (!half && !mbar_wait(smem_addr(&s_free[1]), (used[1]++ & 1) ^ 1, gave_up)) break;
+        if ((buf == 0 || !half) && !mbar_wait(smem_addr(&s_free[0]), (used0++ & 1) ^ 1, gave_up)) break;
+        if ((buf == 1 || !half) && !mbar_wait(smem_addr(&s_free[1]), (used1++ & 1) ^ 1, gave_up)) break;
         tc_fence_after();
-        for (int s = 0; s < n_slices; ++s, ++step) {
-          const int st = step % kStages;
-          if (!mbar_wait(smem_addr(&s_full[st]), step / kStages & 1, gave_up)) {
+        for (int s = 0; s < n_slices; ++s, ++issued) {
+          const int st = ring.at;
+          if (!mbar_wait(smem_addr(&s_full[st]), ring.pass, gave_up)) {
             ok = false;
             break;
           }
+          ring.advance(n_stages);
           tc_fence_after();
-          const uint32_t pa = smem_addr(stages + st * kStageBytes);
-          const uint32_t pb = pa + kMt * kTileABytes;
+          const uint32_t pa = smem_addr(stages + st * stage_bytes);
+          const uint32_t pb = pa + a_tiles * kTileABytes;
           constexpr uint32_t kStepA = kAMn ? 2048 : 32, kStepB = kBMn ? 2048 : 32;
           const int depth = is_tail(tile, s) ? (tile.rows - s * kSlice + 15) / 16 : kSlice / 16;
           for (int i = 0; i < depth; ++i) {
@@ -486,15 +566,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
         }
       }
       // The products are over before the memory they read and write is given up.
-      if (*gave_up != 0) {
-        const unsigned long long t0 = now_ns();
-        for (uint32_t i = 1; i <= kStages && i <= step; ++i) {
-          const uint32_t last = step - i;
-          while (!mbar_try(smem_addr(&s_empty[last % kStages]), last / kStages & 1) &&
-                 now_ns() - t0 < kWaitNs) {
-          }
-        }
-      }
+      if (*gave_up != 0) drain(ring, issued);
     }
     __syncwarp();
   } else if (warp == kEpiWarps + 2) {
@@ -504,10 +576,10 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       uint32_t step = 0;
       uint32_t tails = 0;  // bit st: parity of the stage's tail slices so far
       for (int t = pair; t < total; t += pairs) {
-        const Tile tile = find_tile<kUse, kMt>(a.E, segments, first, t, m_blocks, n_blocks);
+        const Tile tile = tile_at(t);
         const int n_slices = slices(tile);
         if (n_slices > 0 && is_tail(tile, n_slices - 1)) {
-          const int st = (step + n_slices - 1) % kStages;
+          const int st = static_cast<int>((step + n_slices - 1) % n_stages);
           const uint32_t parity = tails >> st & 1;
           tails ^= 1u << st;
           if (!warp_wait(smem_addr(&s_tail[st]), parity, gave_up)) break;
@@ -528,84 +600,85 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     const uint32_t stage = smem_addr(staging + warp * kStagingWarpBytes);
     T* out = static_cast<T*>(a.out);
     T* preact = static_cast<T*>(a.preact);
-    T* residual = static_cast<T*>(const_cast<void*>(a.residual));
-    uint32_t fin[2] = {0, 0};
+    T* residual = kUse == kForward ? static_cast<T*>(const_cast<void*>(a.residual)) : nullptr;
+    uint32_t fin0 = 0, fin1 = 0;
     int next = 0;
     const uint32_t free0 = cluster_addr(smem_addr(&s_free[0]), 0);
     const uint32_t free1 = cluster_addr(smem_addr(&s_free[1]), 0);
     for (int t = pair; t < total; t += pairs) {
-      const Tile tile = find_tile<kUse, kMt>(a.E, segments, first, t, m_blocks, n_blocks);
+      const Tile tile = tile_at(t);
       const int cols = columns(tile);
       const bool any = slices(tile) > 0, half = narrow(cols);
+      const int parts = two(tile) ? 2 : 1;
+      // The warp's blocks: columns c + [0, 32) of A tile i, unit u = (c, i).
+      const int c0 = warp / 4 * 32;
+      const int units = c0 < cols ? (cols - c0 + 63) / 64 * parts : 0;
+      auto residual_block = [&](int u) {
+        const int c = c0 + u / parts * 64;
+        return Block<T>(residual, a.N, tile.lo + c, cols - c, feature(tile, u % parts) + quad * 32,
+                        a.N, stage);
+      };
+      uint4 ahead[4];  // the next unit's residual
+      if (residual != nullptr && units > 0) load_block(ahead, residual_block(0));
       int buf = 0;
       if (any) {
         buf = half ? next : 0;
         next = half ? next ^ 1 : 0;
-        if (!warp_wait(smem_addr(&s_done[buf]), fin[buf]++ & 1, gave_up)) break;
+        const uint32_t parity = (buf == 0 ? fin0++ : fin1++) & 1;
+        if (!warp_wait(smem_addr(&s_done[buf]), parity, gave_up)) break;
         tc_fence_after();
       }
       const uint32_t acc0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kMaxN;
       const uint32_t acc1 = acc0 + (half ? kMaxN / 2 : kMaxN);
-      for (int c = warp / 4 * 32; c < cols; c += 64) {
-        // The block: features m + [0, 32) of rows tile.lo + c + [0, 32).
+      for (int u = 0; u < units; ++u) {
+        const int c = c0 + u / parts * 64, i = u % parts;
         const int64_t row = tile.lo + c;
+        const int64_t m = feature(tile, i) + quad * (kUse == kGated ? 16 : 32);
+        float z[32];
+        if (any) {
+          tmem_load_32x32((i == 0 ? acc0 : acc1) + c, z);
+          tmem_wait_load(z);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[j] = 0.f;
+        }
         if (kUse == kGated) {
           // The warp's 32 lanes: 16 gate rows, then the up rows of the same
-          // features; a thread holds both of a value in z[i] and z[16 + i].
-          const int parts = two(tile) ? 2 : 1;
-          for (int i = 0; i < parts; ++i) {
-            const int64_t m = feature(tile, i) + quad * 16;
-            float z[32];
-            tmem_load_32x32((i == 0 ? acc0 : acc1) + c, z);
-            tmem_wait_load(z);
-            if (preact != nullptr) {
-              write_half_block(z, Block<T, 16>(preact, a.N, row, cols - c, m, F, stage));
-              write_half_block(z + 16, Block<T, 16>(preact + F, a.N, row, cols - c, m, F, stage));
-            }
-            apply_act<16>(a.act, z);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) z[j] *= z[16 + j];
-            write_half_block(z, Block<T, 16>(out, F, row, cols - c, m, F, stage));
+          // features; a thread holds both of a value in z[j] and z[16 + j].
+          if (preact != nullptr) {
+            write_half_block(z, Block<T, 16>(preact, a.N, row, cols - c, m, F, stage));
+            write_half_block(z + 16, Block<T, 16>(preact + F, a.N, row, cols - c, m, F, stage));
           }
+          apply_act<16>(a.act, z);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) z[j] *= z[16 + j];
+          write_half_block(z, Block<T, 16>(out, F, row, cols - c, m, F, stage));
+        } else if (kUse == kForward) {
+          if (a.bias != nullptr) {
+            const T* bias = static_cast<const T*>(a.bias) + static_cast<int64_t>(tile.e) * a.N;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // z[16 h + 4 i + 2 s + b]: feature 16 h + 8 s + g
+              const int64_t f = m + j * 8 + (lane >> 2);
+              const float x = f < a.N ? to_f(bias[f]) : 0.f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) z[j / 2 * 16 + k / 2 * 4 + j % 2 * 2 + k % 2] += x;
+            }
+          }
+          if (preact != nullptr)
+            write_block<true>(z, Block<T>(preact, a.N, row, cols - c, m, a.N, stage));
+          apply_act<32>(a.act, z);
+          if (residual != nullptr) {
+            add_block(z, ahead, residual_block(u));
+            if (u + 1 < units) load_block(ahead, residual_block(u + 1));
+          }
+          write_block<true>(z, Block<T>(out, a.N, row, cols - c, m, a.N, stage));
+        } else if (kUse == kRowsGrad) {
+          write_block<true>(z, Block<T>(out, a.K, row, cols - c, m, a.K, stage));
         } else {
-          const int parts = two(tile) ? 2 : 1;
-          for (int i = 0; i < parts; ++i) {
-            const int64_t m = feature(tile, i) + quad * 32;
-            float z[32];
-            if (any) {
-              tmem_load_32x32((i == 0 ? acc0 : acc1) + c, z);
-              tmem_wait_load(z);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) z[j] = 0.f;
-            }
-            if (kUse == kForward) {
-              if (a.bias != nullptr) {
-                const T* bias = static_cast<const T*>(a.bias) + static_cast<int64_t>(tile.e) * a.N;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {  // z[16 h + 4 i + 2 s + b]: feature 16 h + 8 s + g
-                  const int64_t f = m + j * 8 + (lane >> 2);
-                  const float x = f < a.N ? to_f(bias[f]) : 0.f;
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) z[j / 2 * 16 + k / 2 * 4 + j % 2 * 2 + k % 2] += x;
-                }
-              }
-              if (preact != nullptr)
-                write_block<true>(z, Block<T>(preact, a.N, row, cols - c, m, a.N, stage));
-              apply_act<32>(a.act, z);
-              if (residual != nullptr)
-                add_block(z, Block<T>(residual, a.N, row, cols - c, m, a.N, stage));
-              write_block<true>(z, Block<T>(out, a.N, row, cols - c, m, a.N, stage));
-            } else if (kUse == kRowsGrad) {
-              write_block<true>(z, Block<T>(out, a.K, row, cols - c, m, a.K, stage));
-            } else {
-              const int64_t left = a.N - m;
-              write_block<false>(
-                  z, Block<T>(out, a.K, static_cast<int64_t>(tile.e) * a.N + m,
-                              static_cast<int>(left < 32 ? (left < 0 ? 0 : left) : 32),
-                              tile.n0 + c, a.K, stage));
-            }
-          }
+          const int64_t left = a.N - m;
+          write_block<false>(z, Block<T>(out, a.K, static_cast<int64_t>(tile.e) * a.N + m,
+                                         static_cast<int>(left < 32 ? (left < 0 ? 0 : left) : 32),
+                                         tile.n0 + c, a.K, stage));
         }
       }
       if (any) {

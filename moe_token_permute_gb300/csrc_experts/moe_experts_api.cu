@@ -110,30 +110,18 @@ bool make_gated_map(CUtensorMap* map, const void* base, int64_t E, int64_t F, in
   return make_map_nd<T, 4>(map, base, {K, F, 2, E}, {K, F * K, 2 * F * K}, {64, 16, 2, 1});
 }
 
-#ifndef GATED_MT
-#define GATED_MT 1
-#endif
-#ifndef FWD_MT
-#define FWD_MT 1
-#endif
-#ifndef ROWS_MT
-#define ROWS_MT 1
-#endif
-#ifndef WGRAD_MT
-#define WGRAD_MT 1
-#endif
-// The most tiles a product may have.
-template <int kUse, int kMt>
-int64_t most_tiles(const ProductArgs& a) {
+// The most tiles a product may have with a_tiles A tiles per block.
+template <int kUse>
+int64_t most_tiles(const ProductArgs& a, int a_tiles) {
   const int64_t m = kUse == kForward || kUse == kWeightGrad ? a.N : kUse == kGated ? a.N / 2 : a.K;
   const int64_t columns = kUse == kWeightGrad
                               ? a.E * ceil_div(a.K, kMaxN)
-                              : a.num_rows / kMaxN + std::min<int64_t>(a.E, a.num_rows);
-  return ceil_div(m, m_step<kUse, kMt>()) * columns;
+                              : a.num_rows / (kMaxN / 2) + std::min<int64_t>(a.E, a.num_rows);
+  return ceil_div(m, a_tiles * m_unit<kUse>()) * columns;
 }
 
 // lhs: the weight, or dz for d_weight; rhs: the rows, or dz for d_rows.
-template <typename T, int kUse, int kMt>
+template <typename T, int kUse>
 cudaError_t launch_product(const ProductArgs& a, const void* lhs, const void* rhs, int sms,
                            cudaStream_t s) {
   CUtensorMap map_a, map_b, map_b_large;
@@ -154,9 +142,9 @@ cudaError_t launch_product(const ProductArgs& a, const void* lhs, const void* rh
          make_map<T>(&map_b_large, rhs, 0, a.num_rows, depth, 128);
   }
   if (!ok) return cudaErrorInvalidValue;
-  const int64_t tiles = most_tiles<kUse, kMt>(a);
+  const int64_t tiles = most_tiles<kUse>(a, 1);
   if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
-  return launch(k_expert_product<T, kUse, kMt>,
+  return launch(k_expert_product<T, kUse>,
                 dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, sms / 2))), kProductThreads,
                 product_smem(a.E), s, map_a, map_b, map_b_large, a);
 }
@@ -164,8 +152,8 @@ cudaError_t launch_product(const ProductArgs& a, const void* lhs, const void* rh
 template <typename T, int kUse>
 cudaError_t launch_forward(const ProductArgs& a, const void* weight, const void* rows, int sms,
                            cudaStream_t s) {
-  if (!decode_pays(a.num_rows, a.K, most_tiles<kUse, 2>(a), sms / 2))
-    return launch_product<T, kUse, kUse == kGated ? GATED_MT : FWD_MT>(a, weight, rows, sms, s);
+  if (!decode_pays(a.num_rows, a.K, most_tiles<kUse>(a, 2), sms / 2))
+    return launch_product<T, kUse>(a, weight, rows, sms, s);
   constexpr bool kGatedForm = kUse == kGated;
   // Tasks at most: every expert with rows has one group, and each further
   // kDecodeGroup rows one more.
@@ -217,12 +205,16 @@ cudaError_t product_gradients(const void* dz, const void* rows, const void* weig
   a.status = status;
   if (d_rows != nullptr && num_rows > 0) {
     a.out = d_rows;
-    const cudaError_t err = launch_product<T, kRowsGrad, ROWS_MT>(a, weight, dz, sms, s);
+    const cudaError_t err = launch_product<T, kRowsGrad>(a, weight, dz, sms, s);
     if (err != cudaSuccess) return err;
   }
   if (d_weight != nullptr) {
     a.out = d_weight;
-    return launch_product<T, kWeightGrad, WGRAD_MT>(a, dz, rows, sms, s);
+#ifndef WMT
+#define WMT 1
+#endif
+    a.a_tiles = WMT;
+    return launch_product<T, kWeightGrad>(a, dz, rows, sms, s);
   }
   return cudaSuccess;
 }
