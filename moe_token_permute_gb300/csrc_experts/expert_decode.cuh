@@ -73,9 +73,9 @@ constexpr int kDecodeMaxRows = 32;
 //   gated 128 x 2048 -> 768, 8 / 16 / 32 rows   14 / 17    21 / 19    29 / 27
 //   linear 128 x 768 -> 2048, 8 / 32 rows    24 / 11    57 / 17
 // A task costs about 0.7 us beside its loads, so it needs a long contraction;
-// of 2048 values it pays while the large tiles fill less than half the pairs.
+// of 2048 values it pays while the large tiles do not fill the pairs.
 inline bool decode_pays(int64_t rows, int64_t K, int64_t tiles, int64_t pairs) {
-  return rows <= kDecodeMaxRows && K % 64 == 0 && (K >= 4096 || (K >= 2048 && 2 * tiles <= pairs));
+  return rows <= kDecodeMaxRows && K % 64 == 0 && (K >= 4096 || (K >= 2048 && tiles <= pairs));
 }
 
 template <typename T>

@@ -8,23 +8,24 @@
 // which goes in steps of 16: a segment costs its own rows rounded up to 16,
 // not to 128, and a single row costs one 16-column product.
 //
-// A pair of blocks (two SMs, cta_group::2) computes 256 or 512 x (up to 256)
-// outputs: one or two A tiles of 128 rows in each block against one B tile of
-// which each block holds half the columns.  Gated: an A tile holds 16 gate rows
-// and the 16 up rows of the same features in turns, so that both of an output meet
-// in one thread's registers.  Tensor memory (512 columns) holds two accumulator
-// sets, and then the epilogue of one tile overlaps the products of the next, but
-// only one set of two A tiles by more than 128 columns.
+// A pair of blocks (two SMs, cta_group::2) computes 256 x (up to 256) outputs: an
+// A tile of 128 rows in each block against one B tile of which each block holds
+// half the columns.  Gated: an A tile holds 16 gate rows and the 16 up rows of the
+// same features in turns, so that both of an output meet in one thread's
+// registers.  Tensor memory (512 columns) holds two accumulators: the epilogue of
+// one tile overlaps the products of the next.
 //   warps 0-7  epilogue: tensor memory -> registers -> shared -> rows
-//   warp 8     TMA producer: 64-deep slices into a ring of 192 KB
+//   warp 8     TMA producer: 64-deep slices into a ring of 6 x 32 KB
 //   warp 9     tcgen05.mma issue (first block), tensor memory allocation
 //   warp 10    d_weight: clears what a slice holds beyond the expert's rows
-// What bounds it: a slice of two A tiles by 256 columns is 1024 cycles of
-// products, for which a block loads 48 KB and tcgen05 reads 64 KB of shared
-// memory: 112 of 128 bytes a cycle.  One A tile loads 64 KB for the same work; a
-// block on its own, without the pair, 64 KB, and reads 96.
-// The grid is persistent; tiles are numbered expert by expert, the row blocks
-// of one weight tile next to each other so that they share it in L2.
+// What bounds it: a slice of 256 columns is 512 cycles of products, for which a
+// block loads 32 KB into shared memory and tcgen05 reads 32 KB of it: 128 bytes a
+// cycle, all there is.  (A block on its own, without the pair, would need 160.
+// Two A tiles per block need 112, but fill tensor memory, and then every tile's
+// epilogue holds the products up: Qwen3-shaped training 5% slower, many experts of
+// 128 rows 1% faster.)  Large products run at the power limit: 1.87 PFLOP/s in
+// bursts of 1 ms, Mixtral-shaped gated T = 4096.
+// The grid is persistent; tiles are numbered expert by expert, in panels.
 #pragma once
 
 #include "expert_math.cuh"
@@ -39,8 +40,8 @@ constexpr int kMaxN = 256;     // columns of one accumulator
 constexpr int kSlice = 64;     // contraction depth of one stage: 128 bytes
 constexpr int kTileABytes = 128 * kSlice * 2;
 constexpr int kTileBBytes = kMaxN / 2 * kSlice * 2;
-constexpr int kRingBytes = 192 * 1024;
-constexpr int kMaxStages = kRingBytes / (kTileABytes + kTileBBytes);
+constexpr int kStageBytes = kTileABytes + kTileBBytes;
+constexpr int kStages = 6;
 constexpr int kBoxRows = 32;   // rows of the small TMA box of a k-contiguous B; the large: 128
 constexpr int kEpiWarps = 8;
 constexpr int kProductThreads = (kEpiWarps + 3) * 32;
@@ -53,7 +54,6 @@ struct ProductArgs {
   int64_t K, N;  // in_size and out_size of the weight [E, N, K]
   int E;
   int act;
-  int a_tiles;  // d_weight: A tiles per block
   const void* bias;
   const void* residual;
   void* out;
@@ -64,10 +64,10 @@ struct ProductArgs {
 // Dynamic shared memory: stages (1024-byte aligned), staging, then each
 // expert's rows and its first tile.
 inline size_t product_smem(int E) {
-  return 1024 + kRingBytes + kStagingBytes + static_cast<size_t>(E) * 12 + 4;
+  return 1024 + kStages * kStageBytes + kStagingBytes + static_cast<size_t>(E) * 12 + 4;
 }
 
-static_assert(1024 + kRingBytes + kStagingBytes + MOE_MAX_LOCAL_EXPERTS * 12 + 4 + 1024 <=
+static_assert(1024 + kStages * kStageBytes + kStagingBytes + MOE_MAX_LOCAL_EXPERTS * 12 + 4 + 1024 <=
                   227 * 1024,
               "shared memory of one block");
 
@@ -82,45 +82,52 @@ __device__ __forceinline__ int block_rows(int rows, int blocks) {
   return ((rows + blocks - 1) / blocks + 15) / 16 * 16;
 }
 
-// Output features of one A tile of the pair.
+// Output features of one tile.
 template <int kUse>
-__host__ __device__ constexpr int m_unit() { return kUse == kGated ? 128 : 256; }
+__host__ __device__ constexpr int m_step() { return kUse == kGated ? 128 : 256; }
 
-// How a product over ragged rows is cut: A tiles per block, most columns.  The
-// choice weighs, for the rows there are, full waves of tiles against the cost of
-// a tile; `tiles` counts the column blocks, each with m_size / (a_tiles * unit)
-// tiles.  Cycles, from measured slices and epilogues: a slice is bound by the
-// products (2 per column and A tile), by shared memory (the bytes loaded and read
-// at 128 a cycle), or by L2 (48 bytes a cycle); an epilogue of 700 per 64 columns and
-// A tile is exposed where one accumulator set fills tensor memory.
-constexpr int kCaps = 9;  // most columns: 256, 240, ..., 128
+// The most columns of a tile, chosen for the rows there are.  Six waves of tiles
+// and more are cut into 256.  Below, fewer columns can fill the waves better, but a
+// slice costs 256 + columns cycles (its traffic
+// in shared memory) whether or not the products need them, and a tile about 700 to
+// its first product.  Dense 4096 -> 4096: 500 rows 25 us in blocks of 128 and 31 of
+// 256, 8191 rows 238 and 166.
+constexpr int kCaps = 13;  // 256, 240, ..., 64
 __device__ __forceinline__ int cap_of(int i) { return kMaxN - 16 * i; }
+__device__ __forceinline__ float cap_cost(int blocks, int rows, int m_blocks, int slices, int pairs) {
+  const int64_t waves = (static_cast<int64_t>(blocks) * m_blocks + pairs - 1) / pairs;
+  const float columns = static_cast<float>(rows) / static_cast<float>(max(blocks, 1));
+  return static_cast<float>(waves) * (static_cast<float>(slices) * (256.f + columns) + 700.f);
+}
 
-__device__ __forceinline__ float plan_cost(int a_tiles, int cap, int blocks, int m_size, int unit,
-                                           int slices, int pairs) {
-  const int m_blocks = (m_size + a_tiles * unit - 1) / (a_tiles * unit);
-  const float waves = static_cast<float>((static_cast<int64_t>(blocks) * m_blocks + pairs - 1) / pairs);
-  const float loaded = a_tiles * 16384.f + cap * 64.f;
-  const float read = a_tiles * (16384.f + cap * 64.f);
-  const float slice = fmaxf(2.f * a_tiles * cap, fmaxf((loaded + read) / 128.f, loaded / 48.f));
-  const float products = slices * slice, epilogue = 700.f * a_tiles * ((cap + 63) / 64);
-  const bool overlapped = a_tiles == 1 || cap <= kMaxN / 2;
-  return waves * (products + (overlapped ? fmaxf(0.f, epilogue - products) + 500.f : epilogue + 2000.f));
+// Tile `local` of an expert's m_blocks x n_blocks, in panels of kPanel column
+// blocks, all of a panel's row blocks after one another: the tiles that run at the
+// same time make a square of about kPanel x 76 / kPanel, whose operands together
+// are small enough to be shared through L2.
+constexpr int kPanel = 8;
+__device__ __forceinline__ void place_in_panels(int local, int m_blocks, int n_blocks, int& m,
+                                                int& n) {
+  const int panel = local / (kPanel * m_blocks);
+  const int width = min(kPanel, n_blocks - panel * kPanel);
+  local -= panel * kPanel * m_blocks;
+  m = local / width;
+  n = panel * kPanel + local - m * width;
 }
 
 template <int kUse>
 __device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const int* first, int t,
-                                          int m_step, int m_blocks, int n_blocks, int cap) {
+                                          int m_blocks, int n_blocks, int cap) {
   Tile r;
   if (kUse == kWeightGrad) {
     const int per = m_blocks * n_blocks;
     r.e = t / per;
-    const int local = t - r.e * per;
     const Segment s = segments[r.e];
     r.lo = s.lo;
     r.rows = s.hi - s.lo;
-    r.m0 = local / n_blocks * m_step;
-    r.n0 = local % n_blocks * kMaxN;
+    int m, n;
+    place_in_panels(t - r.e * per, m_blocks, n_blocks, m, n);
+    r.m0 = m * m_step<kUse>();
+    r.n0 = n * kMaxN;
     return r;
   }
   int lo = 0, hi = E;  // first[lo] <= t < first[hi]
@@ -133,11 +140,11 @@ __device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const 
   const Segment s = segments[lo];
   const int rows = s.hi - s.lo;
   const int blocks = row_blocks(rows, cap), step = block_rows(rows, blocks);
-  const int local = t - first[lo];
-  const int b = local % blocks;
-  r.lo = s.lo + b * step;
-  r.rows = min(step, rows - b * step);
-  r.m0 = local / blocks * m_step;
+  int m, n;
+  place_in_panels(t - first[lo], m_blocks, blocks, m, n);
+  r.lo = s.lo + n * step;
+  r.rows = min(step, rows - n * step);
+  r.m0 = m * m_step<kUse>();
   r.n0 = 0;
   return r;
 }
@@ -202,7 +209,9 @@ __device__ __forceinline__ void shared_store16(uint32_t addr, uint4 v) {
 
 // v, as tmem_load_32x32 gives it, rounded and written to the block.
 // kTranspose: tensor memory lanes are the block's columns; else its rows.
-template <bool kTranspose, typename T>
+// kStream: the result is not read again soon and should not displace the operands
+// in L2.
+template <bool kTranspose, bool kStream = false, typename T>
 __device__ __forceinline__ void write_block(const float (&v)[32], const Block<T>& b) {
   uint32_t p[16];
 #pragma unroll
@@ -222,7 +231,11 @@ __device__ __forceinline__ void write_block(const float (&v)[32], const Block<T>
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint4 x = shared_load16(b.line + j * 512);
-    if (8 * j < b.rows) *reinterpret_cast<uint4*>(b.at + j * b.step) = x;
+    if (8 * j < b.rows) {
+      uint4* to = reinterpret_cast<uint4*>(b.at + j * b.step);
+      if (kStream) __stcs(to, x);
+      else *to = x;
+    }
   }
 }
 
@@ -283,17 +296,16 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   constexpr bool kBf16 = sizeof(T) == 2 && !__is_same(T, __half);
   constexpr bool kAMn = kUse == kRowsGrad || kUse == kWeightGrad;
   constexpr bool kBMn = kUse == kWeightGrad;
-  constexpr int kUnit = m_unit<kUse>();
   extern __shared__ uint8_t smem_raw[];
   // s_full, s_free and s_peer are used in the pair's first block only.
-  __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_done[2], s_free[2],
-      s_peer[kMaxStages], s_tail[kMaxStages];
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_done[2], s_free[2],
+      s_peer[kStages], s_tail[kStages];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_gave_up, s_scan[32], s_blocks[kCaps], s_plan;
+  __shared__ int s_gave_up, s_scan[32], s_blocks[kCaps + 1], s_cap;
 
   uint8_t* stages = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* staging = stages + kRingBytes;
+  uint8_t* staging = stages + kStages * kStageBytes;
   Segment* segments = reinterpret_cast<Segment*>(staging + kStagingBytes);
   int* first = reinterpret_cast<int*>(segments + a.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -301,7 +313,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kMaxStages; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_addr(&s_full[i]), 1);
       mbar_init(smem_addr(&s_empty[i]), 1);
       mbar_init(smem_addr(&s_peer[i]), 1);
@@ -317,7 +329,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     tma_prefetch_map(&map_b);
     if (!kBMn) tma_prefetch_map(&map_b_large);
   }
-  if (threadIdx.x < kCaps) s_blocks[threadIdx.x] = 0;
+  if (threadIdx.x <= kCaps) s_blocks[threadIdx.x] = 0;
   if (warp == kEpiWarps + 1) tmem_alloc(smem_addr(&s_tmem), 512);
   pdl_wait();
   __syncthreads();
@@ -328,7 +340,8 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   const int n_blocks = static_cast<int>((a.K + kMaxN - 1) / kMaxN);  // d_weight
   const int k_size = static_cast<int>(kUse == kRowsGrad ? a.N : a.K);
 
-  // The experts' rows, and in how many blocks of each size they are cut.
+  // The experts' rows, and in how many blocks of each size they are cut;
+  // s_blocks[kCaps]: all rows.
   bool bad = false;
   for (int e0 = 0; e0 < a.E; e0 += kProductThreads) {
     const int e = e0 + threadIdx.x;
@@ -346,34 +359,30 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
         const int n = __reduce_add_sync(kFullMask, row_blocks(rows, cap_of(i)));
         if (lane == 0) atomicAdd(&s_blocks[i], n);
       }
+      const int n = __reduce_add_sync(kFullMask, rows);
+      if (lane == 0) atomicAdd(&s_blocks[kCaps], n);
     }
   }
   if (a.status != nullptr && blockIdx.x == 0 && bad)
     atomicOr(a.status, MOE_FLAG_OFFSET_OUT_OF_RANGE);
   __syncthreads();
-  int a_tiles = a.a_tiles, cap = kMaxN;
+  const int m_blocks = (m_size + m_step<kUse>() - 1) / m_step<kUse>();
+  int cap = kMaxN;
   if (kUse != kWeightGrad) {
     if (warp == 0) {
       float cost = INFINITY;
-      if (lane < 2 * kCaps)
-        cost = plan_cost(2 - lane / kCaps, cap_of(lane % kCaps), s_blocks[lane % kCaps], m_size, kUnit,
-                         (k_size + kSlice - 1) / kSlice, pairs);
+      if (lane == 0 || (lane < kCaps && s_blocks[0] < (6 * pairs + m_blocks - 1) / m_blocks))
+        cost = cap_cost(s_blocks[lane], s_blocks[kCaps], m_blocks, (k_size + kSlice - 1) / kSlice,
+                        pairs);
       float best = cost;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) best = fminf(best, __shfl_xor_sync(kFullMask, best, d));
       const unsigned at = __ballot_sync(kFullMask, cost == best);
-      if (lane == 0) s_plan = __ffs(at) - 1;
+      if (lane == 0) s_cap = cap_of(__ffs(at) - 1);
     }
     __syncthreads();
-    a_tiles = 2 - s_plan / kCaps;
-    cap = cap_of(s_plan % kCaps);
-#ifdef FORCE_MT
-    a_tiles = FORCE_MT;
-    cap = FORCE_CAP;
-#endif
+    cap = s_cap;
   }
-  const int m_step = a_tiles * kUnit;
-  const int m_blocks = (m_size + m_step - 1) / m_step;
   // Tiles of each expert, and the sum before it.
   int total = 0;
   if (kUse == kWeightGrad) {
@@ -395,44 +404,40 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* gave_up = &s_gave_up;
-  const int stage_bytes = a_tiles * kTileABytes + kTileBBytes;
-  const int n_stages = a_tiles == 1 ? kMaxStages : kRingBytes / (2 * kTileABytes + kTileBBytes);
 
   // A place in the ring of stages: stage and parity of the pass through them.
   struct Ring {
     int at = 0;
     uint32_t pass = 0;
-    __device__ __forceinline__ void advance(int n) {
-      if (++at == n) at = 0, pass ^= 1;
+    __device__ __forceinline__ void advance() {
+      if (++at == kStages) at = 0, pass ^= 1;
     }
   };
   // After a wait gave up: what was issued last at each stage is given the time of
   // one wait to be used up, so that nothing is in flight when the block ends.
   auto drain = [&](Ring r, uint32_t issued) {
     const unsigned long long t0 = now_ns();
-    for (int i = 0; i < n_stages && static_cast<uint32_t>(i) < issued; ++i) {
-      if (r.at == 0) r.at = n_stages, r.pass ^= 1;
+    for (int i = 0; i < kStages && static_cast<uint32_t>(i) < issued; ++i) {
+      if (r.at == 0) r.at = kStages, r.pass ^= 1;
       --r.at;
       while (!mbar_try(smem_addr(&s_empty[r.at]), r.pass) && now_ns() - t0 < kWaitNs) {
       }
     }
   };
   auto tile_at = [&](int t) {
-    return find_tile<kUse>(a.E, segments, first, t, m_step, m_blocks, n_blocks, cap);
+    return find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks, cap);
   };
   // Slices of the contraction (d_weight: of the expert's rows).
   auto slices = [&](const Tile& t) {
     return ((kUse == kWeightGrad ? t.rows : k_size) + kSlice - 1) / kSlice;
   };
-  // Columns of the tile, those of the product (each block holds half of B), and
-  // whether the second A tiles hold anything.
+  // Columns of the tile, and those of the product (each block holds half of B).
   auto columns = [&](const Tile& t) {
     return kUse == kWeightGrad ? min(kMaxN, static_cast<int>(a.K) - t.n0) : t.rows;
   };
   auto mma_n = [](int cols) { return (cols + 15) / 16 * 16; };
-  auto two = [&](const Tile& t) { return a_tiles == 2 && t.m0 + kUnit < m_size; };
-  // First feature of the block's i-th A tile.
-  auto feature = [&](const Tile& t, int i) { return t.m0 + i * kUnit + rank * (kUnit / 2); };
+  // First feature of the block's A tile.
+  auto feature = [&](const Tile& t) { return t.m0 + rank * (m_step<kUse>() / 2); };
   // Whether slice s of a d_weight tile runs past the expert's rows.
   auto is_tail = [&](const Tile& t, int s) {
     return kUse == kWeightGrad && t.rows - s * kSlice < kSlice;
@@ -441,19 +446,15 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   // expert or to none and may be infinite or NaN, so it is overwritten in both
   // operands rather than multiplied by zeros.
   auto clear_tail = [&](int st, int left) {
-    const int boxes = stage_bytes / (kTileABytes / 2);  // 64 values x 64 rows each
+    constexpr int kBoxes = kStageBytes / (kTileABytes / 2);  // 64 values x 64 rows each
     const int rows = (left + 15) / 16 * 16 - left;
-    for (int box = 0; box < boxes; ++box)
+    for (int box = 0; box < kBoxes; ++box)
       for (int i = lane; i < rows * 8; i += 32)
-        *reinterpret_cast<uint4*>(stages + st * stage_bytes + box * (kTileABytes / 2) +
+        *reinterpret_cast<uint4*>(stages + st * kStageBytes + box * (kTileABytes / 2) +
                                   (left + i / 8) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
     fence_async_shared();
     __syncwarp();
   };
-  // Whether a tile's accumulators take half of tensor memory, the halves in turn;
-  // else all of it.
-  auto narrow = [&](int cols) { return a_tiles == 1 || cols <= kMaxN / 2; };
-
   if (warp == kEpiWarps) {
     if (elect_one()) {  // one lane alone: a warp-wide wait per slice costs a quarter of the rate
       Ring ring;
@@ -463,19 +464,18 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       for (int t = pair; t < total && ok; t += pairs) {
         const Tile tile = tile_at(t);
         const int n_slices = slices(tile), half_n = mma_n(columns(tile)) / 2;
-        const int parts = two(tile) ? 2 : 1;
         const bool large = !kBMn && half_n > 64;
         const int b_boxes = kBMn ? (half_n + 63) / 64
                             : large ? 1 : (half_n + kBoxRows - 1) / kBoxRows;
         const int box_rows = kBMn ? 64 : large ? 128 : kBoxRows;
-        const uint32_t bytes = parts * kTileABytes + b_boxes * box_rows * kSlice * 2;
+        const uint32_t bytes = kTileABytes + b_boxes * box_rows * kSlice * 2;
         for (int s = 0; s < n_slices; ++s, ++issued) {
           const int st = ring.at;
           if (!mbar_wait(smem_addr(&s_empty[st]), ring.pass ^ 1, gave_up)) {
             ok = false;
             break;
           }
-          ring.advance(n_stages);
+          ring.advance();
           // Both blocks' loads report to the first block's barrier; those of a
           // tail slice to their own block's, where it is cleared first.
           uint32_t full = full0 + st * 8;
@@ -485,29 +485,25 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           } else if (rank == 0) {
             mbar_expect(smem_addr(&s_full[st]), 2 * bytes);
           }
-          const uint32_t sa = smem_addr(stages + st * stage_bytes);
-          const uint32_t sb = sa + a_tiles * kTileABytes;
-          const int k = s * kSlice;
-          for (int i = 0; i < parts; ++i) {
-            const int m = feature(tile, i);
-            const uint32_t dst = sa + i * kTileABytes;
-            if (kUse == kGated) {
-              if (F % 16 == 0) {  // a tile in one load (make_gated_map)
-                tma_load_5d(dst, &map_a, k, 0, 0, m / 16, tile.e, full);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  tma_load_4d(dst + j * (kTileABytes / 4), &map_a, k, m + j * 16, 0, tile.e, full);
-              }
-            } else if (kUse == kForward) {
-              tma_load_3d(dst, &map_a, k, m, tile.e, full);
-            } else if (kUse == kRowsGrad) {
-              tma_load_3d(dst, &map_a, m, k, tile.e, full);
-              tma_load_3d(dst + kTileABytes / 2, &map_a, m + 64, k, tile.e, full);
+          const uint32_t sa = smem_addr(stages + st * kStageBytes);
+          const uint32_t sb = sa + kTileABytes;
+          const int k = s * kSlice, m = feature(tile);
+          if (kUse == kGated) {
+            if (F % 16 == 0) {  // a tile in one load (make_gated_map)
+              tma_load_5d(sa, &map_a, k, 0, 0, m / 16, tile.e, full);
             } else {
-              tma_load_2d(dst, &map_a, m, tile.lo + k, full);
-              tma_load_2d(dst + kTileABytes / 2, &map_a, m + 64, tile.lo + k, full);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                tma_load_4d(sa + j * (kTileABytes / 4), &map_a, k, m + j * 16, 0, tile.e, full);
             }
+          } else if (kUse == kForward) {
+            tma_load_3d(sa, &map_a, k, m, tile.e, full);
+          } else if (kUse == kRowsGrad) {
+            tma_load_3d(sa, &map_a, m, k, tile.e, full);
+            tma_load_3d(sa + kTileABytes / 2, &map_a, m + 64, k, tile.e, full);
+          } else {
+            tma_load_2d(sa, &map_a, m, tile.lo + k, full);
+            tma_load_2d(sa + kTileABytes / 2, &map_a, m + 64, tile.lo + k, full);
           }
           for (int i = 0; i < b_boxes; ++i) {
             if (kBMn)
@@ -525,21 +521,16 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   } else if (warp == kEpiWarps + 1) {
     if (rank == 0 && elect_one()) {
       Ring ring;
-      uint32_t issued = 0, used0 = 0, used1 = 0;  // uses of the accumulator halves
-      int next = 0;
+      uint32_t issued = 0, done = 0;
       bool ok = true;
       for (int t = pair; t < total && ok; t += pairs) {
         const Tile tile = tile_at(t);
         const int n_slices = slices(tile);
         if (n_slices == 0) continue;
-        const int cols = columns(tile);
-        const bool both = two(tile), half = narrow(cols);
-        const uint32_t idesc = instr_desc(kBf16, kAMn, kBMn, 256, mma_n(cols));
-        const int buf = half ? next : 0;
-        next = half ? next ^ 1 : 0;
-        const uint32_t acc0 = tmem + buf * kMaxN, acc1 = acc0 + (half ? kMaxN / 2 : kMaxN);
-        if ((buf == 0 || !half) && !mbar_wait(smem_addr(&s_free[0]), (used0++ & 1) ^ 1, gave_up)) break;
-        if ((buf == 1 || !half) && !mbar_wait(smem_addr(&s_free[1]), (used1++ & 1) ^ 1, gave_up)) break;
+        const uint32_t idesc = instr_desc(kBf16, kAMn, kBMn, 256, mma_n(columns(tile)));
+        const uint32_t buf = done & 1, acc = tmem + buf * kMaxN;
+        if (!mbar_wait(smem_addr(&s_free[buf]), (done / 2 & 1) ^ 1, gave_up)) break;
+        ++done;
         tc_fence_after();
         for (int s = 0; s < n_slices; ++s, ++issued) {
           const int st = ring.at;
@@ -547,20 +538,15 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
             ok = false;
             break;
           }
-          ring.advance(n_stages);
+          ring.advance();
           tc_fence_after();
-          const uint32_t pa = smem_addr(stages + st * stage_bytes);
-          const uint32_t pb = pa + a_tiles * kTileABytes;
+          const uint32_t pa = smem_addr(stages + st * kStageBytes);
+          const uint32_t pb = pa + kTileABytes;
           constexpr uint32_t kStepA = kAMn ? 2048 : 32, kStepB = kBMn ? 2048 : 32;
           const int depth = is_tail(tile, s) ? (tile.rows - s * kSlice + 15) / 16 : kSlice / 16;
-          for (int i = 0; i < depth; ++i) {
-            const uint64_t db = smem_desc(pb + i * kStepB, kBMn ? 8192 : 16, 1024);
-            const bool acc = s > 0 || i > 0;
-            tc_mma(acc0, smem_desc(pa + i * kStepA, kAMn ? 8192 : 16, 1024), db, idesc, acc);
-            if (both)
-              tc_mma(acc1, smem_desc(pa + kTileABytes + i * kStepA, kAMn ? 8192 : 16, 1024), db,
-                     idesc, acc);
-          }
+          for (int i = 0; i < depth; ++i)
+            tc_mma(acc, smem_desc(pa + i * kStepA, kAMn ? 8192 : 16, 1024),
+                   smem_desc(pb + i * kStepB, kBMn ? 8192 : 16, 1024), idesc, s > 0 || i > 0);
           tc_commit(smem_addr(&s_empty[st]));
           if (s == n_slices - 1) tc_commit(smem_addr(&s_done[buf]));
         }
@@ -579,7 +565,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
         const Tile tile = tile_at(t);
         const int n_slices = slices(tile);
         if (n_slices > 0 && is_tail(tile, n_slices - 1)) {
-          const int st = static_cast<int>((step + n_slices - 1) % n_stages);
+          const int st = static_cast<int>((step + n_slices - 1) % kStages);
           const uint32_t parity = tails >> st & 1;
           tails ^= 1u << st;
           if (!warp_wait(smem_addr(&s_tail[st]), parity, gave_up)) break;
@@ -601,42 +587,32 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     T* out = static_cast<T*>(a.out);
     T* preact = static_cast<T*>(a.preact);
     T* residual = kUse == kForward ? static_cast<T*>(const_cast<void*>(a.residual)) : nullptr;
-    uint32_t fin0 = 0, fin1 = 0;
-    int next = 0;
+    uint32_t done = 0;
     const uint32_t free0 = cluster_addr(smem_addr(&s_free[0]), 0);
-    const uint32_t free1 = cluster_addr(smem_addr(&s_free[1]), 0);
     for (int t = pair; t < total; t += pairs) {
       const Tile tile = tile_at(t);
       const int cols = columns(tile);
-      const bool any = slices(tile) > 0, half = narrow(cols);
-      const int parts = two(tile) ? 2 : 1;
-      // The warp's blocks: columns c + [0, 32) of A tile i, unit u = (c, i).
+      const bool any = slices(tile) > 0;
+      // The warp's 32 features, its columns c + [0, 32).
+      const int64_t m = feature(tile) + quad * (kUse == kGated ? 16 : 32);
       const int c0 = warp / 4 * 32;
-      const int units = c0 < cols ? (cols - c0 + 63) / 64 * parts : 0;
-      auto residual_block = [&](int u) {
-        const int c = c0 + u / parts * 64;
-        return Block<T>(residual, a.N, tile.lo + c, cols - c, feature(tile, u % parts) + quad * 32,
-                        a.N, stage);
+      uint4 ahead[4];  // the next columns' residual
+      auto residual_block = [&](int c) {
+        return Block<T>(residual, a.N, tile.lo + c, cols - c, m, a.N, stage);
       };
-      uint4 ahead[4];  // the next unit's residual
-      if (residual != nullptr && units > 0) load_block(ahead, residual_block(0));
-      int buf = 0;
+      if (residual != nullptr && c0 < cols) load_block(ahead, residual_block(c0));
+      const uint32_t buf = done & 1;
       if (any) {
-        buf = half ? next : 0;
-        next = half ? next ^ 1 : 0;
-        const uint32_t parity = (buf == 0 ? fin0++ : fin1++) & 1;
-        if (!warp_wait(smem_addr(&s_done[buf]), parity, gave_up)) break;
+        if (!warp_wait(smem_addr(&s_done[buf]), done / 2 & 1, gave_up)) break;
+        ++done;
         tc_fence_after();
       }
-      const uint32_t acc0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kMaxN;
-      const uint32_t acc1 = acc0 + (half ? kMaxN / 2 : kMaxN);
-      for (int u = 0; u < units; ++u) {
-        const int c = c0 + u / parts * 64, i = u % parts;
+      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kMaxN;
+      for (int c = c0; c < cols; c += 64) {
         const int64_t row = tile.lo + c;
-        const int64_t m = feature(tile, i) + quad * (kUse == kGated ? 16 : 32);
         float z[32];
         if (any) {
-          tmem_load_32x32((i == 0 ? acc0 : acc1) + c, z);
+          tmem_load_32x32(acc + c, z);
           tmem_wait_load(z);
         } else {
 #pragma unroll
@@ -668,15 +644,15 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
             write_block<true>(z, Block<T>(preact, a.N, row, cols - c, m, a.N, stage));
           apply_act<32>(a.act, z);
           if (residual != nullptr) {
-            add_block(z, ahead, residual_block(u));
-            if (u + 1 < units) load_block(ahead, residual_block(u + 1));
+            add_block(z, ahead, residual_block(c));
+            if (c + 64 < cols) load_block(ahead, residual_block(c + 64));
           }
           write_block<true>(z, Block<T>(out, a.N, row, cols - c, m, a.N, stage));
         } else if (kUse == kRowsGrad) {
           write_block<true>(z, Block<T>(out, a.K, row, cols - c, m, a.K, stage));
         } else {
           const int64_t left = a.N - m;
-          write_block<false>(z, Block<T>(out, a.K, static_cast<int64_t>(tile.e) * a.N + m,
+          write_block<false, true>(z, Block<T>(out, a.K, static_cast<int64_t>(tile.e) * a.N + m,
                                          static_cast<int>(left < 32 ? (left < 0 ? 0 : left) : 32),
                                          tile.n0 + c, a.K, stage));
         }
@@ -684,10 +660,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       if (any) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_relaxed_cluster(buf == 0 ? free0 : free1);
-          if (!half) mbar_arrive_relaxed_cluster(free1);
-        }
+        if (lane == 0) mbar_arrive_relaxed_cluster(free0 + buf * 8);
       }
     }
   }

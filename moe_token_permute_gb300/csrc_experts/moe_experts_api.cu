@@ -110,14 +110,15 @@ bool make_gated_map(CUtensorMap* map, const void* base, int64_t E, int64_t F, in
   return make_map_nd<T, 4>(map, base, {K, F, 2, E}, {K, F * K, 2 * F * K}, {64, 16, 2, 1});
 }
 
-// The most tiles a product may have with a_tiles A tiles per block.
+// The most tiles a product may have.
 template <int kUse>
-int64_t most_tiles(const ProductArgs& a, int a_tiles) {
+int64_t most_tiles(const ProductArgs& a) {
   const int64_t m = kUse == kForward || kUse == kWeightGrad ? a.N : kUse == kGated ? a.N / 2 : a.K;
+  constexpr int cap_least = kMaxN - 16 * (kCaps - 1);
   const int64_t columns = kUse == kWeightGrad
                               ? a.E * ceil_div(a.K, kMaxN)
-                              : a.num_rows / (kMaxN / 2) + std::min<int64_t>(a.E, a.num_rows);
-  return ceil_div(m, a_tiles * m_unit<kUse>()) * columns;
+                              : a.num_rows / cap_least + std::min<int64_t>(a.E, a.num_rows);
+  return ceil_div(m, m_step<kUse>()) * columns;
 }
 
 // lhs: the weight, or dz for d_weight; rhs: the rows, or dz for d_rows.
@@ -142,7 +143,7 @@ cudaError_t launch_product(const ProductArgs& a, const void* lhs, const void* rh
          make_map<T>(&map_b_large, rhs, 0, a.num_rows, depth, 128);
   }
   if (!ok) return cudaErrorInvalidValue;
-  const int64_t tiles = most_tiles<kUse>(a, 1);
+  const int64_t tiles = most_tiles<kUse>(a);
   if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
   return launch(k_expert_product<T, kUse>,
                 dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, sms / 2))), kProductThreads,
@@ -152,7 +153,7 @@ cudaError_t launch_product(const ProductArgs& a, const void* lhs, const void* rh
 template <typename T, int kUse>
 cudaError_t launch_forward(const ProductArgs& a, const void* weight, const void* rows, int sms,
                            cudaStream_t s) {
-  if (!decode_pays(a.num_rows, a.K, most_tiles<kUse>(a, 2), sms / 2))
+  if (!decode_pays(a.num_rows, a.K, most_tiles<kUse>(a), sms / 2))
     return launch_product<T, kUse>(a, weight, rows, sms, s);
   constexpr bool kGatedForm = kUse == kGated;
   // Tasks at most: every expert with rows has one group, and each further
@@ -210,10 +211,6 @@ cudaError_t product_gradients(const void* dz, const void* rows, const void* weig
   }
   if (d_weight != nullptr) {
     a.out = d_weight;
-#ifndef WMT
-#define WMT 1
-#endif
-    a.a_tiles = WMT;
     return launch_product<T, kWeightGrad>(a, dz, rows, sms, s);
   }
   return cudaSuccess;
