@@ -297,9 +297,9 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   constexpr bool kAMn = kUse == kRowsGrad || kUse == kWeightGrad;
   constexpr bool kBMn = kUse == kWeightGrad;
   extern __shared__ uint8_t smem_raw[];
-  // s_full, s_free and s_peer are used in the pair's first block only.
+  // s_full, s_free and s_clear are used in the pair's first block only.
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_done[2], s_free[2],
-      s_peer[kStages], s_tail[kStages];
+      s_clear[kStages], s_tail[kStages];
   __shared__ uint32_t s_tmem;
   __shared__ int s_gave_up, s_scan[32], s_blocks[kCaps + 1], s_cap;
 
@@ -316,7 +316,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_addr(&s_full[i]), 1);
       mbar_init(smem_addr(&s_empty[i]), 1);
-      mbar_init(smem_addr(&s_peer[i]), 1);
+      mbar_init(smem_addr(&s_clear[i]), 2);
       mbar_init(smem_addr(&s_tail[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -446,12 +446,15 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   // expert or to none and may be infinite or NaN, so it is overwritten in both
   // operands rather than multiplied by zeros.
   auto clear_tail = [&](int st, int left) {
-    constexpr int kBoxes = kStageBytes / (kTileABytes / 2);  // 64 values x 64 rows each
-    const int rows = (left + 15) / 16 * 16 - left;
-    for (int box = 0; box < kBoxes; ++box)
-      for (int i = lane; i < rows * 8; i += 32)
-        *reinterpret_cast<uint4*>(stages + st * kStageBytes + box * (kTileABytes / 2) +
-                                  (left + i / 8) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+    const int chunks = ((left + 15) / 16 * 16 - left) * 8;  // of 16 bytes, in each box
+    uint8_t* at = stages + st * kStageBytes + left * 128 + lane * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i * 32 + lane < chunks) {
+#pragma unroll
+        for (int box = 0; box < 4; ++box)  // 64 values x 64 rows: two of A, two of B
+          *reinterpret_cast<uint4*>(at + i * 512 + box * (kTileABytes / 2)) = make_uint4(0, 0, 0, 0);
+      }
     fence_async_shared();
     __syncwarp();
   };
@@ -477,9 +480,10 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           }
           ring.advance();
           // Both blocks' loads report to the first block's barrier; those of a
-          // tail slice to their own block's, where it is cleared first.
+          // tail slice to their own block's, where it is cleared first (s_clear).
           uint32_t full = full0 + st * 8;
           if (is_tail(tile, s)) {
+            if (rank == 0) mbar_arrive(smem_addr(&s_full[st]));
             full = smem_addr(&s_tail[st]);
             mbar_expect(full, bytes);
           } else if (rank == 0) {
@@ -522,6 +526,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     if (rank == 0 && elect_one()) {
       Ring ring;
       uint32_t issued = 0, done = 0;
+      uint32_t tails = 0;  // bit st: parity of the stage's tail slices so far
       bool ok = true;
       for (int t = pair; t < total && ok; t += pairs) {
         const Tile tile = tile_at(t);
@@ -537,6 +542,13 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           if (!mbar_wait(smem_addr(&s_full[st]), ring.pass, gave_up)) {
             ok = false;
             break;
+          }
+          if (is_tail(tile, s)) {
+            if (!mbar_wait(smem_addr(&s_clear[st]), tails >> st & 1, gave_up)) {
+              ok = false;
+              break;
+            }
+            tails ^= 1u << st;
           }
           ring.advance();
           tc_fence_after();
@@ -557,8 +569,8 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     __syncwarp();
   } else if (warp == kEpiWarps + 2) {
     if (kUse == kWeightGrad) {
-      // Tail slices: both blocks clear theirs, the second tells the first, and
-      // the first releases the slice to the products.
+      // Tail slices: each block clears its own and tells the first block.
+      const uint32_t clear0 = cluster_addr(smem_addr(&s_clear[0]), 0);
       uint32_t step = 0;
       uint32_t tails = 0;  // bit st: parity of the stage's tail slices so far
       for (int t = pair; t < total; t += pairs) {
@@ -570,12 +582,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           tails ^= 1u << st;
           if (!warp_wait(smem_addr(&s_tail[st]), parity, gave_up)) break;
           clear_tail(st, tile.rows - (n_slices - 1) * kSlice);
-          if (rank != 0) {
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&s_peer[st]), 0));
-          } else {
-            if (!warp_wait(smem_addr(&s_peer[st]), parity, gave_up)) break;
-            if (lane == 0) mbar_arrive(smem_addr(&s_full[st]));
-          }
+          if (lane == 0) mbar_arrive_cluster(clear0 + st * 8);
         }
         step += n_slices;
       }
