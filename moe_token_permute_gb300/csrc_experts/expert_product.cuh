@@ -120,12 +120,13 @@ __device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const 
   Tile r;
   if (kUse == kWeightGrad) {
     const int per = m_blocks * n_blocks;
-    r.e = t / per;
+    const int place = t / per;
+    r.e = first[place];  // experts by falling number of rows
     const Segment s = segments[r.e];
     r.lo = s.lo;
     r.rows = s.hi - s.lo;
     int m, n;
-    place_in_panels(t - r.e * per, m_blocks, n_blocks, m, n);
+    place_in_panels(t - place * per, m_blocks, n_blocks, m, n);
     r.m0 = m * m_step<kUse>();
     r.n0 = n * kMaxN;
     return r;
@@ -386,7 +387,20 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   // Tiles of each expert, and the sum before it.
   int total = 0;
   if (kUse == kWeightGrad) {
+    // A tile costs its expert's rows: the experts go by falling rows, and the
+    // pairs take the tiles to and fro (Walk), so that each gets its share of the
+    // long ones (Zipf 1.2 over 128 experts: the longest pair 1.4% over the average
+    // instead of 14%).
     total = a.E * m_blocks * n_blocks;
+    for (int e = threadIdx.x; e < a.E; e += kProductThreads) {
+      const int rows = segments[e].hi - segments[e].lo;
+      int before = 0;
+      for (int f = 0; f < a.E; ++f) {
+        const int other = segments[f].hi - segments[f].lo;
+        before += other > rows || (other == rows && f < e);
+      }
+      first[before] = e;
+    }
   } else {
     for (int e0 = 0; e0 < a.E; e0 += kProductThreads) {
       const int e = e0 + threadIdx.x;
@@ -422,6 +436,18 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       --r.at;
       while (!mbar_try(smem_addr(&s_empty[r.at]), r.pass) && now_ns() - t0 < kWaitNs) {
       }
+    }
+  };
+  // The pair's tiles: one of every `pairs`, in turn from the front and the back.
+  struct Walk {
+    int t, up, down;
+    __device__ __forceinline__ Walk(int pair, int pairs)
+        : t(pair), up(2 * (pairs - pair) - 1), down(2 * pair + 1) {}
+    __device__ __forceinline__ void next() {
+      t += up;
+      const int s = up;
+      up = down;
+      down = s;
     }
   };
   auto tile_at = [&](int t) {
@@ -464,8 +490,8 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       uint32_t issued = 0;
       bool ok = true;
       const uint32_t full0 = cluster_addr(smem_addr(&s_full[0]), 0);  // the first block's
-      for (int t = pair; t < total && ok; t += pairs) {
-        const Tile tile = tile_at(t);
+      for (Walk walk(pair, pairs); walk.t < total && ok; walk.next()) {
+        const Tile tile = tile_at(walk.t);
         const int n_slices = slices(tile), half_n = mma_n(columns(tile)) / 2;
         const bool large = !kBMn && half_n > 64;
         const int b_boxes = kBMn ? (half_n + 63) / 64
@@ -528,8 +554,8 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       uint32_t issued = 0, done = 0;
       uint32_t tails = 0;  // bit st: parity of the stage's tail slices so far
       bool ok = true;
-      for (int t = pair; t < total && ok; t += pairs) {
-        const Tile tile = tile_at(t);
+      for (Walk walk(pair, pairs); walk.t < total && ok; walk.next()) {
+        const Tile tile = tile_at(walk.t);
         const int n_slices = slices(tile);
         if (n_slices == 0) continue;
         const uint32_t idesc = instr_desc(kBf16, kAMn, kBMn, 256, mma_n(columns(tile)));
@@ -573,8 +599,8 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       const uint32_t clear0 = cluster_addr(smem_addr(&s_clear[0]), 0);
       uint32_t step = 0;
       uint32_t tails = 0;  // bit st: parity of the stage's tail slices so far
-      for (int t = pair; t < total; t += pairs) {
-        const Tile tile = tile_at(t);
+      for (Walk walk(pair, pairs); walk.t < total; walk.next()) {
+        const Tile tile = tile_at(walk.t);
         const int n_slices = slices(tile);
         if (n_slices > 0 && is_tail(tile, n_slices - 1)) {
           const int st = static_cast<int>((step + n_slices - 1) % kStages);
@@ -596,8 +622,8 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     T* residual = kUse == kForward ? static_cast<T*>(const_cast<void*>(a.residual)) : nullptr;
     uint32_t done = 0;
     const uint32_t free0 = cluster_addr(smem_addr(&s_free[0]), 0);
-    for (int t = pair; t < total; t += pairs) {
-      const Tile tile = tile_at(t);
+    for (Walk walk(pair, pairs); walk.t < total; walk.next()) {
+      const Tile tile = tile_at(walk.t);
       const int cols = columns(tile);
       const bool any = slices(tile) > 0;
       // The warp's 32 features, its columns c + [0, 32).
