@@ -3,6 +3,7 @@
 #pragma once
 
 #include "expert_math.cuh"
+#include "tcgen05.cuh"
 
 namespace moe {
 namespace experts {
@@ -10,86 +11,112 @@ namespace experts {
 constexpr int kGradThreads = 256;
 constexpr int kGradWarps = kGradThreads / 32;
 
-// dz from d_out and the saved z, one warp per (row, 32 vectors of 8 columns).
+// dz from d_out and the saved z.
 //   gated:  z = [gate, up] [rows, 2W]; dz = [d * up * act'(gate), d * act(gate)]
 //   linear: z [rows, W]; dz = d * act'(z)
 // W is d_out's width.  Computed in fp32 from 16-bit z and rounded once: dz is
-// the operand of two 16-bit matrix products.
+// the operand of two 16-bit matrix products.  A warp has 32 vectors of 8 columns
+// (blockIdx.y) and takes rows of them, two in flight.
 template <typename T, bool kGatedForm, int kAct>
 __global__ void __launch_bounds__(kGradThreads)
 k_act_grad(const T* __restrict__ d_out, const T* __restrict__ z, T* __restrict__ dz,
            const int64_t* __restrict__ offset, int E, int64_t num_rows, int64_t W) {
+  constexpr int kRows = 2;
   pdl_wait();
   const int64_t n = rows_in_use(offset, E, num_rows);
-  const int64_t vecs = W / 8;
-  const int64_t chunks = (vecs + 31) / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t warp0 = static_cast<int64_t>(blockIdx.x) * kGradWarps + (threadIdx.x >> 5);
-  const int64_t n_warps = static_cast<int64_t>(gridDim.x) * kGradWarps;
-  for (int64_t item = warp0; item < n * chunks; item += n_warps) {
-    const int64_t r = item / chunks;
-    const int64_t c = (item - r * chunks) * 32 + lane;
-    if (c >= vecs) continue;
-    Vec8<T> d, g, u;
-    d.v = ld_stream(reinterpret_cast<const uint4*>(d_out + r * W) + c);
-    if (kGatedForm) {
-      g.v = ld_stream(reinterpret_cast<const uint4*>(z + r * 2 * W) + c);
-      u.v = ld_stream(reinterpret_cast<const uint4*>(z + r * 2 * W + W) + c);
-    } else {
-      g.v = ld_stream(reinterpret_cast<const uint4*>(z + r * W) + c);
-    }
-    Vec8<T> dg, du;
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * 32 + (threadIdx.x & 31);
+  if (c >= W / 8) return;
+  const int64_t zw = kGatedForm ? 2 * W : W;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGradWarps;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGradWarps + (threadIdx.x >> 5); r0 < n;
+       r0 += kRows * step) {
+    Vec8<T> d[kRows], g[kRows], u[kRows];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float a;
-      const float da = act_grad<kAct>(to_f(g.e[i]), a);
-      const float di = to_f(d.e[i]);
-      if (kGatedForm) {
-        dg.e[i] = from_f<T>(di * to_f(u.e[i]) * da);
-        du.e[i] = from_f<T>(di * a);
-      } else {
-        dg.e[i] = from_f<T>(di * da);
-      }
+    for (int j = 0; j < kRows; ++j) {
+      const int64_t r = r0 + j * step;
+      if (r >= n) break;
+      d[j].v = ld_stream(reinterpret_cast<const uint4*>(d_out + r * W) + c);
+      g[j].v = ld_stream(reinterpret_cast<const uint4*>(z + r * zw) + c);
+      if (kGatedForm) u[j].v = ld_stream(reinterpret_cast<const uint4*>(z + r * zw + W) + c);
     }
-    if (kGatedForm) {
-      reinterpret_cast<uint4*>(dz + r * 2 * W)[c] = dg.v;
-      reinterpret_cast<uint4*>(dz + r * 2 * W + W)[c] = du.v;
-    } else {
-      reinterpret_cast<uint4*>(dz + r * W)[c] = dg.v;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int64_t r = r0 + j * step;
+      if (r >= n) break;
+      Vec8<T> dg, du;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float a;
+        const float da = act_grad<kAct>(to_f(g[j].e[i]), a);
+        const float di = to_f(d[j].e[i]);
+        if (kGatedForm) {
+          dg.e[i] = from_f<T>(di * to_f(u[j].e[i]) * da);
+          du.e[i] = from_f<T>(di * a);
+        } else {
+          dg.e[i] = from_f<T>(di * da);
+        }
+      }
+      reinterpret_cast<uint4*>(dz + r * zw)[c] = dg.v;
+      if (kGatedForm) reinterpret_cast<uint4*>(dz + r * zw + W)[c] = du.v;
     }
   }
 }
 
 // d_bias[e] = column sums of dz over e's rows, in fp32 and in a fixed order: a
 // block takes 64 columns of one expert, 8 threads a row and 32 rows at a time.
+// With few experts and columns a cluster of blocks shares the rows and the first
+// adds the others' sums up.
+constexpr int kBiasSplit = 8;
+
 template <typename T>
 __global__ void __launch_bounds__(kGradThreads)
 k_bias_grad(const T* __restrict__ dz, const int64_t* __restrict__ offset, int64_t num_rows,
             int64_t N, T* __restrict__ d_bias) {
+  constexpr int kAhead = 8;
   pdl_wait();
   __shared__ float part[32][64 + 1];
+  __shared__ float sums[64];
   const int e = blockIdx.y;
   const Segment s = segment(offset, e, num_rows);
+  const int splits = gridDim.z, split = blockIdx.z;
+  const int share = (s.hi - s.lo + splits - 1) / splits;
+  const int lo = min(s.hi, s.lo + split * share), hi = min(s.hi, lo + share);
   const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + tx;
   float acc[8] = {};
   if (c < N / 8) {
-#pragma unroll 4
-    for (int r = s.lo + ty; r < s.hi; r += 32) {
-      Vec8<T> v;
-      v.v = ld_stream(reinterpret_cast<const uint4*>(dz + static_cast<int64_t>(r) * N) + c);
+    const uint4* at = reinterpret_cast<const uint4*>(dz) + c;
+    for (int r = lo + ty; r < hi; r += 32 * kAhead) {
+      Vec8<T> v[kAhead];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += to_f(v.e[i]);
+      for (int j = 0; j < kAhead; ++j)
+        v[j].v = r + 32 * j < hi ? ld_stream(at + static_cast<int64_t>(r + 32 * j) * (N / 8))
+                                 : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += to_f(v[j].e[i]);
     }
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) part[ty][tx * 8 + i] = acc[i];
   __syncthreads();
+  float sum = 0.f;
   if (threadIdx.x < 64) {
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
-    float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) sum += part[i][threadIdx.x];
+    sums[threadIdx.x] = sum;
+  }
+  if (splits > 1) {
+    cluster_sync();
+    if (split == 0 && threadIdx.x < 64) {
+      for (int i = 1; i < splits; ++i)
+        sum += cluster_load(cluster_addr(smem_addr(&sums[threadIdx.x]), i));
+    }
+    cluster_sync();  // the others' sums stay until they are read
+  }
+  if (split == 0 && threadIdx.x < 64) {
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
     if (col < N) d_bias[static_cast<int64_t>(e) * N + col] = from_f<T>(sum);
   }
 }

@@ -177,18 +177,25 @@ cudaError_t launch_act_grad(const void* d_out, const void* z, void* dz, const in
   if (act == MOE_ACT_SILU) kern = k_act_grad<T, kGatedForm, MOE_ACT_SILU>;
   if (act == MOE_ACT_GELU) kern = k_act_grad<T, kGatedForm, MOE_ACT_GELU>;
   if (act == MOE_ACT_RELU) kern = k_act_grad<T, kGatedForm, MOE_ACT_RELU>;
-  const int64_t warps = num_rows * ceil_div(W / 8, 32);
-  const int64_t grid = std::min<int64_t>(ceil_div(warps, kGradWarps), 8 * static_cast<int64_t>(sms));
-  return launch(kern, dim3(static_cast<unsigned>(grid)), kGradThreads, 0, s,
+  const int64_t columns = ceil_div(W / 8, 32);
+  if (columns > 65535) return cudaErrorInvalidConfiguration;
+  // About 8 blocks per SM, and never fewer than one.
+  const int64_t grid = std::min(ceil_div(num_rows, kGradWarps),
+                                std::max<int64_t>(1, 8 * static_cast<int64_t>(sms) / columns));
+  return launch(kern, dim3(static_cast<unsigned>(grid), static_cast<unsigned>(columns)),
+                kGradThreads, 0, s,
                 static_cast<const T*>(d_out), static_cast<const T*>(z), static_cast<T*>(dz),
                 offset, E, num_rows, W);
 }
 
 template <typename T>
 cudaError_t launch_bias_grad(const void* dz, const int64_t* offset, int E, int64_t num_rows,
-                             int64_t N, void* d_bias, cudaStream_t s) {
-  return launch(k_bias_grad<T>, dim3(static_cast<unsigned>(ceil_div(N, 64)), E), kGradThreads, 0,
-                s, static_cast<const T*>(dz), offset, num_rows, N, static_cast<T*>(d_bias));
+                             int64_t N, void* d_bias, int sms, cudaStream_t s) {
+  const int64_t blocks = ceil_div(N, 64);
+  const unsigned splits = blocks * E <= sms ? kBiasSplit : 1;
+  return launch_clusters(k_bias_grad<T>, dim3(static_cast<unsigned>(blocks), E, splits), splits,
+                         kGradThreads, 0, s, static_cast<const T*>(dz), offset, num_rows, N,
+                         static_cast<T*>(d_bias));
 }
 
 // d_rows and d_weight of z = x W^T from dz.
@@ -219,15 +226,20 @@ cudaError_t product_gradients(const void* dz, const void* rows, const void* weig
 template <typename VecT>
 cudaError_t launch_unpermute_backward(const void* d_out, const void* rows, int64_t num_rows,
                                       int64_t H, const float* w, const int32_t* inv, int64_t T,
-                                      int K, void* d_rows, float* d_w, unsigned* status,
+                                      int K, void* d_rows, float* d_w, unsigned* status, int sms,
                                       cudaStream_t s) {
-  constexpr int V = 4;
   const int64_t vecs = H * 2 / static_cast<int64_t>(sizeof(VecT));
-  const int64_t warps = std::min<int64_t>(kCombineMaxWarps, ceil_div(vecs, 32));
-  return launch(k_unpermute_backward<VecT, V>, dim3(static_cast<unsigned>(T)),
-                static_cast<unsigned>(warps * 32), 0, s, static_cast<const VecT*>(d_out),
-                static_cast<const VecT*>(rows), num_rows, vecs, w, inv, K,
-                static_cast<VecT*>(d_rows), d_w, status);
+  // (t, k) per warp: one while there are few, then so many that the warps are 150
+  // per SM (64: DeepSeek-V3 shape T = 4096 162 us instead of 150; 220 and more:
+  // DeepSeek-V2-Lite with its map 36 us instead of 30).
+  const int64_t items = T * K;
+  const int64_t per_warp =
+      std::max<int64_t>(1, std::min<int64_t>(32, items / (150 * static_cast<int64_t>(sms))));
+  const int64_t blocks = ceil_div(ceil_div(items, per_warp), kCombineWarps);
+  return launch(k_unpermute_backward<VecT>, dim3(static_cast<unsigned>(blocks)),
+                kCombineWarps * 32, 0, s, static_cast<const VecT*>(d_out),
+                static_cast<const VecT*>(rows), num_rows, vecs, w, inv, items, K,
+                static_cast<int>(per_warp), static_cast<VecT*>(d_rows), d_w, status);
 }
 
 int finish(cudaError_t err) {
@@ -381,7 +393,7 @@ int moe_expert_linear_backward(const void* d_out, const void* rows, const void* 
   }
   if (err == cudaSuccess && d_bias != nullptr) {
     auto grad = bf ? launch_bias_grad<__nv_bfloat16> : launch_bias_grad<__half>;
-    err = grad(dz, expert_first_token_offset, num_local_experts, num_rows, out_size, d_bias, s);
+    err = grad(dz, expert_first_token_offset, num_local_experts, num_rows, out_size, d_bias, sms, s);
   }
   if (err != cudaSuccess) return finish(err);
   auto gradients = bf ? product_gradients<__nv_bfloat16> : product_gradients<__half>;
@@ -406,7 +418,8 @@ int moe_unpermute_backward(const void* d_out, const void* permuted_rows, int64_t
   if (num_rows > 0 && (permuted_rows == nullptr) != (d_topk_weights == nullptr))
     return MOE_ERR_INVALID_ARG;
   if (d_rows == nullptr && d_topk_weights == nullptr) return MOE_ERR_INVALID_ARG;
-  if (supported_sm_count() == 0) return MOE_ERR_UNSUPPORTED_DEVICE;
+  const int sms = supported_sm_count();
+  if (sms == 0) return MOE_ERR_UNSUPPORTED_DEVICE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   unsigned* status = status_of(workspace);
   size_t vb = 16;
@@ -418,7 +431,7 @@ int moe_unpermute_backward(const void* d_out, const void* permuted_rows, int64_t
              : vb == 4 ? launch_unpermute_backward<uint32_t>
                        : launch_unpermute_backward<uint16_t>;
   return finish(run(d_out, permuted_rows, num_rows, H, topk_weights, inv_permuted_idx, T, topk,
-                    d_rows, d_topk_weights, status, s));
+                    d_rows, d_topk_weights, status, sms, s));
 }
 
 }  // extern "C"

@@ -1,5 +1,5 @@
-// tcgen05.cuh -- the PTX the grouped products are written in: mbarriers, TMA
-// tile loads, tensor memory and tcgen05.mma.  Formats are those of the PTX ISA.
+// tcgen05.cuh -- the PTX the grouped products are written in: mbarriers, clusters,
+// TMA tile loads, tensor memory and tcgen05.mma.  Formats are those of the PTX ISA.
 #pragma once
 
 #include <cuda.h>
@@ -57,6 +57,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
+}
+__device__ __forceinline__ float cluster_load(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
