@@ -28,6 +28,8 @@
 // linear: they are zero (16 features per task would balance worse).
 #pragma once
 
+#include <algorithm>
+
 #include "expert_product.cuh"
 
 namespace moe {
@@ -69,13 +71,15 @@ constexpr int kDecodeMaxRows = 32;
 //   gated 64 x 7168 -> 2048, 8 / 16 rows     72 / 77    112 / 131
 //   gated 8 x 4096 -> 14336, 2 / 8 rows      71 / 83    167 / 180
 //   linear 8 x 14336 -> 4096, 2 / 32 rows    41 / 92    147 / 152
-//   linear 1 x 4096 -> 4096, 8 / 16 / 32 rows   12 / 31    18 / 31    31 / 31
+//   linear 1 x 4096 -> 4096, 8 / 16 / 24 rows   12 / 16    18 / 16    25 / 16
 //   gated 128 x 2048 -> 768, 8 / 16 / 32 rows   14 / 17    21 / 19    29 / 27
 //   linear 128 x 768 -> 2048, 8 / 32 rows    24 / 11    57 / 17
 // A task costs about 0.7 us beside its loads, so it needs a long contraction;
-// of 2048 values it pays while the large tiles do not fill the pairs.
-inline bool decode_pays(int64_t rows, int64_t K, int64_t tiles, int64_t pairs) {
-  return rows <= kDecodeMaxRows && K % 64 == 0 && (K >= 4096 || (K >= 2048 && tiles <= pairs));
+// of 2048 values it pays while the large tiles do not fill the pairs.  More than 8
+// rows of one expert read its weights again.
+inline bool decode_pays(int64_t rows, int64_t E, int64_t K, int64_t tiles, int64_t pairs) {
+  return rows <= std::min<int64_t>(kDecodeMaxRows, kDecodeGroup * E) && K % 64 == 0 &&
+         (K >= 4096 || (K >= 2048 && tiles <= pairs));
 }
 
 template <typename T>

@@ -26,6 +26,11 @@
 // 128 rows 1% faster.)  Large products run at the power limit: 1.87 PFLOP/s in
 // bursts of 1 ms, Mixtral-shaped gated T = 4096.
 // The grid is persistent; tiles are numbered expert by expert, in panels.
+// Where the tiles are at most half as many as the pairs (a dense layer and few
+// rows), two pairs make a cluster and share a tile's contraction: each takes half
+// of its slices, the second leaves its sums in its own shared memory, and the
+// first adds them to its own through the cluster.  Dense 4096 -> 4096, 64 rows: 16
+// us instead of 22; four pairs, whose clusters do not all run at once, 26.
 #pragma once
 
 #include "expert_math.cuh"
@@ -42,6 +47,7 @@ constexpr int kTileABytes = 128 * kSlice * 2;
 constexpr int kTileBBytes = kMaxN / 2 * kSlice * 2;
 constexpr int kStageBytes = kTileABytes + kTileBBytes;
 constexpr int kStages = 6;
+constexpr int kMaxSplits = 2;  // pairs of a cluster
 constexpr int kBoxRows = 32;   // rows of the small TMA box of a k-contiguous B; the large: 128
 constexpr int kEpiWarps = 8;
 constexpr int kProductThreads = (kEpiWarps + 3) * 32;
@@ -93,6 +99,7 @@ __host__ __device__ constexpr int m_step() { return kUse == kGated ? 128 : 256; 
 // its first product.  Dense 4096 -> 4096: 500 rows 25 us in blocks of 128 and 31 of
 // 256, 8191 rows 238 and 166.
 constexpr int kCaps = 13;  // 256, 240, ..., 64
+constexpr int kLeastCap = kMaxN - 16 * (kCaps - 1);
 __device__ __forceinline__ int cap_of(int i) { return kMaxN - 16 * i; }
 __device__ __forceinline__ float cap_cost(int blocks, int rows, int m_blocks, int slices, int pairs) {
   const int64_t waves = (static_cast<int64_t>(blocks) * m_blocks + pairs - 1) / pairs;
@@ -290,7 +297,7 @@ __device__ __forceinline__ void add_block(float (&v)[32], const uint4 (&x)[4], c
 // 128-byte swizzle) by 128 (forward A), 64 (MN-major) or kBoxRows rows; map_b_large
 // by 128.  map_a of the gated product: make_gated_map.
 template <typename T, int kUse>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
+__global__ void __launch_bounds__(kProductThreads, 1)
 k_expert_product(const __grid_constant__ CUtensorMap map_a,
                  const __grid_constant__ CUtensorMap map_b,
                  const __grid_constant__ CUtensorMap map_b_large, const ProductArgs a) {
@@ -298,9 +305,10 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   constexpr bool kAMn = kUse == kRowsGrad || kUse == kWeightGrad;
   constexpr bool kBMn = kUse == kWeightGrad;
   extern __shared__ uint8_t smem_raw[];
-  // s_full, s_free and s_clear are used in the pair's first block only.
+  // s_full, s_free and s_clear are used in a pair's first block only, s_parts in
+  // the cluster's first pair.
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_done[2], s_free[2],
-      s_clear[kStages], s_tail[kStages];
+      s_clear[kStages], s_tail[kStages], s_parts;
   __shared__ uint32_t s_tmem;
   __shared__ int s_gave_up, s_scan[32], s_blocks[kCaps + 1], s_cap;
 
@@ -310,8 +318,12 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   Segment* segments = reinterpret_cast<Segment*>(staging + kStagingBytes);
   int* first = reinterpret_cast<int*>(segments + a.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_rank());
-  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  // Clusters of `splits` pairs; the block's place in its pair; the rank of the
+  // pair's first block.
+  const uint32_t place = cluster_rank(), leader = place & ~1u;
+  const int rank = static_cast<int>(place & 1u), split = static_cast<int>(place / 2);
+  const int splits = static_cast<int>(cluster_size() / 2);
+  const int pair = blockIdx.x / (2 * splits), pairs = gridDim.x / (2 * splits);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -324,6 +336,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       mbar_init(smem_addr(&s_done[i]), 1);
       mbar_init(smem_addr(&s_free[i]), 2 * kEpiWarps);
     }
+    mbar_init(smem_addr(&s_parts), kEpiWarps);
     mbar_init_fence();
     s_gave_up = 0;
     tma_prefetch_map(&map_a);
@@ -369,7 +382,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   __syncthreads();
   const int m_blocks = (m_size + m_step<kUse>() - 1) / m_step<kUse>();
   int cap = kMaxN;
-  if (kUse != kWeightGrad) {
+  if (kUse != kWeightGrad && splits == 1) {
     if (warp == 0) {
       float cost = INFINITY;
       if (lane == 0 || (lane < kCaps && s_blocks[0] < (6 * pairs + m_blocks - 1) / m_blocks))
@@ -411,6 +424,8 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       total += part;
     }
     if (threadIdx.x == 0) first[a.E] = total;
+    // (More only where bad offsets make segments overlap.)
+    if (splits > 1) total = min(total, pairs);
   }
   tc_fence_before();
   __syncthreads();
@@ -453,9 +468,13 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   auto tile_at = [&](int t) {
     return find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks, cap);
   };
-  // Slices of the contraction (d_weight: of the expert's rows).
+  // Slices of the contraction (d_weight: of the expert's rows), from first_slice on
+  // in pairs that share it.
+  const int all_slices = (k_size + kSlice - 1) / kSlice;
+  const int first_slice = all_slices * split / splits;
   auto slices = [&](const Tile& t) {
-    return ((kUse == kWeightGrad ? t.rows : k_size) + kSlice - 1) / kSlice;
+    return kUse == kWeightGrad ? (t.rows + kSlice - 1) / kSlice
+                               : all_slices * (split + 1) / splits - first_slice;
   };
   // Columns of the tile, and those of the product (each block holds half of B).
   auto columns = [&](const Tile& t) {
@@ -489,7 +508,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       Ring ring;
       uint32_t issued = 0;
       bool ok = true;
-      const uint32_t full0 = cluster_addr(smem_addr(&s_full[0]), 0);  // the first block's
+      const uint32_t full0 = cluster_addr(smem_addr(&s_full[0]), leader);
       for (Walk walk(pair, pairs); walk.t < total && ok; walk.next()) {
         const Tile tile = tile_at(walk.t);
         const int n_slices = slices(tile), half_n = mma_n(columns(tile)) / 2;
@@ -517,7 +536,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           }
           const uint32_t sa = smem_addr(stages + st * kStageBytes);
           const uint32_t sb = sa + kTileABytes;
-          const int k = s * kSlice, m = feature(tile);
+          const int k = ((kUse == kWeightGrad ? 0 : first_slice) + s) * kSlice, m = feature(tile);
           if (kUse == kGated) {
             if (F % 16 == 0) {  // a tile in one load (make_gated_map)
               tma_load_5d(sa, &map_a, k, 0, 0, m / 16, tile.e, full);
@@ -553,6 +572,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       Ring ring;
       uint32_t issued = 0, done = 0;
       uint32_t tails = 0;  // bit st: parity of the stage's tail slices so far
+      const uint16_t both = static_cast<uint16_t>(3u << leader);
       bool ok = true;
       for (Walk walk(pair, pairs); walk.t < total && ok; walk.next()) {
         const Tile tile = tile_at(walk.t);
@@ -585,8 +605,8 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           for (int i = 0; i < depth; ++i)
             tc_mma(acc, smem_desc(pa + i * kStepA, kAMn ? 8192 : 16, 1024),
                    smem_desc(pb + i * kStepB, kBMn ? 8192 : 16, 1024), idesc, s > 0 || i > 0);
-          tc_commit(smem_addr(&s_empty[st]));
-          if (s == n_slices - 1) tc_commit(smem_addr(&s_done[buf]));
+          tc_commit(smem_addr(&s_empty[st]), both);
+          if (s == n_slices - 1) tc_commit(smem_addr(&s_done[buf]), both);
         }
       }
       // The products are over before the memory they read and write is given up.
@@ -596,7 +616,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   } else if (warp == kEpiWarps + 2) {
     if (kUse == kWeightGrad) {
       // Tail slices: each block clears its own and tells the first block.
-      const uint32_t clear0 = cluster_addr(smem_addr(&s_clear[0]), 0);
+      const uint32_t clear0 = cluster_addr(smem_addr(&s_clear[0]), leader);
       uint32_t step = 0;
       uint32_t tails = 0;  // bit st: parity of the stage's tail slices so far
       for (Walk walk(pair, pairs); walk.t < total; walk.next()) {
@@ -621,7 +641,12 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     T* preact = static_cast<T*>(a.preact);
     T* residual = kUse == kForward ? static_cast<T*>(const_cast<void*>(a.residual)) : nullptr;
     uint32_t done = 0;
-    const uint32_t free0 = cluster_addr(smem_addr(&s_free[0]), 0);
+    const uint32_t free0 = cluster_addr(smem_addr(&s_free[0]), leader);
+    // Pairs that share a tile have one tile at most: its sums may lie over the
+    // stages, which are through.  A lane's 32 values of the warp's columns c: 8
+    // steps of 512 bytes from part + 64 c on.
+    const uint32_t part = smem_addr(stages + warp * 4 * 4096) + lane * 16;
+    const uint32_t other_part = splits > 1 ? cluster_addr(part, 2 + rank) : 0;
     for (Walk walk(pair, pairs); walk.t < total; walk.next()) {
       const Tile tile = tile_at(walk.t);
       const int cols = columns(tile);
@@ -641,6 +666,24 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
         tc_fence_after();
       }
       const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kMaxN;
+      if (kUse != kWeightGrad && splits > 1) {
+        if (split > 0) {
+          for (int c = c0; c < cols; c += 64) {
+            float z[32];
+            tmem_load_32x32(acc + c, z);
+            tmem_wait_load(z);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              shared_store16(part + (c - c0) * 64 + j * 512,
+                             make_uint4(__float_as_uint(z[4 * j]), __float_as_uint(z[4 * j + 1]),
+                                        __float_as_uint(z[4 * j + 2]), __float_as_uint(z[4 * j + 3])));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&s_parts), rank));
+          break;
+        }
+        if (!warp_wait(smem_addr(&s_parts), 0, gave_up)) break;
+      }
       for (int c = c0; c < cols; c += 64) {
         const int64_t row = tile.lo + c;
         float z[32];
@@ -650,6 +693,13 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) z[j] = 0.f;
+        }
+        if (kUse != kWeightGrad && splits > 1) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 x = cluster_load4(other_part + (c - c0) * 64 + j * 512);
+            z[4 * j] += x.x, z[4 * j + 1] += x.y, z[4 * j + 2] += x.z, z[4 * j + 3] += x.w;
+          }
         }
         if (kUse == kGated) {
           // The warp's 32 lanes: 16 gate rows, then the up rows of the same
@@ -699,7 +749,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // the pair's products, loads and arrivals are over in both blocks
+  cluster_sync();  // the products, loads, arrivals and reads of the cluster are over
   tc_fence_after();
   if (threadIdx.x == 0 && *gave_up != 0 && a.status != nullptr)
     atomicOr(a.status, MOE_FLAG_BARRIER_TIMEOUT);

@@ -45,9 +45,9 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Launch with programmatic stream serialization: the grid may be scheduled as
 // soon as the previous grid in the stream allows it; every kernel here calls
 // griddepcontrol.wait before it touches memory a previous grid may write.
-// cluster_z: blocks of a cluster along z, for kernels that name no cluster.
+// cluster: blocks of a cluster.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kern)(KArgs...), dim3 grid, unsigned cluster_z, unsigned block,
+cudaError_t launch_clusters(void (*kern)(KArgs...), dim3 grid, dim3 cluster, unsigned block,
                             size_t smem, cudaStream_t stream, Args... args) {
   if (smem > 48 * 1024) {
     const cudaError_t err =
@@ -65,18 +65,18 @@ cudaError_t launch_clusters(void (*kern)(KArgs...), dim3 grid, unsigned cluster_
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 1;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = cluster_z;
+  attr[1].val.clusterDim.x = cluster.x;
+  attr[1].val.clusterDim.y = cluster.y;
+  attr[1].val.clusterDim.z = cluster.z;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster_z > 1 ? 2 : 1;
+  cfg.numAttrs = cluster.x * cluster.y * cluster.z > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch(void (*kern)(KArgs...), dim3 grid, unsigned block, size_t smem,
                    cudaStream_t stream, Args... args) {
-  return launch_clusters(kern, grid, 1, block, smem, stream, args...);
+  return launch_clusters(kern, grid, dim3(1), block, smem, stream, args...);
 }
 
 }  // namespace experts

@@ -110,15 +110,19 @@ bool make_gated_map(CUtensorMap* map, const void* base, int64_t E, int64_t F, in
   return make_map_nd<T, 4>(map, base, {K, F, 2, E}, {K, F * K, 2 * F * K}, {64, 16, 2, 1});
 }
 
-// The most tiles a product may have.
+// The most tiles a product may have, of at most `columns` columns each.
 template <int kUse>
-int64_t most_tiles(const ProductArgs& a) {
+int64_t most_tiles(const ProductArgs& a, int columns) {
   const int64_t m = kUse == kForward || kUse == kWeightGrad ? a.N : kUse == kGated ? a.N / 2 : a.K;
-  constexpr int cap_least = kMaxN - 16 * (kCaps - 1);
-  const int64_t columns = kUse == kWeightGrad
-                              ? a.E * ceil_div(a.K, kMaxN)
-                              : a.num_rows / cap_least + std::min<int64_t>(a.E, a.num_rows);
-  return ceil_div(m, m_step<kUse>()) * columns;
+  const int64_t blocks = kUse == kWeightGrad ? a.E * ceil_div(a.K, kMaxN)
+                         : a.E == 1          ? ceil_div(a.num_rows, columns)
+                                    : a.num_rows / columns + std::min<int64_t>(a.E, a.num_rows);
+  return ceil_div(m, m_step<kUse>()) * blocks;
+}
+
+// Pairs that share a tile, each with 4 slices at least.
+int tile_splits(int64_t tiles, int64_t slices, int64_t pairs) {
+  return tiles * kMaxSplits <= pairs && slices >= 4 * kMaxSplits ? kMaxSplits : 1;
 }
 
 // lhs: the weight, or dz for d_weight; rhs: the rows, or dz for d_rows.
@@ -143,17 +147,22 @@ cudaError_t launch_product(const ProductArgs& a, const void* lhs, const void* rh
          make_map<T>(&map_b_large, rhs, 0, a.num_rows, depth, 128);
   }
   if (!ok) return cudaErrorInvalidValue;
-  const int64_t tiles = most_tiles<kUse>(a);
+  const int64_t pairs = sms / 2;
+  const int splits = kUse == kWeightGrad
+                         ? 1
+                         : tile_splits(most_tiles<kUse>(a, kMaxN),
+                                       ceil_div(kUse == kRowsGrad ? a.N : a.K, kSlice), pairs);
+  const int64_t tiles = most_tiles<kUse>(a, splits > 1 ? kMaxN : kLeastCap);
   if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
-  return launch(k_expert_product<T, kUse>,
-                dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, sms / 2))), kProductThreads,
-                product_smem(a.E), s, map_a, map_b, map_b_large, a);
+  const unsigned blocks = 2 * splits * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
+  return launch_clusters(k_expert_product<T, kUse>, dim3(blocks), dim3(2 * splits),
+                         kProductThreads, product_smem(a.E), s, map_a, map_b, map_b_large, a);
 }
 
 template <typename T, int kUse>
 cudaError_t launch_forward(const ProductArgs& a, const void* weight, const void* rows, int sms,
                            cudaStream_t s) {
-  if (!decode_pays(a.num_rows, a.K, most_tiles<kUse>(a), sms / 2))
+  if (!decode_pays(a.num_rows, a.E, a.K, most_tiles<kUse>(a, 64), sms / 2))
     return launch_product<T, kUse>(a, weight, rows, sms, s);
   constexpr bool kGatedForm = kUse == kGated;
   // Tasks at most: every expert with rows has one group, and each further
@@ -193,7 +202,7 @@ cudaError_t launch_bias_grad(const void* dz, const int64_t* offset, int E, int64
                              int64_t N, void* d_bias, int sms, cudaStream_t s) {
   const int64_t blocks = ceil_div(N, 64);
   const unsigned splits = blocks * E <= sms ? kBiasSplit : 1;
-  return launch_clusters(k_bias_grad<T>, dim3(static_cast<unsigned>(blocks), E, splits), splits,
+  return launch_clusters(k_bias_grad<T>, dim3(static_cast<unsigned>(blocks), E, splits), dim3(1, 1, splits),
                          kGradThreads, 0, s, static_cast<const T*>(dz), offset, num_rows, N,
                          static_cast<T*>(d_bias));
 }

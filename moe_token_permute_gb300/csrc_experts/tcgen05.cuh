@@ -63,6 +63,19 @@ __device__ __forceinline__ float cluster_load(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -222,13 +235,13 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1 : 0)
       : "memory");
 }
-// The barrier at this address in both blocks gets one arrival when every
-// tcgen05.mma issued before is done.
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
+// The barrier at this address in the cluster's blocks of `mask` (the pair) gets one
+// arrival when every tcgen05.mma issued before is done.
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint16_t mask) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
       "[%0], %1;" ::"r"(bar),
-      "h"(static_cast<uint16_t>(3))
+      "h"(mask)
       : "memory");
 }
 
