@@ -74,12 +74,15 @@ constexpr int kDecodeMaxRows = 32;
 //   linear 1 x 4096 -> 4096, 8 / 16 / 24 rows   12 / 16    18 / 16    25 / 16
 //   gated 128 x 2048 -> 768, 8 / 16 / 32 rows   14 / 17    21 / 19    29 / 27
 //   linear 128 x 768 -> 2048, 8 / 32 rows    24 / 11    57 / 17
-// A task costs about 0.7 us beside its loads, so it needs a long contraction;
-// of 2048 values it pays while the large tiles do not fill the pairs.  More than 8
-// rows of one expert read its weights again.
-inline bool decode_pays(int64_t rows, int64_t E, int64_t K, int64_t tiles, int64_t pairs) {
+//   linear 8 x 2048 -> 1024, 8 rows          14 / 11
+// A task costs about 0.7 us beside its loads, so its weights have to be long; of 64
+// KB they pay while the large tiles do not fill the pairs.  More than 8 rows of
+// one expert read its weights again.
+inline bool decode_pays(bool gated, int64_t rows, int64_t E, int64_t K, int64_t tiles,
+                        int64_t pairs) {
+  const int64_t task_bytes = (gated ? 2 : 1) * kDecodeFeatures * K * 2;
   return rows <= std::min<int64_t>(kDecodeMaxRows, kDecodeGroup * E) && K % 64 == 0 &&
-         (K >= 4096 || (K >= 2048 && tiles <= pairs));
+         (task_bytes >= 128 * 1024 || (task_bytes >= 64 * 1024 && tiles <= pairs));
 }
 
 template <typename T>

@@ -310,7 +310,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_done[2], s_free[2],
       s_clear[kStages], s_tail[kStages], s_parts;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_gave_up, s_scan[32], s_blocks[kCaps + 1], s_cap;
+  __shared__ int s_gave_up, s_cap;
 
   uint8_t* stages = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -343,68 +343,31 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     tma_prefetch_map(&map_b);
     if (!kBMn) tma_prefetch_map(&map_b_large);
   }
-  if (threadIdx.x <= kCaps) s_blocks[threadIdx.x] = 0;
+  __syncthreads();
+  cluster_arrive();  // this block's barriers exist
   if (warp == kEpiWarps + 1) tmem_alloc(smem_addr(&s_tmem), 512);
   pdl_wait();
-  __syncthreads();
 
   const int F = static_cast<int>(a.N / 2);
   const int m_size = static_cast<int>(kUse == kForward ? a.N : kUse == kGated ? F
                                       : kUse == kRowsGrad ? a.K : a.N);
+  const int m_blocks = (m_size + m_step<kUse>() - 1) / m_step<kUse>();
   const int n_blocks = static_cast<int>((a.K + kMaxN - 1) / kMaxN);  // d_weight
   const int k_size = static_cast<int>(kUse == kRowsGrad ? a.N : a.K);
+  const int all_slices = (k_size + kSlice - 1) / kSlice;
 
-  // The experts' rows, and in how many blocks of each size they are cut;
-  // s_blocks[kCaps]: all rows.
-  bool bad = false;
-  for (int e0 = 0; e0 < a.E; e0 += kProductThreads) {
-    const int e = e0 + threadIdx.x;
-    int rows = 0;
-    if (e < a.E) {
-      bool b;
-      const Segment s = segment(a.offset, e, a.num_rows, &b);
-      bad |= b;
-      segments[e] = s;
-      rows = s.hi - s.lo;
-    }
-    if (kUse != kWeightGrad && __any_sync(kFullMask, rows > 0)) {
-#pragma unroll
-      for (int i = 0; i < kCaps; ++i) {
-        const int n = __reduce_add_sync(kFullMask, row_blocks(rows, cap_of(i)));
-        if (lane == 0) atomicAdd(&s_blocks[i], n);
-      }
-      const int n = __reduce_add_sync(kFullMask, rows);
-      if (lane == 0) atomicAdd(&s_blocks[kCaps], n);
-    }
+  for (int e = threadIdx.x; e < a.E; e += kProductThreads) {
+    bool bad;
+    segments[e] = segment(a.offset, e, a.num_rows, &bad);
+    if (bad && a.status != nullptr && blockIdx.x == 0)
+      atomicOr(a.status, MOE_FLAG_OFFSET_OUT_OF_RANGE);
   }
-  if (a.status != nullptr && blockIdx.x == 0 && bad)
-    atomicOr(a.status, MOE_FLAG_OFFSET_OUT_OF_RANGE);
   __syncthreads();
-  const int m_blocks = (m_size + m_step<kUse>() - 1) / m_step<kUse>();
-  int cap = kMaxN;
-  if (kUse != kWeightGrad && splits == 1) {
-    if (warp == 0) {
-      float cost = INFINITY;
-      if (lane == 0 || (lane < kCaps && s_blocks[0] < (6 * pairs + m_blocks - 1) / m_blocks))
-        cost = cap_cost(s_blocks[lane], s_blocks[kCaps], m_blocks, (k_size + kSlice - 1) / kSlice,
-                        pairs);
-      float best = cost;
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) best = fminf(best, __shfl_xor_sync(kFullMask, best, d));
-      const unsigned at = __ballot_sync(kFullMask, cost == best);
-      if (lane == 0) s_cap = cap_of(__ffs(at) - 1);
-    }
-    __syncthreads();
-    cap = s_cap;
-  }
-  // Tiles of each expert, and the sum before it.
-  int total = 0;
   if (kUse == kWeightGrad) {
     // A tile costs its expert's rows: the experts go by falling rows, and the
     // pairs take the tiles to and fro (Walk), so that each gets its share of the
     // long ones (Zipf 1.2 over 128 experts: the longest pair 1.4% over the average
     // instead of 14%).
-    total = a.E * m_blocks * n_blocks;
     for (int e = threadIdx.x; e < a.E; e += kProductThreads) {
       const int rows = segments[e].hi - segments[e].lo;
       int before = 0;
@@ -414,23 +377,60 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       }
       first[before] = e;
     }
-  } else {
-    for (int e0 = 0; e0 < a.E; e0 += kProductThreads) {
-      const int e = e0 + threadIdx.x;
-      const int n = e < a.E ? row_blocks(segments[e].hi - segments[e].lo, cap) * m_blocks : 0;
-      int part;
-      const int before = block_exclusive_sum(n, s_scan, &part);
-      if (e < a.E) first[e] = total + before;
-      total += part;
+  } else if (warp == 0) {
+    // In how many blocks of each size the experts' rows are cut; the choice; and
+    // each expert's first tile.
+    int cap = kMaxN;
+    if (splits == 1) {
+      int blocks[kCaps] = {}, all = 0;
+      for (int e = lane; e < a.E; e += 32) {
+        const int rows = segments[e].hi - segments[e].lo;
+        all += rows;
+#pragma unroll
+        for (int i = 0; i < kCaps; ++i) blocks[i] += row_blocks(rows, cap_of(i));
+      }
+      all = __reduce_add_sync(kFullMask, all);
+      int mine = 0, most = 0;  // lane i: with cap_of(i)
+#pragma unroll
+      for (int i = 0; i < kCaps; ++i) {
+        const int n = __reduce_add_sync(kFullMask, blocks[i]);
+        if (i == 0) most = n;
+        if (lane == i) mine = n;
+      }
+      float cost = INFINITY;
+      if (lane == 0 || (lane < kCaps && most < (6 * pairs + m_blocks - 1) / m_blocks))
+        cost = cap_cost(mine, all, m_blocks, all_slices, pairs);
+      float best = cost;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) best = fminf(best, __shfl_xor_sync(kFullMask, best, d));
+      cap = cap_of(__ffs(__ballot_sync(kFullMask, cost == best)) - 1);
     }
-    if (threadIdx.x == 0) first[a.E] = total;
-    // (More only where bad offsets make segments overlap.)
-    if (splits > 1) total = min(total, pairs);
+    int before = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int n = e < a.E ? row_blocks(segments[e].hi - segments[e].lo, cap) * m_blocks : 0;
+      int sum = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(kFullMask, sum, d);
+        if (lane >= d) sum += x;
+      }
+      if (e < a.E) first[e] = before + sum - n;
+      before += __shfl_sync(kFullMask, sum, 31);
+    }
+    if (lane == 0) {
+      first[a.E] = before;
+      s_cap = cap;
+    }
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // both blocks' barriers exist before either's loads or arrivals
+  cluster_wait();  // the other blocks' barriers exist too
   tc_fence_after();
+  const int cap = s_cap;
+  int total = kUse == kWeightGrad ? a.E * m_blocks * n_blocks : first[a.E];
+  // (More tiles than pairs only where bad offsets make segments overlap.)
+  if (splits > 1) total = min(total, pairs);
   const uint32_t tmem = s_tmem;
   volatile int* gave_up = &s_gave_up;
 
@@ -470,7 +470,6 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   };
   // Slices of the contraction (d_weight: of the expert's rows), from first_slice on
   // in pairs that share it.
-  const int all_slices = (k_size + kSlice - 1) / kSlice;
   const int first_slice = all_slices * split / splits;
   auto slices = [&](const Tile& t) {
     return kUse == kWeightGrad ? (t.rows + kSlice - 1) / kSlice

@@ -162,9 +162,9 @@ cudaError_t launch_product(const ProductArgs& a, const void* lhs, const void* rh
 template <typename T, int kUse>
 cudaError_t launch_forward(const ProductArgs& a, const void* weight, const void* rows, int sms,
                            cudaStream_t s) {
-  if (!decode_pays(a.num_rows, a.E, a.K, most_tiles<kUse>(a, 64), sms / 2))
-    return launch_product<T, kUse>(a, weight, rows, sms, s);
   constexpr bool kGatedForm = kUse == kGated;
+  if (!decode_pays(kGatedForm, a.num_rows, a.E, a.K, most_tiles<kUse>(a, 64), sms / 2))
+    return launch_product<T, kUse>(a, weight, rows, sms, s);
   // Tasks at most: every expert with rows has one group, and each further
   // kDecodeGroup rows one more.
   const int64_t groups = std::min<int64_t>(a.E, a.num_rows) + a.num_rows / kDecodeGroup;
