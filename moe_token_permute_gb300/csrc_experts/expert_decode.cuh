@@ -150,6 +150,7 @@ k_expert_decode(const __grid_constant__ CUtensorMap map, const T* __restrict__ x
     tma_prefetch_map(&map);
   }
   pdl_wait();
+  pdl_launch_dependents();
   int groups = 0;
   bool bad = false;
   for (int e0 = 0; e0 < a.E; e0 += kDecodeThreads) {

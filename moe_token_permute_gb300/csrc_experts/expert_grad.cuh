@@ -23,6 +23,7 @@ k_act_grad(const T* __restrict__ d_out, const T* __restrict__ z, T* __restrict__
            const int64_t* __restrict__ offset, int E, int64_t num_rows, int64_t W) {
   constexpr int kRows = 2;
   pdl_wait();
+  pdl_launch_dependents();
   const int64_t n = rows_in_use(offset, E, num_rows);
   const int64_t c = static_cast<int64_t>(blockIdx.y) * 32 + (threadIdx.x & 31);
   if (c >= W / 8) return;
@@ -74,6 +75,7 @@ k_bias_grad(const T* __restrict__ dz, const int64_t* __restrict__ offset, int64_
             int64_t N, T* __restrict__ d_bias) {
   constexpr int kAhead = 8;
   pdl_wait();
+  pdl_launch_dependents();
   __shared__ float part[32][64 + 1];
   __shared__ float sums[64];
   const int e = blockIdx.y;

@@ -347,6 +347,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   cluster_arrive();  // this block's barriers exist
   if (warp == kEpiWarps + 1) tmem_alloc(smem_addr(&s_tmem), 512);
   pdl_wait();
+  pdl_launch_dependents();
 
   const int F = static_cast<int>(a.N / 2);
   const int m_size = static_cast<int>(kUse == kForward ? a.N : kUse == kGated ? F

@@ -37,6 +37,7 @@ k_unpermute_backward(const VecT* __restrict__ d_out, const VecT* rows, int64_t n
   constexpr int kE = BfVec<VecT>::kElems;
   constexpr int V = kCombineAhead;
   pdl_wait();
+  pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5)) * per_warp;
   // Lane l: item i0 + l, whose row is p_lane.
