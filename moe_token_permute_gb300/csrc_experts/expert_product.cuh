@@ -406,21 +406,26 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       for (int d = 16; d > 0; d >>= 1) best = fminf(best, __shfl_xor_sync(kFullMask, best, d));
       cap = cap_of(__ffs(__ballot_sync(kFullMask, cost == best)) - 1);
     }
-    int before = 0;
+    // The host has made sure that the tiles of num_rows rows can be counted; where
+    // bad offsets make segments overlap, those beyond kMostTiles are left out.
+    constexpr int64_t kMostTiles = INT32_MAX / 2;
+    int64_t before = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
-      const int n = e < a.E ? row_blocks(segments[e].hi - segments[e].lo, cap) * m_blocks : 0;
-      int sum = n;
+      const int64_t n = e < a.E ? static_cast<int64_t>(
+                                      row_blocks(segments[e].hi - segments[e].lo, cap)) * m_blocks
+                                : 0;
+      int64_t sum = n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int x = __shfl_up_sync(kFullMask, sum, d);
+        const int64_t x = __shfl_up_sync(kFullMask, sum, d);
         if (lane >= d) sum += x;
       }
-      if (e < a.E) first[e] = before + sum - n;
+      if (e < a.E) first[e] = static_cast<int>(min(kMostTiles, before + sum - n));
       before += __shfl_sync(kFullMask, sum, 31);
     }
     if (lane == 0) {
-      first[a.E] = before;
+      first[a.E] = static_cast<int>(min(kMostTiles, before));
       s_cap = cap;
     }
   }

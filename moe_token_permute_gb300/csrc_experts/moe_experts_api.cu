@@ -153,7 +153,7 @@ cudaError_t launch_product(const ProductArgs& a, const void* lhs, const void* rh
                          : tile_splits(most_tiles<kUse>(a, kMaxN),
                                        ceil_div(kUse == kRowsGrad ? a.N : a.K, kSlice), pairs);
   const int64_t tiles = most_tiles<kUse>(a, splits > 1 ? kMaxN : kLeastCap);
-  if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
   const unsigned blocks = 2 * splits * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
   return launch_clusters(k_expert_product<T, kUse>, dim3(blocks), dim3(2 * splits),
                          kProductThreads, product_smem(a.E), s, map_a, map_b, map_b_large, a);

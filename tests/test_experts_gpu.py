@@ -352,6 +352,82 @@ def test_matrices_beyond_32_bit_element_offsets():
     ref.check(dw[2:], want, BF, "d_weight of the last expert")
 
 
+# ---- the other ways a product is cut ---------------------------------------
+# Few rows and a long contraction stream the weights (k_expert_decode); few tiles
+# are shared by two pairs of SMs; few waves of tiles are cut narrower.
+
+STREAMED = {
+    "one": [1], "eight": [8], "spread": [1, 0, 2, 1, 0, 8, 5, 1], "crowded": [9, 0, 17, 6],
+    "most": [20, 12, 0, 0], "empty": [0, 0],
+}
+
+
+@pytest.mark.parametrize("K", [2048, 2112, 4096, 4160])
+@pytest.mark.parametrize("counts", STREAMED, ids=str)
+def test_few_rows(counts, K):
+    dtype = (BF, HF)[K // 64 % 2]
+    tail = 3 if counts == "spread" else 0
+    run_gated(STREAMED[counts], K, 40, dtype, "silu", seed=20, tail=tail, train=False)
+    run_linear(STREAMED[counts], K, 72, dtype, "gelu", 21, True, True, tail=tail)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_few_rows_an_experts_infinities_stay_with_it(bad):
+    counts, K = [3, 5, 2], 4096
+    g, n, offset, x, w = setup(counts, K, 80, BF, 22)
+    outs = []
+    for name in ("clean", "bad"):
+        if name == "bad":
+            x[3:8], w[1] = bad, bad
+        h, y = blank(n, 40, dtype=BF), blank(n, 80, dtype=BF)
+        mp.moe_expert_gated(x, w, offset, h)
+        mp.moe_expert_linear(x, w, offset, y)
+        outs.append([torch.cat([t[:3], t[8:]]) for t in (h, y)])
+    for a, c in zip(*outs):
+        assert torch.isfinite(a.float()).all() and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("rows", [9, 33, 100, 255, 256, 257, 300])
+@pytest.mark.parametrize("K", [512, 520, 1096])
+def test_few_tiles(rows, K):
+    """One expert: half of the contraction in each of two pairs."""
+    dtype = (BF, HF)[rows % 2]
+    run_gated([rows], K, 520, dtype, "silu", seed=23)
+    run_linear([rows], K, 520, dtype, "gelu", 24, True, True, tail=rows % 3)
+
+
+@pytest.mark.parametrize("counts,N", [([1900], 2048), ([500], 4096), ([700, 0, 90, 1200], 1024),
+                                      ([60] * 40, 512)], ids=str)
+def test_few_waves(counts, N):
+    run_linear(counts, 264, N, BF, "none", 25, False, False)
+
+
+def test_many_experts():
+    """As many as there may be, most of them without rows."""
+    E = mp.MOE_MAX_LOCAL_EXPERTS
+    counts = [0] * E
+    for e, n in ((0, 3), (1, 130), (511, 1), (700, 40), (E - 1, 7)):
+        counts[e] = n
+    run_gated(counts, 72, 24, BF, "silu", seed=26, tail=5)
+    run_linear(counts, 72, 24, HF, "relu", 27, True, False)
+    few = [0] * E
+    few[3], few[E - 1] = 4, 9
+    run_gated(few, 2048, 16, BF, "silu", seed=28, train=False)
+
+
+@pytest.mark.parametrize("n,K,E", [(30, 4096, 4), (100, 1024, 1)])
+def test_bad_offsets_are_flagged_however_the_product_is_cut(n, K, E):
+    _, _, _, x, w = setup([n] + [0] * (E - 1), K, 64, BF, 29)
+    ws = torch.zeros(mp.moe_permute_workspace_size(1, 1, 1), dtype=torch.uint8, device=DEV)
+    mp.moe_permute_workspace_init(ws)
+    for bad in ([0, n, 0, n, n], [0, 2 ** 40, 5, 0, -3], [-1, n + 1, 0, n, 0]):
+        offset = torch.tensor(bad[:E + 1] if E > 1 else [bad[0], bad[1] + 1], device=DEV)
+        y = blank(n, 64, dtype=BF)
+        mp.moe_expert_linear(x, w, offset, y, workspace=ws)
+        assert mp.moe_read_status(ws) == mp.MOE_FLAG_OFFSET_OUT_OF_RANGE
+        mp.moe_clear_status(ws)
+
+
 # ---- moe_unpermute's gradient ----------------------------------------------
 
 def run_combine(T, K, E, H, seed, local=None, off=0):
