@@ -1,19 +1,18 @@
 // expert_decode.cuh -- the forward products of a few rows (decoding): the
 // weights of the experts that have rows are streamed once, and that is the time.
 //
-// The tiles of expert_product.cuh would leave most of the GPU idle here: 512
-// features per pair of SMs make 24 tiles of eight experts' 768 features.  Here
-// the work is cut into tasks of 8 features (8 weight rows; gated: 8 gate and 8 up
-// rows) times up to 8 rows of x, and each SM takes every 152nd task (768 in that
-// example).
+// The tiles of expert_product.cuh are 128 or 256 features of a pair of SMs: eight
+// experts' 2 x 768 features make 48 of them.  Here the work is cut into tasks of 8
+// features (8 weight rows; gated: 8 gate and 8 up rows) times up to 8 rows of x, and
+// each SM takes every 152nd task (768 in that example).
 //
 //   warps 0-15  consumers: two sets of 8 take turns with the stages, the warps
 //               of a set share the stage's part of the contraction
 //   warp 16     producer
 //   warp 17     adds the 16 partial sums up, epilogue
 // Everything comes through one ring per SM that runs on from task to task, so
-// loads never pause (96 or 128 KB of weights in flight); the sums of a task are joined
-// while the next is computed.  A stage's weights are one TMA tile (gated: two) of
+// loads never pause (96 or 128 KB of weights in flight); the sums of a task are
+// joined while the next is computed.  A stage's weights are one TMA tile (gated: two) of
 // 64 x 8 rows x 16 values, K being read as K/64 blocks: a copy per row instead kept
 // the producer at 84 cycles a copy, and the memory at 5.4 of 6.7 TB/s.  Rows of x,
 // few, are bulk copies 64 bytes apart modulo 128, and the tiles are in the 128-byte
@@ -23,9 +22,13 @@
 // loads; tcgen05's smallest tile is 64 weight rows.  The sum over k may be taken
 // in any order, so the fragments are not loaded in the instruction's own k
 // order: lane (g, q) loads 16 consecutive bytes (8 k-values) of weight row g and
-// of row g of x, the even and then the odd ones of 128, and two instructions take two words of each.  Gated: rows 8-15 of the
-// instruction's tile are the up rows, so that a thread has both of a feature;
-// linear: they are zero (16 features per task would balance worse).
+// of row g of x, first the even and then the odd ones of a line of 128, and two
+// instructions take two words of each.  Gated: rows 8-15 of the instruction's tile
+// are the up rows, so that a thread has both of a feature; linear: they are zero
+// (16 features per task would balance worse).
+// On GB300: 2 rows of 8 x [14336 -> 4096] 40 us, 5.8 TB/s (87% of the measured copy
+// bandwidth); 8 rows of 128 x [2048 -> 2 x 768] 13.8 us for 7.5 us of weights: 5.05
+// tasks per SM are 6 rounds, and about 4 us pass before the first loads arrive.
 #pragma once
 
 #include <algorithm>
@@ -65,24 +68,23 @@ struct DecodeShape {
 // Rows up to which these kernels are used; a call has no more groups than rows.
 constexpr int kDecodeMaxRows = 32;
 
-// Which calls: at most `tiles` of the large products' tiles against `pairs` of
-// SMs to fill.  us, this kernel / large tiles, measured on GB300 (E experts, in
-// -> features):
-//   gated 64 x 7168 -> 2048, 8 / 16 rows     72 / 77    112 / 131
-//   gated 8 x 4096 -> 14336, 2 / 8 rows      71 / 83    167 / 180
-//   linear 8 x 14336 -> 4096, 2 / 32 rows    41 / 92    147 / 152
-//   linear 1 x 4096 -> 4096, 8 / 16 / 24 rows   12 / 16    18 / 16    25 / 16
-//   gated 128 x 2048 -> 768, 8 / 16 / 32 rows   14 / 17    21 / 19    29 / 27
-//   linear 128 x 768 -> 2048, 8 / 32 rows    24 / 11    57 / 17
-//   linear 8 x 2048 -> 1024, 8 rows          14 / 11
-// A task costs about 0.7 us beside its loads, so its weights have to be long; of 64
-// KB they pay while the large tiles do not fill the pairs.  More than 8 rows of
-// one expert read its weights again.
-inline bool decode_pays(bool gated, int64_t rows, int64_t E, int64_t K, int64_t tiles,
-                        int64_t pairs) {
+// Which calls.  us, this kernel / large tiles, on GB300 (E experts, in -> features):
+//   gated 64 x 7168 -> 2048, 8 / 16 / 32 rows    72 / 78    110 / 119    212 / 230
+//   gated 8 x 4096 -> 14336, 2 / 8 / 32 rows     70 / 74    164 / 179    260 / 272
+//   gated 128 x 2048 -> 768, 8 / 16 / 32 rows    14 / 15     22 / 23      29 / 29
+//   linear 8 x 14336 -> 4096, 2 / 8 / 32 rows    41 / 44     89 / 132    141 / 149
+//   linear 8 x 4096 -> 4096, 2 / 8 rows          15 / 15     33 / 43
+//   linear 1 x 4096 -> 4096, 1 / 8 / 16 rows     11 / 13     12 / 13      18 / 13
+//   linear 64 x 2048 -> 7168, 8 rows             75 / 42
+//   linear 128 x 768 -> 2048, 8 / 32 rows        23 / 11     56 / 17
+// A task costs about 0.7 us beside its loads, so its weights have to be long; more
+// than 8 rows of one expert read its weights again.
+inline bool decode_pays(bool gated, int64_t rows, int64_t E, int64_t K) {
   const int64_t task_bytes = (gated ? 2 : 1) * kDecodeFeatures * K * 2;
-  return rows <= std::min<int64_t>(kDecodeMaxRows, kDecodeGroup * E) && K % 64 == 0 &&
-         (task_bytes >= 128 * 1024 || (task_bytes >= 64 * 1024 && tiles <= pairs));
+  const int64_t most = task_bytes >= 128 * 1024  ? kDecodeMaxRows
+                       : task_bytes >= 64 * 1024 ? kDecodeMaxRows / 2
+                                                 : 0;
+  return rows <= std::min<int64_t>(most, kDecodeGroup * E) && K % 64 == 0;
 }
 
 template <typename T>

@@ -23,8 +23,10 @@
 // cycle, all there is.  (A block on its own, without the pair, would need 160.
 // Two A tiles per block need 112, but fill tensor memory, and then every tile's
 // epilogue holds the products up: Qwen3-shaped training 5% slower, many experts of
-// 128 rows 1% faster.)  Large products run at the power limit: 1.87 PFLOP/s in
-// bursts of 1 ms, Mixtral-shaped gated T = 4096.
+// 128 rows 1% faster.)  Large products run at the power limit: Mixtral-shaped
+// gated T = 4096 at 1.87 PFLOP/s in a burst and 1.60 over seconds.  With few rows
+// per expert the weights' way from memory bounds it: Qwen3-shaped gated T = 64 at
+// 6.2 TB/s.
 // The grid is persistent; tiles are numbered expert by expert, in panels.
 // Where the tiles are at most half as many as the pairs (a dense layer and few
 // rows), two pairs make a cluster and share a tile's contraction: each takes half
@@ -98,10 +100,9 @@ __host__ __device__ constexpr int m_step() { return kUse == kGated ? 128 : 256; 
 
 // The most columns of a tile, chosen for the rows there are.  Six waves of tiles
 // and more are cut into 256.  Below, fewer columns can fill the waves better, but a
-// slice costs 256 + columns cycles (its traffic
-// in shared memory) whether or not the products need them, and a tile about 700 to
-// its first product.  Dense 4096 -> 4096: 500 rows 25 us in blocks of 128 and 31 of
-// 256, 8191 rows 238 and 166.
+// slice costs 256 + columns cycles (its traffic in shared memory) whether or not the
+// products need them, and a tile about 700 to its first product.  Dense 4096 ->
+// 4096: 500 rows 25 us in blocks of 128 and 31 of 256, 8191 rows 238 and 166.
 constexpr int kCaps = 13;  // 256, 240, ..., 64
 constexpr int kLeastCap = kMaxN - 16 * (kCaps - 1);
 __device__ __forceinline__ int cap_of(int i) { return kMaxN - 16 * i; }
@@ -114,7 +115,8 @@ __device__ __forceinline__ float cap_cost(int blocks, int rows, int m_blocks, in
 // Tile `local` of an expert's m_blocks x n_blocks, in panels of kPanel column
 // blocks, all of a panel's row blocks after one another: the tiles that run at the
 // same time make a square of about kPanel x 76 / kPanel, whose operands together
-// are small enough to be shared through L2.
+// are small enough to be shared through L2 (dense 4096 -> 4096, 16384 rows: 333 us
+// instead of 389 with all column blocks in one panel).
 constexpr int kPanel = 8;
 __device__ __forceinline__ void place_in_panels(int local, int m_blocks, int n_blocks, int& m,
                                                 int& n) {

@@ -163,7 +163,7 @@ template <typename T, int kUse>
 cudaError_t launch_forward(const ProductArgs& a, const void* weight, const void* rows, int sms,
                            cudaStream_t s) {
   constexpr bool kGatedForm = kUse == kGated;
-  if (!decode_pays(kGatedForm, a.num_rows, a.E, a.K, most_tiles<kUse>(a, 64), sms / 2))
+  if (!decode_pays(kGatedForm, a.num_rows, a.E, a.K))
     return launch_product<T, kUse>(a, weight, rows, sms, s);
   // Tasks at most: every expert with rows has one group, and each further
   // kDecodeGroup rows one more.

@@ -358,11 +358,11 @@ def test_matrices_beyond_32_bit_element_offsets():
 
 STREAMED = {
     "one": [1], "eight": [8], "spread": [1, 0, 2, 1, 0, 8, 5, 1], "crowded": [9, 0, 17, 6],
-    "most": [20, 12, 0, 0], "empty": [0, 0],
+    "most": [20, 12, 0, 0], "few": [1, 0, 3, 2, 0, 4], "empty": [0, 0],
 }
 
 
-@pytest.mark.parametrize("K", [2048, 2112, 4096, 4160])
+@pytest.mark.parametrize("K", [2048, 2112, 4096, 4160, 8256])
 @pytest.mark.parametrize("counts", STREAMED, ids=str)
 def test_few_rows(counts, K):
     dtype = (BF, HF)[K // 64 % 2]
