@@ -25,6 +25,7 @@
  *    and raise MOE_FLAG_OFFSET_OUT_OF_RANGE.
  *  - workspace is optional (may be NULL): only its status word is used.
  *  - Results do not depend on timing: no atomic adds.
+ *  - Outputs overlap no other buffer of the call, except where noted.
  */
 #ifndef MOE_EXPERTS_H
 #define MOE_EXPERTS_H

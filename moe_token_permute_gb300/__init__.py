@@ -1,10 +1,12 @@
-"""GB300 (sm_103a) MoE token permute / unpermute behind a C ABI.
+"""GB300 (sm_103a) MoE token permute / unpermute, the expert products between
+them and their gradients, behind a C ABI.
 
 The Python functions below carry the names of the C entry points declared in
-include/moe_permute.h and only marshal torch tensors into pointers and sizes;
-all work runs in libmoe_permute.so.  Every output buffer and the workspace are
-supplied by the caller, so no call allocates (vLLM PR #43014 digest,
-"implementation breakdown": scratch allocated once and reused).
+include/moe_permute.h and include/moe_experts.h and only marshal torch tensors
+into pointers and sizes; all work runs in libmoe_permute.so.  Every output
+buffer and the workspace are supplied by the caller, so no call allocates (vLLM
+PR #43014 digest, "implementation breakdown": scratch allocated once and
+reused).
 ``MoEPermuteScratch`` allocates such a set of buffers once, up front.
 """
 from __future__ import annotations

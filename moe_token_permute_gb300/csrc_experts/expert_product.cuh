@@ -66,6 +66,9 @@ struct ProductArgs {
   int64_t K, N;  // in_size and out_size of the weight [E, N, K]
   int E;
   int act;
+  // The launch before is another of the same call and reads what this one reads:
+  // nothing is waited for at the start, and that launch at the end.
+  bool beside_previous;
   const void* bias;
   const void* residual;
   void* out;
@@ -223,9 +226,7 @@ __device__ __forceinline__ void shared_store16(uint32_t addr, uint4 v) {
 
 // v, as tmem_load_32x32 gives it, rounded and written to the block.
 // kTranspose: tensor memory lanes are the block's columns; else its rows.
-// kStream: the result is not read again soon and should not displace the operands
-// in L2.
-template <bool kTranspose, bool kStream = false, typename T>
+template <bool kTranspose, typename T>
 __device__ __forceinline__ void write_block(const float (&v)[32], const Block<T>& b) {
   uint32_t p[16];
 #pragma unroll
@@ -245,11 +246,7 @@ __device__ __forceinline__ void write_block(const float (&v)[32], const Block<T>
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint4 x = shared_load16(b.line + j * 512);
-    if (8 * j < b.rows) {
-      uint4* to = reinterpret_cast<uint4*>(b.at + j * b.step);
-      if (kStream) __stcs(to, x);
-      else *to = x;
-    }
+    if (8 * j < b.rows) *reinterpret_cast<uint4*>(b.at + j * b.step) = x;
   }
 }
 
@@ -352,7 +349,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   __syncthreads();
   cluster_arrive();  // this block's barriers exist
   if (warp == kEpiWarps + 1) tmem_alloc(smem_addr(&s_tmem), 512);
-  pdl_wait();
+  if (!a.beside_previous) pdl_wait();
   pdl_launch_dependents();
 
   const int F = static_cast<int>(a.N / 2);
@@ -758,7 +755,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           write_block<true>(z, Block<T>(out, a.K, row, cols - c, m, a.K, stage));
         } else {
           const int64_t left = a.N - m;
-          write_block<false, true>(z, Block<T>(out, a.K, static_cast<int64_t>(tile.e) * a.N + m,
+          write_block<false>(z, Block<T>(out, a.K, static_cast<int64_t>(tile.e) * a.N + m,
                                          static_cast<int>(left < 32 ? (left < 0 ? 0 : left) : 32),
                                          tile.n0 + c, a.K, stage));
         }
@@ -777,6 +774,8 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   if (threadIdx.x == 0 && *gave_up != 0 && a.status != nullptr)
     atomicOr(a.status, MOE_FLAG_BARRIER_TIMEOUT);
   if (warp == kEpiWarps + 1) tmem_free(tmem, 512);
+  // What follows waits for this launch alone, so it ends after the one before.
+  if (a.beside_previous) pdl_wait();
 }
 
 }  // namespace experts

@@ -207,13 +207,16 @@ cudaError_t launch_bias_grad(const void* dz, const int64_t* offset, int E, int64
                          static_cast<T*>(d_bias));
 }
 
-// d_rows and d_weight of z = x W^T from dz.
+// d_rows and d_weight of z = x W^T from dz.  beside_previous: the launch before is
+// one of this call that only reads dz too.  The two products run beside one another
+// where the first leaves SMs free (at its end, or all along when it is small).
 template <typename T>
 cudaError_t product_gradients(const void* dz, const void* rows, const void* weight,
                               const int64_t* offset, int64_t num_rows, int64_t K, int64_t N,
-                              int E, void* d_rows, void* d_weight, unsigned* status, int sms,
-                              cudaStream_t s) {
+                              int E, void* d_rows, void* d_weight, bool beside_previous,
+                              unsigned* status, int sms, cudaStream_t s) {
   ProductArgs a = {};
+  a.beside_previous = beside_previous;
   a.offset = offset;
   a.num_rows = num_rows;
   a.K = K;
@@ -224,6 +227,7 @@ cudaError_t product_gradients(const void* dz, const void* rows, const void* weig
     a.out = d_rows;
     const cudaError_t err = launch_product<T, kRowsGrad>(a, weight, dz, sms, s);
     if (err != cudaSuccess) return err;
+    a.beside_previous = true;
   }
   if (d_weight != nullptr) {
     a.out = d_weight;
@@ -329,7 +333,7 @@ int moe_expert_gated_backward(const void* d_out, const void* permuted_rows, cons
   }
   auto gradients = bf ? product_gradients<__nv_bfloat16> : product_gradients<__half>;
   return finish(gradients(d_preact, permuted_rows, weight, expert_first_token_offset, num_rows,
-                          hidden_size, 2 * ffn_size, num_local_experts, d_rows, d_weight,
+                          hidden_size, 2 * ffn_size, num_local_experts, d_rows, d_weight, false,
                           status_of(workspace), sms, s));
 }
 
@@ -407,7 +411,8 @@ int moe_expert_linear_backward(const void* d_out, const void* rows, const void* 
   if (err != cudaSuccess) return finish(err);
   auto gradients = bf ? product_gradients<__nv_bfloat16> : product_gradients<__half>;
   return finish(gradients(dz, rows, weight, expert_first_token_offset, num_rows, in_size, out_size,
-                          num_local_experts, d_rows, d_weight, status_of(workspace), sms, s));
+                          num_local_experts, d_rows, d_weight, d_bias != nullptr,
+                          status_of(workspace), sms, s));
 }
 
 int moe_unpermute_backward(const void* d_out, const void* permuted_rows, int64_t num_rows,
