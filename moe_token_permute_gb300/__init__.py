@@ -222,7 +222,7 @@ def _matrix(t, rows, cols, dtype, what):
         return
     if t.dtype != dtype:
         raise ValueError(f"{what} is {t.dtype}; this call takes {dtype}")
-    if t.dim() < 2 or t.shape[-1] != cols or t.numel() != rows * cols:
+    if t.dim() < 2 or t.size(-1) != cols or t.numel() != rows * cols:
         raise ValueError(f"{what} must hold {rows} rows of {cols}; its shape is "
                          f"{tuple(t.shape)}")
 

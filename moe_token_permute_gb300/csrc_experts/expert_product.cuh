@@ -54,7 +54,7 @@ constexpr int kMaxSplits = 2;  // pairs of a cluster
 // (Mixtral-shaped linear training step, 1024 rows per expert: 1702 us; 1767 without
 // the delay, 1835 with the tail loaded last).
 constexpr int kTailDelay = 3;
-constexpr int kBoxRows = 32;   // rows of the small TMA box of a k-contiguous B; the large: 128
+constexpr int kBoxBytes = 64 * kSlice * 2;  // a TMA load of B: 64 rows or columns of a slice
 constexpr int kEpiWarps = 8;
 constexpr int kProductThreads = (kEpiWarps + 3) * 32;
 constexpr int kStagingWarpBytes = 32 * 64;  // 32 x 32 outputs of 16 bits
@@ -297,13 +297,12 @@ __device__ __forceinline__ void add_block(float (&v)[32], const uint4 (&x)[4], c
 }
 
 // map_a, map_b: the operands as TMA tiles of 64 contiguous values (128 bytes,
-// 128-byte swizzle) by 128 (forward A), 64 (MN-major) or kBoxRows rows; map_b_large
-// by 128.  map_a of the gated product: make_gated_map.
+// 128-byte swizzle) by 64 rows, A of the forward product by 128.  map_a of the gated
+// product: make_gated_map.
 template <typename T, int kUse>
 __global__ void __launch_bounds__(kProductThreads, 1)
 k_expert_product(const __grid_constant__ CUtensorMap map_a,
-                 const __grid_constant__ CUtensorMap map_b,
-                 const __grid_constant__ CUtensorMap map_b_large, const ProductArgs a) {
+                 const __grid_constant__ CUtensorMap map_b, const ProductArgs a) {
   constexpr bool kBf16 = sizeof(T) == 2 && !__is_same(T, __half);
   constexpr bool kAMn = kUse == kRowsGrad || kUse == kWeightGrad;
   constexpr bool kBMn = kUse == kWeightGrad;
@@ -344,7 +343,6 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     s_gave_up = 0;
     tma_prefetch_map(&map_a);
     tma_prefetch_map(&map_b);
-    if (!kBMn) tma_prefetch_map(&map_b_large);
   }
   __syncthreads();
   cluster_arrive();  // this block's barriers exist
@@ -519,11 +517,8 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       for (Walk walk(pair, pairs); walk.t < total && ok; walk.next()) {
         const Tile tile = tile_at(walk.t);
         const int n_slices = slices(tile), half_n = mma_n(columns(tile)) / 2;
-        const bool large = !kBMn && half_n > 64;
-        const int b_boxes = kBMn ? (half_n + 63) / 64
-                            : large ? 1 : (half_n + kBoxRows - 1) / kBoxRows;
-        const int box_rows = kBMn ? 64 : large ? 128 : kBoxRows;
-        const uint32_t bytes = kTileABytes + b_boxes * box_rows * kSlice * 2;
+        const int b_boxes = (half_n + 63) / 64;
+        const uint32_t bytes = kTileABytes + b_boxes * kBoxBytes;
         for (int s = 0; s < n_slices; ++s, ++issued) {
           const int st = ring.at;
           if (!mbar_wait(smem_addr(&s_empty[st]), ring.pass ^ 1, gave_up)) {
@@ -566,12 +561,9 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
             tma_load_2d(sa + kTileABytes / 2, &map_a, m + 64, tile.lo + k, full);
           }
           for (int i = 0; i < b_boxes; ++i) {
-            if (kBMn)
-              tma_load_2d(sb + i * 64 * kSlice * 2, &map_b, tile.n0 + rank * half_n + i * 64,
-                          tile.lo + k, full);
-            else
-              tma_load_2d(sb + i * kBoxRows * kSlice * 2, large ? &map_b_large : &map_b, k,
-                          tile.lo + rank * half_n + i * kBoxRows, full);
+            const int n = rank * half_n + i * 64;
+            if (kBMn) tma_load_2d(sb + i * kBoxBytes, &map_b, tile.n0 + n, tile.lo + k, full);
+            else tma_load_2d(sb + i * kBoxBytes, &map_b, k, tile.lo + n, full);
           }
         }
       }

@@ -5,7 +5,9 @@
 
 #include <cstdint>
 #include <cstring>
+#include <map>
 #include <mutex>
+#include <utility>
 
 namespace moe {
 namespace experts {
@@ -42,6 +44,23 @@ inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Raises a kernel's dynamic shared memory limit where it is below `bytes`; asked of
+// the runtime once per device and size.
+inline cudaError_t allow_smem(const void* kern, size_t bytes) {
+  static std::mutex mu;
+  static std::map<std::pair<int, const void*>, size_t> limit;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  std::lock_guard<std::mutex> lock(mu);
+  size_t& now = limit[{dev, kern}];
+  if (bytes <= now) return cudaSuccess;
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(bytes));
+  if (err == cudaSuccess) now = bytes;
+  return err;
+}
+
 // Launch with programmatic stream serialization: the grid may be scheduled as
 // soon as the previous grid in the stream allows it; every kernel here calls
 // griddepcontrol.wait before it touches memory a previous grid may write.
@@ -50,9 +69,7 @@ template <typename... KArgs, typename... Args>
 cudaError_t launch_clusters(void (*kern)(KArgs...), dim3 grid, dim3 cluster, unsigned block,
                             size_t smem, cudaStream_t stream, Args... args) {
   if (smem > 48 * 1024) {
-    const cudaError_t err =
-        cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t err = allow_smem(reinterpret_cast<const void*>(kern), smem);
     if (err != cudaSuccess) return err;
   }
   cudaLaunchConfig_t cfg;

@@ -129,7 +129,7 @@ int tile_splits(int64_t tiles, int64_t slices, int64_t pairs) {
 template <typename T, int kUse>
 cudaError_t launch_product(const ProductArgs& a, const void* lhs, const void* rhs, int sms,
                            cudaStream_t s) {
-  CUtensorMap map_a, map_b, map_b_large;
+  CUtensorMap map_a, map_b;
   bool ok;
   if (kUse == kWeightGrad) {
     // Without rows the products are empty and the maps are never used.
@@ -137,14 +137,12 @@ cudaError_t launch_product(const ProductArgs& a, const void* lhs, const void* rh
     const void* any = a.out;
     ok = make_map<T>(&map_a, lhs != nullptr ? lhs : any, 0, rows, a.N, kSlice) &&
          make_map<T>(&map_b, rhs != nullptr ? rhs : any, 0, rows, a.K, kSlice);
-    map_b_large = map_b;  // not used
   } else {
     const int64_t depth = kUse == kRowsGrad ? a.N : a.K;
     ok = (kUse == kGated ? make_gated_map<T>(&map_a, lhs, a.E, a.N / 2, a.K)
                          : make_map<T>(&map_a, lhs, a.E, a.N, a.K,
                                        kUse == kRowsGrad ? kSlice : 128)) &&
-         make_map<T>(&map_b, rhs, 0, a.num_rows, depth, kBoxRows) &&
-         make_map<T>(&map_b_large, rhs, 0, a.num_rows, depth, 128);
+         make_map<T>(&map_b, rhs, 0, a.num_rows, depth, 64);
   }
   if (!ok) return cudaErrorInvalidValue;
   const int64_t pairs = sms / 2;
@@ -156,7 +154,7 @@ cudaError_t launch_product(const ProductArgs& a, const void* lhs, const void* rh
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
   const unsigned blocks = 2 * splits * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
   return launch_clusters(k_expert_product<T, kUse>, dim3(blocks), dim3(2 * splits),
-                         kProductThreads, product_smem(a.E), s, map_a, map_b, map_b_large, a);
+                         kProductThreads, product_smem(a.E), s, map_a, map_b, a);
 }
 
 template <typename T, int kUse>
