@@ -64,36 +64,42 @@ k_act_grad(const T* __restrict__ d_out, const T* __restrict__ z, T* __restrict__
 }
 
 // d_bias[e] = column sums of dz over e's rows, in fp32 and in a fixed order: a
-// block takes 64 columns of one expert, 8 threads a row and 32 rows at a time.
-// With few experts and columns a cluster of blocks shares the rows and the first
-// adds the others' sums up.
+// block takes kVecs vectors of 8 columns of one expert and 256 / kVecs rows at a
+// time: 64 columns and 32 rows, or, for experts of few rows, 512 and 4 (256 experts
+// of 8 rows, 7168 columns: 43 us in narrow blocks).  With few experts and columns a
+// cluster of blocks shares the rows and the first adds the others' sums up.
+// 8 experts of 1024 rows, 4096 columns: 10.9 us, 92% of the measured copy bandwidth.
 constexpr int kBiasSplit = 8;
+constexpr int kBiasNarrow = 8, kBiasWide = 64;
 
-template <typename T>
+template <typename T, int kVecs>
 __global__ void __launch_bounds__(kGradThreads)
 k_bias_grad(const T* __restrict__ dz, const int64_t* __restrict__ offset, int64_t num_rows,
             int64_t N, T* __restrict__ d_bias) {
-  constexpr int kAhead = 8;
+  constexpr int kAhead = kVecs == kBiasNarrow ? 8 : 4;
+  constexpr int kLanes = kGradThreads / kVecs;  // rows at a time
+  constexpr int kCols = 8 * kVecs;
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ float part[32][64 + 1];
-  __shared__ float sums[64];
+  __shared__ float part[kLanes][kCols + 1];
+  __shared__ float sums[kCols];
   const int e = blockIdx.y;
   const Segment s = segment(offset, e, num_rows);
   const int splits = gridDim.z, split = blockIdx.z;
   const int share = (s.hi - s.lo + splits - 1) / splits;
   const int lo = min(s.hi, s.lo + split * share), hi = min(s.hi, lo + share);
-  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + tx;
+  const int tx = threadIdx.x % kVecs, ty = threadIdx.x / kVecs;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kVecs + tx;
   float acc[8] = {};
   if (c < N / 8) {
     const uint4* at = reinterpret_cast<const uint4*>(dz) + c;
-    for (int r = lo + ty; r < hi; r += 32 * kAhead) {
+    for (int r = lo + ty; r < hi; r += kLanes * kAhead) {
       Vec8<T> v[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j)
-        v[j].v = r + 32 * j < hi ? ld_stream(at + static_cast<int64_t>(r + 32 * j) * (N / 8))
-                                 : make_uint4(0, 0, 0, 0);
+        v[j].v = r + kLanes * j < hi
+                     ? ld_stream(at + static_cast<int64_t>(r + kLanes * j) * (N / 8))
+                     : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int j = 0; j < kAhead; ++j)
 #pragma unroll
@@ -103,24 +109,22 @@ k_bias_grad(const T* __restrict__ dz, const int64_t* __restrict__ offset, int64_
 #pragma unroll
   for (int i = 0; i < 8; ++i) part[ty][tx * 8 + i] = acc[i];
   __syncthreads();
-  float sum = 0.f;
-  if (threadIdx.x < 64) {
+  for (int i = threadIdx.x; i < kCols; i += kGradThreads) {
+    float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) sum += part[i][threadIdx.x];
-    sums[threadIdx.x] = sum;
+    for (int j = 0; j < kLanes; ++j) sum += part[j][i];
+    sums[i] = sum;
   }
-  if (splits > 1) {
-    cluster_sync();
-    if (split == 0 && threadIdx.x < 64) {
-      for (int i = 1; i < splits; ++i)
-        sum += cluster_load(cluster_addr(smem_addr(&sums[threadIdx.x]), i));
+  if (splits > 1) cluster_sync();
+  if (split == 0) {
+    for (int i = threadIdx.x; i < kCols; i += kGradThreads) {
+      float sum = sums[i];
+      for (int j = 1; j < splits; ++j) sum += cluster_load(cluster_addr(smem_addr(&sums[i]), j));
+      const int64_t col = static_cast<int64_t>(blockIdx.x) * kCols + i;
+      if (col < N) d_bias[static_cast<int64_t>(e) * N + col] = from_f<T>(sum);
     }
-    cluster_sync();  // the others' sums stay until they are read
   }
-  if (split == 0 && threadIdx.x < 64) {
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
-    if (col < N) d_bias[static_cast<int64_t>(e) * N + col] = from_f<T>(sum);
-  }
+  if (splits > 1) cluster_sync();  // the others' sums stay until they are read
 }
 
 }  // namespace experts

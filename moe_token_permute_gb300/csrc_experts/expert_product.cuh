@@ -10,9 +10,8 @@
 //
 // A pair of blocks (two SMs, cta_group::2) computes 256 x (up to 256) outputs: an
 // A tile of 128 rows in each block against one B tile of which each block holds
-// half the columns.  Gated: an A tile holds 16 gate rows and the 16 up rows of the
-// same features in turns, so that both of an output meet in one thread's
-// registers.  Tensor memory (512 columns) holds two accumulators: the epilogue of
+// half the columns.  Gated: an A tile holds 8 gate rows and the 8 up rows of the same
+// features in turns, so that both of an output meet in one thread's registers.  Tensor memory (512 columns) holds two accumulators: the epilogue of
 // one tile overlaps the products of the next.
 //   warps 0-7  epilogue: tensor memory -> registers -> shared -> rows
 //   warp 8     TMA producer: 64-deep slices into a ring of 6 x 32 KB
@@ -88,13 +87,14 @@ static_assert(1024 + kStages * kStageBytes + kStagingBytes + MOE_MAX_LOCAL_EXPER
 
 struct Tile {
   int e, lo, rows;  // expert; first row and row count (d_weight: all of e's rows)
-  int m0, n0;       // first output feature; d_weight: first column
+  int m0, n0, cols;  // first output feature; d_weight: first column and their number
 };
 
-// Row blocks of a segment: as few as fit, of even size (a multiple of 16).
+// Row blocks of a segment, and column blocks of a d_weight: as few as fit, of even
+// size (a multiple of 16).
 __device__ __forceinline__ int row_blocks(int rows, int most) { return (rows + most - 1) / most; }
-__device__ __forceinline__ int block_rows(int rows, int blocks) {
-  return ((rows + blocks - 1) / blocks + 15) / 16 * 16;
+__device__ __forceinline__ int even_step(int size, int blocks) {
+  return ((size + blocks - 1) / blocks + 15) / 16 * 16;
 }
 
 // Output features of one tile.
@@ -132,7 +132,7 @@ __device__ __forceinline__ void place_in_panels(int local, int m_blocks, int n_b
 
 template <int kUse>
 __device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const int* first, int t,
-                                          int m_blocks, int n_blocks, int cap) {
+                                          int m_blocks, int n_blocks, int n_size, int cap) {
   Tile r;
   if (kUse == kWeightGrad) {
     const int per = m_blocks * n_blocks;
@@ -144,7 +144,9 @@ __device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const 
     int m, n;
     place_in_panels(t - place * per, m_blocks, n_blocks, m, n);
     r.m0 = m * m_step<kUse>();
-    r.n0 = n * kMaxN;
+    const int step = even_step(n_size, n_blocks);
+    r.n0 = n * step;
+    r.cols = min(step, n_size - r.n0);
     return r;
   }
   int lo = 0, hi = E;  // first[lo] <= t < first[hi]
@@ -156,13 +158,14 @@ __device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const 
   r.e = lo;
   const Segment s = segments[lo];
   const int rows = s.hi - s.lo;
-  const int blocks = row_blocks(rows, cap), step = block_rows(rows, blocks);
+  const int blocks = row_blocks(rows, cap), step = even_step(rows, blocks);
   int m, n;
   place_in_panels(t - first[lo], m_blocks, blocks, m, n);
   r.lo = s.lo + n * step;
   r.rows = min(step, rows - n * step);
   r.m0 = m * m_step<kUse>();
   r.n0 = 0;
+  r.cols = r.rows;
   return r;
 }
 
@@ -250,7 +253,8 @@ __device__ __forceinline__ void write_block(const float (&v)[32], const Block<T>
   }
 }
 
-// The transposed block of 16 tensor memory lanes: v[4 i + 2 s + b].
+// The transposed block of 16 columns, v[4 i + 2 s + b] being column 8 s + g and row
+// 8 i + 2 q + b.
 template <typename T>
 __device__ __forceinline__ void write_half_block(const float* v, const Block<T, 16>& b) {
   uint32_t p[8];
@@ -473,7 +477,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     }
   };
   auto tile_at = [&](int t) {
-    return find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks, cap);
+    return find_tile<kUse>(a.E, segments, first, t, m_blocks, n_blocks, static_cast<int>(a.K), cap);
   };
   // Slices of the contraction (d_weight: of the expert's rows), from first_slice on
   // in pairs that share it.
@@ -482,10 +486,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     return kUse == kWeightGrad ? (t.rows + kSlice - 1) / kSlice
                                : all_slices * (split + 1) / splits - first_slice;
   };
-  // Columns of the tile, and those of the product (each block holds half of B).
-  auto columns = [&](const Tile& t) {
-    return kUse == kWeightGrad ? min(kMaxN, static_cast<int>(a.K) - t.n0) : t.rows;
-  };
+  // Columns of a tile's product (each block holds half of B).
   auto mma_n = [](int cols) { return (cols + 15) / 16 * 16; };
   // First feature of the block's A tile.
   auto feature = [&](const Tile& t) { return t.m0 + rank * (m_step<kUse>() / 2); };
@@ -516,7 +517,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       const uint32_t full0 = cluster_addr(smem_addr(&s_full[0]), leader);
       for (Walk walk(pair, pairs); walk.t < total && ok; walk.next()) {
         const Tile tile = tile_at(walk.t);
-        const int n_slices = slices(tile), half_n = mma_n(columns(tile)) / 2;
+        const int n_slices = slices(tile), half_n = mma_n(tile.cols) / 2;
         const int b_boxes = (half_n + 63) / 64;
         const uint32_t bytes = kTileABytes + b_boxes * kBoxBytes;
         for (int s = 0; s < n_slices; ++s, ++issued) {
@@ -544,13 +545,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
                                                 : s - 1;
           const int k = slice * kSlice, m = feature(tile);
           if (kUse == kGated) {
-            if (F % 16 == 0) {  // a tile in one load (make_gated_map)
-              tma_load_5d(sa, &map_a, k, 0, 0, m / 16, tile.e, full);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                tma_load_4d(sa + j * (kTileABytes / 4), &map_a, k, m + j * 16, 0, tile.e, full);
-            }
+            tma_load_5d(sa, &map_a, k, 0, 0, m / 8, tile.e, full);
           } else if (kUse == kForward) {
             tma_load_3d(sa, &map_a, k, m, tile.e, full);
           } else if (kUse == kRowsGrad) {
@@ -581,7 +576,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
         const Tile tile = tile_at(walk.t);
         const int n_slices = slices(tile);
         if (n_slices == 0) continue;
-        const uint32_t idesc = instr_desc(kBf16, kAMn, kBMn, 256, mma_n(columns(tile)));
+        const uint32_t idesc = instr_desc(kBf16, kAMn, kBMn, 256, mma_n(tile.cols));
         const uint32_t buf = done & 1, acc = tmem + buf * kMaxN;
         if (!mbar_wait(smem_addr(&s_free[buf]), (done / 2 & 1) ^ 1, gave_up)) break;
         ++done;
@@ -661,7 +656,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     const uint32_t other_part = splits > 1 ? cluster_addr(part, 2 + rank) : 0;
     for (Walk walk(pair, pairs); walk.t < total; walk.next()) {
       const Tile tile = tile_at(walk.t);
-      const int cols = columns(tile);
+      const int cols = tile.cols;
       const bool any = slices(tile) > 0;
       // The warp's 32 features, its columns c + [0, 32).
       const int64_t m = feature(tile) + quad * (kUse == kGated ? 16 : 32);
@@ -714,16 +709,23 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           }
         }
         if (kUse == kGated) {
-          // The warp's 32 lanes: 16 gate rows, then the up rows of the same
-          // features; a thread holds both of a value in z[j] and z[16 + j].
-          if (preact != nullptr) {
-            write_half_block(z, Block<T, 16>(preact, a.N, row, cols - c, m, F, stage));
-            write_half_block(z + 16, Block<T, 16>(preact + F, a.N, row, cols - c, m, F, stage));
-          }
-          apply_act<16>(a.act, z);
+          // The warp's 32 lanes: 8 gate rows and the up rows of the same features,
+          // and again; a thread holds both of a value, z[16 h + 4 i + 2 s + b]
+          // being gate (s = 0) or up of feature 8 h + g, row 8 i + 2 q + b.
+          float gate[16], up[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) z[j] *= z[16 + j];
-          write_half_block(z, Block<T, 16>(out, F, row, cols - c, m, F, stage));
+          for (int j = 0; j < 16; ++j) {  // j = 4 i + 2 h + b
+            gate[j] = z[j / 2 % 2 * 16 + j / 4 * 4 + j % 2];
+            up[j] = z[j / 2 % 2 * 16 + j / 4 * 4 + 2 + j % 2];
+          }
+          if (preact != nullptr) {
+            write_half_block(gate, Block<T, 16>(preact, a.N, row, cols - c, m, F, stage));
+            write_half_block(up, Block<T, 16>(preact + F, a.N, row, cols - c, m, F, stage));
+          }
+          apply_act<16>(a.act, gate);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) gate[j] *= up[j];
+          write_half_block(gate, Block<T, 16>(out, F, row, cols - c, m, F, stage));
         } else if (kUse == kForward) {
           if (a.bias != nullptr) {
             const T* bias = static_cast<const T*>(a.bias) + static_cast<int64_t>(tile.e) * a.N;
@@ -749,7 +751,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           const int64_t left = a.N - m;
           write_block<false>(z, Block<T>(out, a.K, static_cast<int64_t>(tile.e) * a.N + m,
                                          static_cast<int>(left < 32 ? (left < 0 ? 0 : left) : 32),
-                                         tile.n0 + c, a.K, stage));
+                                         tile.n0 + c, tile.n0 + cols, stage));
         }
       }
       if (any) {

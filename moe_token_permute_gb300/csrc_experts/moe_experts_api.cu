@@ -97,17 +97,14 @@ bool make_decode_map(CUtensorMap* map, const void* base, int64_t E, int64_t N, i
                            {64, kDecodeFeatures, kDecodeBlocks, 1});
 }
 
-// The gated weight [E, 2, F, K], in tiles of gate and up x 16 features x 64: in an
-// A tile 16 gate rows and the 16 up rows of the same features take turns, so that
-// they meet in the 32 tensor memory lanes of one warp.  Where F is a multiple of
-// 16 one load takes four such tiles, a whole A tile (as four loads the products
-// of 2048 -> 2 x 768 ran 11% slower).
+// The gated weight [E, 2, F, K] as [E, F/8, 2, 8, K], tiles of 8 x 2 x 8 rows by 64: in
+// an A tile 8 gate rows and the 8 up rows of the same features take turns, so that
+// they meet in the tensor memory lanes that one thread reads.  One load takes the
+// whole tile (as four, the products of 2048 -> 2 x 768 ran 11% slower).
 template <typename T>
 bool make_gated_map(CUtensorMap* map, const void* base, int64_t E, int64_t F, int64_t K) {
-  if (F % 16 == 0)
-    return make_map_nd<T, 5>(map, base, {K, 16, 2, F / 16, E}, {K, F * K, 16 * K, 2 * F * K},
-                             {64, 16, 2, 4, 1});
-  return make_map_nd<T, 4>(map, base, {K, F, 2, E}, {K, F * K, 2 * F * K}, {64, 16, 2, 1});
+  return make_map_nd<T, 5>(map, base, {K, 8, 2, F / 8, E}, {K, F * K, 8 * K, 2 * F * K},
+                           {64, 8, 2, 8, 1});
 }
 
 // The most tiles a product may have, of at most `columns` columns each.
@@ -198,9 +195,11 @@ cudaError_t launch_act_grad(const void* d_out, const void* z, void* dz, const in
 template <typename T>
 cudaError_t launch_bias_grad(const void* dz, const int64_t* offset, int E, int64_t num_rows,
                              int64_t N, void* d_bias, int sms, cudaStream_t s) {
-  const int64_t blocks = ceil_div(N, 64);
-  const unsigned splits = blocks * E <= sms ? kBiasSplit : 1;
-  return launch_clusters(k_bias_grad<T>, dim3(static_cast<unsigned>(blocks), E, splits), dim3(1, 1, splits),
+  // Few rows per expert: wide blocks; few blocks: clusters that share the rows.
+  const bool wide = num_rows <= 16 * static_cast<int64_t>(E);
+  const int64_t blocks = ceil_div(N, wide ? 8 * kBiasWide : 8 * kBiasNarrow);
+  const unsigned splits = !wide && blocks * E <= sms ? kBiasSplit : 1;
+  return launch_clusters(wide ? k_bias_grad<T, kBiasWide> : k_bias_grad<T, kBiasNarrow>, dim3(static_cast<unsigned>(blocks), E, splits), dim3(1, 1, splits),
                          kGradThreads, 0, s, static_cast<const T*>(dz), offset, num_rows, N,
                          static_cast<T*>(d_bias));
 }
