@@ -181,11 +181,11 @@ __device__ __forceinline__ void apply_act(int a, float* v) {
   else if (a == MOE_ACT_RELU) apply_act<kCount, MOE_ACT_RELU>(v);
 }
 
-// A warp's block of a matrix in memory: rows r0 + [0, rows), at most 32, and
-// columns c0 + [0, kCols) below `cols` (a multiple of 8).  Its shared memory copy
-// has rows of kCols values, the 16-byte chunks of some rows exchanged so that
-// neither the fragments' accesses (8 rows of a chunk) nor the rows' (128 bytes)
-// meet in a bank.
+// A warp's block of a matrix in memory: rows r0 + [0, rows), at most 32 (16 with 64
+// columns), and columns c0 + [0, kCols) below `cols` (a multiple of 8).  Its shared
+// memory copy has rows of kCols values, the 16-byte chunks of some rows exchanged
+// so that neither the fragments' accesses (8 rows of a chunk) nor the rows' (128
+// bytes) meet in a bank.
 template <typename T, int kCols = 32>
 struct Block {
   static constexpr int kChunks = kCols / 8;          // 16 bytes each, of a row
@@ -197,7 +197,8 @@ struct Block {
   uint32_t matrix;  // and of the row the lane gives for fragments
 
   static __device__ __forceinline__ uint32_t place(int row, int chunk) {
-    return row * (kCols * 2) + ((chunk ^ (kCols == 32 ? row >> 1 & 3 : row >> 2 & 1)) << 4);
+    const int turn = kCols == 64 ? row & 7 : kCols == 32 ? row >> 1 & 3 : row >> 2 & 1;
+    return row * (kCols * 2) + ((chunk ^ turn) << 4);
   }
   __device__ __forceinline__ Block(T* base, int64_t pitch, int64_t r0, int n_rows, int64_t c0,
                                    int64_t cols, uint32_t stage) {
@@ -206,10 +207,10 @@ struct Block {
     step = kLaneRows * pitch;
     rows = c0 + c * 8 < cols ? n_rows - r : 0;
     line = stage + place(r, c);
-    // 32 columns: lane l row l % 8 of chunk l / 8; 16: chunk l / 8 % 2 of row
+    // 64 and 32 columns: lane l row l % 8 of chunk l / 8; 16: chunk l / 8 % 2 of row
     // l % 8, the upper lanes of row 8 + l % 8.
     const int k = lane >> 3;
-    matrix = stage + (kCols == 32 ? place(lane & 7, k) : place((k >> 1) * 8 + (lane & 7), k & 1));
+    matrix = stage + (kCols == 16 ? place((k >> 1) * 8 + (lane & 7), k & 1) : place(lane & 7, k));
   }
 };
 
@@ -227,29 +228,46 @@ __device__ __forceinline__ void shared_store16(uint32_t addr, uint4 v) {
                : "memory");
 }
 
-// v, as tmem_load_32x32 gives it, rounded and written to the block.
-// kTranspose: tensor memory lanes are the block's columns; else its rows.
-template <bool kTranspose, typename T>
+// v, as tmem_load_32x32 gives it, rounded and written to the block: tensor memory
+// lanes are the block's columns.
+template <typename T>
 __device__ __forceinline__ void write_block(const float (&v)[32], const Block<T>& b) {
   uint32_t p[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) p[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
   __syncwarp();  // the block before this one is read
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    // p[8 h + 2 i + s]: lanes 16 h + 8 s + [0, 8), columns 8 i + [0, 8)
-    if (kTranspose)
-      store_matrices<true>(b.matrix + j * 512, p[2 * j], p[2 * j + 1], p[8 + 2 * j],
-                           p[8 + 2 * j + 1]);
-    else
-      store_matrices<false>(b.matrix + j * 512, p[j / 2 * 8 + j % 2], p[j / 2 * 8 + 2 + j % 2],
-                            p[j / 2 * 8 + 4 + j % 2], p[j / 2 * 8 + 6 + j % 2]);
-  }
+  for (int j = 0; j < 4; ++j)  // p[8 h + 2 i + s]: lanes 16 h + 8 s + [0, 8), columns 8 i + [0, 8)
+    store_matrices<true>(b.matrix + j * 512, p[2 * j], p[2 * j + 1], p[8 + 2 * j],
+                         p[8 + 2 * j + 1]);
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint4 x = shared_load16(b.line + j * 512);
     if (8 * j < b.rows) *reinterpret_cast<uint4*>(b.at + j * b.step) = x;
+  }
+}
+
+// v, as tmem_load_16x64 gives it: tensor memory lanes are the block's rows.  128
+// bytes of a row at a time: where rows are not whole sectors, pieces of 64 bytes
+// touch three sectors for two.
+template <typename T>
+__device__ __forceinline__ void write_row_block(const float (&v)[32], const Block<T, 64>& b) {
+  uint32_t p[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) p[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+  __syncwarp();  // the block before this one is read
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {  // p[2 i + s]: lanes 8 s + [0, 8), columns 8 i + [0, 8)
+    const int s = j / 2, i = j % 2 * 4;
+    store_matrices<false>((b.matrix + s * 1024) ^ (i << 4), p[2 * i + s], p[2 * i + 2 + s],
+                          p[2 * i + 4 + s], p[2 * i + 6 + s]);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 x = shared_load16((b.line + j * 512) ^ (j % 2 * 64));
+    if (4 * j < b.rows) *reinterpret_cast<uint4*>(b.at + j * b.step) = x;
   }
 }
 
@@ -691,17 +709,31 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
         }
         if (!warp_wait(smem_addr(&s_parts), 0, gave_up)) break;
       }
+      if (kUse == kWeightGrad) {
+        for (int c = warp / 4 * 64; c < cols; c += 128) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // lanes 16 h + [0, 16)
+            float z[32];
+            if (any) {
+              tmem_load_16x64(acc + (static_cast<uint32_t>(16 * h) << 16) + c, z);
+              tmem_wait_load(z);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) z[j] = 0.f;
+            }
+            const int64_t left = a.N - m - 16 * h;
+            write_row_block(z, Block<T, 64>(out, a.K, static_cast<int64_t>(tile.e) * a.N + m + 16 * h,
+                                            static_cast<int>(left < 0 ? 0 : left < 16 ? left : 16),
+                                            tile.n0 + c, tile.n0 + cols, stage));
+          }
+        }
+      } else
       for (int c = c0; c < cols; c += 64) {
         const int64_t row = tile.lo + c;
         float z[32];
-        if (any) {
-          tmem_load_32x32(acc + c, z);
-          tmem_wait_load(z);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) z[j] = 0.f;
-        }
-        if (kUse != kWeightGrad && splits > 1) {
+        tmem_load_32x32(acc + c, z);
+        tmem_wait_load(z);
+        if (splits > 1) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float4 x = cluster_load4(other_part + (c - c0) * 64 + j * 512);
@@ -738,20 +770,15 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
             }
           }
           if (preact != nullptr)
-            write_block<true>(z, Block<T>(preact, a.N, row, cols - c, m, a.N, stage));
+            write_block(z, Block<T>(preact, a.N, row, cols - c, m, a.N, stage));
           apply_act<32>(a.act, z);
           if (residual != nullptr) {
             add_block(z, ahead, residual_block(c));
             if (c + 64 < cols) load_block(ahead, residual_block(c + 64));
           }
-          write_block<true>(z, Block<T>(out, a.N, row, cols - c, m, a.N, stage));
-        } else if (kUse == kRowsGrad) {
-          write_block<true>(z, Block<T>(out, a.K, row, cols - c, m, a.K, stage));
+          write_block(z, Block<T>(out, a.N, row, cols - c, m, a.N, stage));
         } else {
-          const int64_t left = a.N - m;
-          write_block<false>(z, Block<T>(out, a.K, static_cast<int64_t>(tile.e) * a.N + m,
-                                         static_cast<int>(left < 32 ? (left < 0 ? 0 : left) : 32),
-                                         tile.n0 + c, tile.n0 + cols, stage));
+          write_block(z, Block<T>(out, a.K, row, cols - c, m, a.K, stage));
         }
       }
       if (any) {

@@ -265,6 +265,25 @@ __device__ __forceinline__ void tmem_load_32x32(uint32_t addr, float (&v)[32]) {
   tmem_load_16x32<0>(addr, v);
   tmem_load_16x32<16>(addr + (16u << 16), v);
 }
+// 64 columns of 16 of the warp's 32 lanes: v[4 i + 2 s + b] = D[lane 8 s + g][column
+// 8 i + 2 q + b].
+__device__ __forceinline__ void tmem_load_16x64(uint32_t addr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, "
+      "%8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, "
+      "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]),
+        "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
+        "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+        "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(addr));
+}
 // The loaded values pass through the wait, so that no use of them can be moved
 // in front of it.
 __device__ __forceinline__ void tmem_wait_load(float (&v)[32]) {
