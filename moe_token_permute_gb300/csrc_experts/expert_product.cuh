@@ -23,9 +23,10 @@
 // Two A tiles per block need 112, but fill tensor memory, and then every tile's
 // epilogue holds the products up: Qwen3-shaped training 5% slower, many experts of
 // 128 rows 1% faster.)  Large products run at the power limit: Mixtral-shaped
-// gated T = 4096 at 1.87 PFLOP/s in a burst and 1.60 over seconds.  With few rows
+// gated T = 4096 at 1.83-1.90 PFLOP/s in a burst and 1.53-1.60 over seconds.  With few rows
 // per expert the weights' way from memory bounds it: Qwen3-shaped gated T = 64 at
-// 6.2 TB/s.
+// 6.2 TB/s.  Rows that are not whole 128-byte lines make every load touch two lines
+// for one (a contraction of 792 takes 1.65 times as long as one of 768).
 // The grid is persistent; tiles are numbered expert by expert, in panels.
 // Where the tiles are at most half as many as the pairs (a dense layer and few
 // rows), two pairs make a cluster and share a tile's contraction: each takes half

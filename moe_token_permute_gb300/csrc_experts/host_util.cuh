@@ -5,9 +5,7 @@
 
 #include <cstdint>
 #include <cstring>
-#include <map>
 #include <mutex>
-#include <utility>
 
 namespace moe {
 namespace experts {
@@ -45,19 +43,26 @@ inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Raises a kernel's dynamic shared memory limit where it is below `bytes`; asked of
-// the runtime once per device and size.
+// the runtime once per device and size (a fixed table: nothing here may throw).
 inline cudaError_t allow_smem(const void* kern, size_t bytes) {
+  struct Limit {
+    const void* kern;
+    size_t bytes;
+  };
+  constexpr int kKernels = 32;
   static std::mutex mu;
-  static std::map<std::pair<int, const void*>, size_t> limit;
+  static Limit limits[kMaxDevices][kKernels];
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   std::lock_guard<std::mutex> lock(mu);
-  size_t& now = limit[{dev, kern}];
-  if (bytes <= now) return cudaSuccess;
+  Limit* at = nullptr;
+  for (int i = 0; dev < kMaxDevices && i < kKernels && at == nullptr; ++i)
+    if (limits[dev][i].kern == kern || limits[dev][i].kern == nullptr) at = &limits[dev][i];
+  if (at != nullptr && at->kern == kern && bytes <= at->bytes) return cudaSuccess;
   err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(bytes));
-  if (err == cudaSuccess) now = bytes;
+  if (err == cudaSuccess && at != nullptr) *at = {kern, bytes};
   return err;
 }
 
