@@ -61,7 +61,7 @@ def _need_rows(t, T, what):
 
 def _stream(stream):
     if stream is None:  # the handle itself: a Stream object takes 3 us to make
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -218,13 +218,12 @@ _ACTIVATIONS = {"none": _b.MOE_ACT_NONE, "silu": _b.MOE_ACT_SILU, "gelu": _b.MOE
 
 def _matrix(t, rows, cols, dtype, what):
     """A contiguous matrix of `rows` x `cols` of the call's type, or None."""
-    if t is None:
+    if t is None or (t.dtype == dtype and t.shape == (rows, cols)):
         return
     if t.dtype != dtype:
         raise ValueError(f"{what} is {t.dtype}; this call takes {dtype}")
-    if t.dim() < 2 or t.size(-1) != cols or t.numel() != rows * cols:
-        raise ValueError(f"{what} must hold {rows} rows of {cols}; its shape is "
-                         f"{tuple(t.shape)}")
+    if t.dim() < 2 or t.shape[-1] != cols or t.numel() != rows * cols:
+        raise ValueError(f"{what} must hold {rows} rows of {cols}; its shape is {tuple(t.shape)}")
 
 
 def _expert_sizes(rows, num_rows, weight_shape, dtype, offset, activation):
