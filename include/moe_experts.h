@@ -17,7 +17,8 @@
  *    weight, bias and gradient.  Products are accumulated in fp32, the
  *    epilogue is computed in fp32 and rounded once (round to nearest even).
  *  - Matrix bases are 16-byte aligned and the sizes hidden_size, ffn_size,
- *    in_size and out_size are multiples of 8 (16-byte rows); any num_rows.
+ *    in_size and out_size are multiples of 8 (16-byte rows); num_rows is
+ *    any up to 2^31 - 1024.
  *  - Rows at and behind expert_first_token_offset[num_local_experts] belong to
  *    no expert: they are not written, and what they hold (infinities and NaN
  *    too) reaches no output.

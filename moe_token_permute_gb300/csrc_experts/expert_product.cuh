@@ -11,8 +11,9 @@
 // A pair of blocks (two SMs, cta_group::2) computes 256 x (up to 256) outputs: an
 // A tile of 128 rows in each block against one B tile of which each block holds
 // half the columns.  Gated: an A tile holds 8 gate rows and the 8 up rows of the same
-// features in turns, so that both of an output meet in one thread's registers.  Tensor memory (512 columns) holds two accumulators: the epilogue of
-// one tile overlaps the products of the next.
+// features in turns, so that both of an output meet in one thread's registers.  Tensor
+// memory (512 columns) holds two accumulators: the epilogue of one tile overlaps the
+// products of the next.
 //   warps 0-7  epilogue: tensor memory -> registers -> shared -> rows
 //   warp 8     TMA producer: 64-deep slices into a ring of 6 x 32 KB
 //   warp 9     tcgen05.mma issue (first block), tensor memory allocation

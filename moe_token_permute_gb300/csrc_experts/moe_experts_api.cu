@@ -23,9 +23,12 @@ namespace {
 bool is_type(moe_dtype_t dt) { return dt == MOE_DTYPE_BF16 || dt == MOE_DTYPE_FP16; }
 bool is_act(moe_activation_t a) { return a >= MOE_ACT_NONE && a <= MOE_ACT_RELU; }
 
+// The kernels count rows in 32 bits, in steps of up to 512 that may pass the last row.
+constexpr int64_t kMostRows = INT32_MAX - 1023;
+
 // Sizes of a [E, N, K] weight and its rows.
 bool sizes_ok(int64_t num_rows, int64_t K, int64_t N, int32_t E) {
-  return num_rows >= 0 && num_rows <= INT32_MAX && K >= 8 && N >= 8 && K % 8 == 0 && N % 8 == 0 &&
+  return num_rows >= 0 && num_rows <= kMostRows && K >= 8 && N >= 8 && K % 8 == 0 && N % 8 == 0 &&
          K <= INT32_MAX / 2 && N <= INT32_MAX / 2 && E >= 1 && E <= MOE_MAX_LOCAL_EXPERTS;
 }
 
@@ -203,7 +206,8 @@ cudaError_t launch_bias_grad(const void* dz, const int64_t* offset, int E, int64
   const bool wide = num_rows <= 16 * static_cast<int64_t>(E);
   const int64_t blocks = ceil_div(N, wide ? 8 * kBiasWide : 8 * kBiasNarrow);
   const unsigned splits = !wide && blocks * E <= sms ? kBiasSplit : 1;
-  return launch_clusters(wide ? k_bias_grad<T, kBiasWide> : k_bias_grad<T, kBiasNarrow>, dim3(static_cast<unsigned>(blocks), E, splits), dim3(1, 1, splits),
+  return launch_clusters(wide ? k_bias_grad<T, kBiasWide> : k_bias_grad<T, kBiasNarrow>,
+                         dim3(static_cast<unsigned>(blocks), E, splits), dim3(1, 1, splits),
                          kGradThreads, 0, s, static_cast<const T*>(dz), offset, num_rows, N,
                          static_cast<T*>(d_bias));
 }

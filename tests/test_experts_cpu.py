@@ -85,6 +85,18 @@ def test_unpermute_backward_refuses(lib, over):
     assert call(lib, "moe_unpermute_backward", UNPERMUTE_BW, over) == b.MOE_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("name,args", [
+    ("moe_expert_gated", GATED), ("moe_expert_gated_backward", GATED_BW),
+    ("moe_expert_linear", LINEAR), ("moe_expert_linear_backward", LINEAR_BW)],
+    ids=["gated", "gated_backward", "linear", "linear_backward"])
+def test_rows_are_counted_in_32_bits(lib, name, args):
+    """The kernels step past the last row by less than 1024.  (The last number that is
+    allowed would be enqueued on a device.)"""
+    assert call(lib, name, args, dict(R=2 ** 31 - 1023)) == b.MOE_ERR_INVALID_ARG
+    if not torch.cuda.is_available():
+        assert call(lib, name, args, dict(R=2 ** 31 - 1024)) == b.MOE_ERR_UNSUPPORTED_DEVICE
+
+
 def test_no_rows_is_valid_and_needs_no_device(lib):
     none = dict(R=0, x=None, off=None, out=None, w=None)
     assert call(lib, "moe_expert_gated", GATED, none) == b.MOE_OK
