@@ -16,7 +16,8 @@ constexpr int kGradWarps = kGradThreads / 32;
 //   linear: z [rows, W]; dz = d * act'(z)
 // W is d_out's width.  Computed in fp32 from 16-bit z and rounded once: dz is
 // the operand of two 16-bit matrix products.  A warp has 32 vectors of 8 columns
-// (blockIdx.y) and takes rows of them, two in flight.
+// (blockIdx.y) and takes rows of them, two in flight.  dz is written for the rows of
+// the experts' segments, which are what the products read, and for no others.
 template <typename T, bool kGatedForm, int kAct>
 __global__ void __launch_bounds__(kGradThreads)
 k_act_grad(const T* __restrict__ d_out, const T* __restrict__ z, T* __restrict__ dz,
@@ -24,18 +25,20 @@ k_act_grad(const T* __restrict__ d_out, const T* __restrict__ z, T* __restrict__
   constexpr int kRows = 2;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t n = rows_in_use(offset, E, num_rows);
+  const RowRange range = rows_in_use<kGradThreads>(offset, E, num_rows);
   const int64_t c = static_cast<int64_t>(blockIdx.y) * 32 + (threadIdx.x & 31);
-  if (c >= W / 8) return;
+  const bool in_width = c < W / 8;  // (the whole warp stays for in_segment)
   const int64_t zw = kGatedForm ? 2 * W : W;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGradWarps;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGradWarps + (threadIdx.x >> 5); r0 < n;
-       r0 += kRows * step) {
+  for (int64_t r0 = range.lo + static_cast<int64_t>(blockIdx.x) * kGradWarps + (threadIdx.x >> 5);
+       r0 < range.hi; r0 += kRows * step) {
     Vec8<T> d[kRows], g[kRows], u[kRows];
+    bool use[kRows];
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
       const int64_t r = r0 + j * step;
-      if (r >= n) break;
+      use[j] = r < range.hi && (!range.bad || in_segment(offset, E, num_rows, r)) && in_width;
+      if (!use[j]) continue;
       d[j].v = ld_stream(reinterpret_cast<const uint4*>(d_out + r * W) + c);
       g[j].v = ld_stream(reinterpret_cast<const uint4*>(z + r * zw) + c);
       if (kGatedForm) u[j].v = ld_stream(reinterpret_cast<const uint4*>(z + r * zw + W) + c);
@@ -43,7 +46,7 @@ k_act_grad(const T* __restrict__ d_out, const T* __restrict__ z, T* __restrict__
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
       const int64_t r = r0 + j * step;
-      if (r >= n) break;
+      if (!use[j]) continue;
       Vec8<T> dg, du;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {

@@ -121,11 +121,43 @@ __device__ __forceinline__ Segment segment(const int64_t* offset, int e, int64_t
   return {static_cast<int>(lo), static_cast<int>(hi)};
 }
 
-// Rows that belong to an expert at all.
-__device__ __forceinline__ int64_t rows_in_use(const int64_t* offset, int num_experts,
-                                               int64_t num_rows) {
-  const int64_t n = __ldg(offset + num_experts);
-  return n < 0 ? 0 : (n > num_rows ? num_rows : n);
+// The rows that belong to an expert at all, found by a whole block of kThreads: a range
+// that holds every segment.  Valid offsets leave no gaps in it (a thread looks at one
+// expert in kThreads, and the range is the offsets' ends); decreasing ones may, and then
+// in_segment says which of its rows count.
+struct RowRange {
+  int lo, hi;
+  bool bad;
+};
+
+template <int kThreads>
+__device__ __forceinline__ RowRange rows_in_use(const int64_t* offset, int num_experts,
+                                                int64_t num_rows) {
+  const int64_t first = __ldg(offset), last = __ldg(offset + num_experts);
+  bool bad = false;
+  for (int e = threadIdx.x; e < num_experts; e += kThreads) {
+    bool b;
+    segment(offset, e, num_rows, &b);
+    bad |= b;
+  }
+  if (!__syncthreads_or(bad)) return {static_cast<int>(first), static_cast<int>(last), false};
+  int lo = INT32_MAX, hi = 0;
+  for (int e = threadIdx.x & 31; e < num_experts; e += 32) {
+    const Segment s = segment(offset, e, num_rows);
+    if (s.lo < s.hi) lo = min(lo, s.lo), hi = max(hi, s.hi);
+  }
+  return {__reduce_min_sync(kFullMask, lo), __reduce_max_sync(kFullMask, hi), true};
+}
+
+// Whether row r, the same in the whole warp, lies in any expert's segment.
+__device__ __forceinline__ bool in_segment(const int64_t* offset, int num_experts,
+                                           int64_t num_rows, int64_t r) {
+  bool in = false;
+  for (int e = threadIdx.x & 31; e < num_experts; e += 32) {
+    const Segment s = segment(offset, e, num_rows);
+    in |= s.lo <= r && r < s.hi;
+  }
+  return __any_sync(kFullMask, in) != 0;
 }
 
 }  // namespace experts
