@@ -21,11 +21,14 @@ constexpr int kGradWarps = kGradThreads / 32;
 template <typename T, bool kGatedForm, int kAct>
 __global__ void __launch_bounds__(kGradThreads)
 k_act_grad(const T* __restrict__ d_out, const T* __restrict__ z, T* __restrict__ dz,
-           const int64_t* __restrict__ offset, int E, int64_t num_rows, int64_t W) {
+           const int64_t* __restrict__ offset, int E, int64_t num_rows, int64_t W,
+           unsigned* __restrict__ status) {
   constexpr int kRows = 2;
   pdl_wait();
   pdl_launch_dependents();
   const RowRange range = rows_in_use<kGradThreads>(offset, E, num_rows);
+  if (range.bad && status != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+    atomicOr(status, MOE_FLAG_OFFSET_OUT_OF_RANGE);
   const int64_t c = static_cast<int64_t>(blockIdx.y) * 32 + (threadIdx.x & 31);
   const bool in_width = c < W / 8;  // (the whole warp stays for in_segment)
   const int64_t zw = kGatedForm ? 2 * W : W;
@@ -78,7 +81,7 @@ constexpr int kBiasNarrow = 8, kBiasWide = 64;
 template <typename T, int kVecs>
 __global__ void __launch_bounds__(kGradThreads)
 k_bias_grad(const T* __restrict__ dz, const int64_t* __restrict__ offset, int64_t num_rows,
-            int64_t N, T* __restrict__ d_bias) {
+            int64_t N, T* __restrict__ d_bias, unsigned* __restrict__ status) {
   constexpr int kAhead = kVecs == kBiasNarrow ? 8 : 4;
   constexpr int kLanes = kGradThreads / kVecs;  // rows at a time
   constexpr int kCols = 8 * kVecs;
@@ -87,7 +90,10 @@ k_bias_grad(const T* __restrict__ dz, const int64_t* __restrict__ offset, int64_
   __shared__ float part[kLanes][kCols + 1];
   __shared__ float sums[kCols];
   const int e = blockIdx.y;
-  const Segment s = segment(offset, e, num_rows);
+  bool bad;
+  const Segment s = segment(offset, e, num_rows, &bad);
+  if (bad && status != nullptr && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0)
+    atomicOr(status, MOE_FLAG_OFFSET_OUT_OF_RANGE);
   const int splits = gridDim.z, split = blockIdx.z;
   const int share = (s.hi - s.lo + splits - 1) / splits;
   const int lo = min(s.hi, s.lo + split * share), hi = min(s.hi, lo + share);

@@ -182,8 +182,8 @@ cudaError_t launch_forward(const ProductArgs& a, const void* weight, const void*
 
 template <typename T, bool kGatedForm>
 cudaError_t launch_act_grad(const void* d_out, const void* z, void* dz, const int64_t* offset,
-                            int E, int64_t num_rows, int64_t W, moe_activation_t act, int sms,
-                            cudaStream_t s) {
+                            int E, int64_t num_rows, int64_t W, moe_activation_t act,
+                            unsigned* status, int sms, cudaStream_t s) {
   auto kern = k_act_grad<T, kGatedForm, MOE_ACT_NONE>;
   if (act == MOE_ACT_SILU) kern = k_act_grad<T, kGatedForm, MOE_ACT_SILU>;
   if (act == MOE_ACT_GELU) kern = k_act_grad<T, kGatedForm, MOE_ACT_GELU>;
@@ -196,12 +196,13 @@ cudaError_t launch_act_grad(const void* d_out, const void* z, void* dz, const in
   return launch(kern, dim3(static_cast<unsigned>(grid), static_cast<unsigned>(columns)),
                 kGradThreads, 0, s,
                 static_cast<const T*>(d_out), static_cast<const T*>(z), static_cast<T*>(dz),
-                offset, E, num_rows, W);
+                offset, E, num_rows, W, status);
 }
 
 template <typename T>
 cudaError_t launch_bias_grad(const void* dz, const int64_t* offset, int E, int64_t num_rows,
-                             int64_t N, void* d_bias, int sms, cudaStream_t s) {
+                             int64_t N, void* d_bias, unsigned* status, int sms,
+                             cudaStream_t s) {
   // Few rows per expert: wide blocks; few blocks: clusters that share the rows.
   const bool wide = num_rows <= 16 * static_cast<int64_t>(E);
   const int64_t blocks = ceil_div(N, wide ? 8 * kBiasWide : 8 * kBiasNarrow);
@@ -209,7 +210,7 @@ cudaError_t launch_bias_grad(const void* dz, const int64_t* offset, int E, int64
   return launch_clusters(wide ? k_bias_grad<T, kBiasWide> : k_bias_grad<T, kBiasNarrow>,
                          dim3(static_cast<unsigned>(blocks), E, splits), dim3(1, 1, splits),
                          kGradThreads, 0, s, static_cast<const T*>(dz), offset, num_rows, N,
-                         static_cast<T*>(d_bias));
+                         static_cast<T*>(d_bias), status);
 }
 
 // d_rows and d_weight of z = x W^T from dz.  beside_previous: the launch before is
@@ -327,19 +328,21 @@ int moe_expert_gated_backward(const void* d_out, const void* permuted_rows, cons
   if (sms == 0) return MOE_ERR_UNSUPPORTED_DEVICE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = dtype == MOE_DTYPE_BF16;
+  unsigned* status = status_of(workspace);
   if (num_rows > 0) {
     const cudaError_t err =
         bf ? launch_act_grad<__nv_bfloat16, true>(d_out, preact, d_preact,
                                                   expert_first_token_offset, num_local_experts,
-                                                  num_rows, ffn_size, activation, sms, s)
+                                                  num_rows, ffn_size, activation, status, sms, s)
            : launch_act_grad<__half, true>(d_out, preact, d_preact, expert_first_token_offset,
-                                           num_local_experts, num_rows, ffn_size, activation, sms, s);
+                                           num_local_experts, num_rows, ffn_size, activation,
+                                           status, sms, s);
     if (err != cudaSuccess) return finish(err);
   }
   auto gradients = bf ? product_gradients<__nv_bfloat16> : product_gradients<__half>;
   return finish(gradients(d_preact, permuted_rows, weight, expert_first_token_offset, num_rows,
                           hidden_size, 2 * ffn_size, num_local_experts, d_rows, d_weight, false,
-                          status_of(workspace), sms, s));
+                          status, sms, s));
 }
 
 int moe_expert_linear(const void* rows, const void* weight, moe_dtype_t dtype,
@@ -401,23 +404,24 @@ int moe_expert_linear_backward(const void* d_out, const void* rows, const void* 
   if (sms == 0) return MOE_ERR_UNSUPPORTED_DEVICE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = dtype == MOE_DTYPE_BF16;
+  unsigned* status = status_of(workspace);
   const void* dz = d_out;
   cudaError_t err = cudaSuccess;
   if (with_act && num_rows > 0) {
     auto grad = bf ? launch_act_grad<__nv_bfloat16, false> : launch_act_grad<__half, false>;
     err = grad(d_out, preact, d_preact, expert_first_token_offset, num_local_experts, num_rows,
-               out_size, activation, sms, s);
+               out_size, activation, status, sms, s);
     dz = d_preact;
   }
   if (err == cudaSuccess && d_bias != nullptr) {
     auto grad = bf ? launch_bias_grad<__nv_bfloat16> : launch_bias_grad<__half>;
-    err = grad(dz, expert_first_token_offset, num_local_experts, num_rows, out_size, d_bias, sms, s);
+    err = grad(dz, expert_first_token_offset, num_local_experts, num_rows, out_size, d_bias,
+               status, sms, s);
   }
   if (err != cudaSuccess) return finish(err);
   auto gradients = bf ? product_gradients<__nv_bfloat16> : product_gradients<__half>;
   return finish(gradients(dz, rows, weight, expert_first_token_offset, num_rows, in_size, out_size,
-                          num_local_experts, d_rows, d_weight, d_bias != nullptr,
-                          status_of(workspace), sms, s));
+                          num_local_experts, d_rows, d_weight, d_bias != nullptr, status, sms, s));
 }
 
 int moe_unpermute_backward(const void* d_out, const void* permuted_rows, int64_t num_rows,

@@ -91,3 +91,28 @@ def test_dz_covers_the_cut_segments_and_nothing_else(form, name):
     assert (dx[~inside] == SENTINEL).all(), "d_rows of rows of no expert was written"
     ref.check(dz[inside], rows_of(want, inside), BF, "d_preact")
     check_products(dz, x, w, segments, dx, dw, db)
+
+
+@pytest.mark.parametrize("what", ["d_bias", "d_preact of linear", "d_preact of gated"])
+@pytest.mark.parametrize("values", [[0, 60, 30], [0, 20, 2 ** 40], [-1, 20, 60]], ids=str)
+def test_malformed_offsets_are_flagged_without_a_product(values, what):
+    n, K, N = 60, 16, 64
+    x, w = (torch.zeros(*s, dtype=BF, device=DEV) for s in ((n, K), (2, N, K)))
+    d, dz = (torch.ones(n, N, dtype=BF, device=DEV) for _ in range(2))
+    ws = torch.zeros(mp.moe_permute_workspace_size(1, 1, 1), dtype=torch.uint8, device=DEV)
+    mp.moe_permute_workspace_init(ws)
+    for offset, flags in ((values, mp.MOE_FLAG_OFFSET_OUT_OF_RANGE), ([0, 20, 60], 0)):
+        offset = torch.tensor(offset, device=DEV)
+        if what == "d_bias":
+            db = torch.empty(2, N, dtype=BF, device=DEV)
+            mp.moe_expert_linear_backward(d, x, w, offset, d_bias=db, workspace=ws)
+            sizes = [hi - lo for lo, hi in cut(offset.tolist(), n)]
+            assert db[:, 0].tolist() == sizes  # sums of ones, below 2^8: exact
+        elif what == "d_preact of linear":
+            mp.moe_expert_linear_backward(d, x, w, offset, activation="relu", preact=d, d_preact=dz,
+                                          workspace=ws)
+        else:
+            mp.moe_expert_gated_backward(d[:, :N // 2].contiguous(), x, w, offset, d, dz,
+                                         workspace=ws)
+        assert mp.moe_read_status(ws) == flags
+        mp.moe_clear_status(ws)
