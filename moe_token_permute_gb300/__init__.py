@@ -239,11 +239,21 @@ def _expert_sizes(rows, num_rows, weight_shape, dtype, offset, activation):
     return E, N, K
 
 
-def _weight_shape(weight, d_weight):
-    t = weight if weight is not None else d_weight
-    if t is None or t.dim() != 3:
+def _weight_shape(weight):
+    if weight is None or weight.dim() != 3:
         raise ValueError("the weight (or its gradient) must be [experts, out, in]")
-    return tuple(t.shape)
+    return tuple(weight.shape)
+
+
+def _gradient_shape(weight, d_weight, out_size, offset, d_bias, rows, d_rows):
+    """[experts, out, in] of a backward call, which may have neither the weight nor
+    its gradient: the experts are then d_bias's, or the offsets' less one, and no
+    result depends on the size of a row that is not given."""
+    if weight is not None or d_weight is not None:
+        return _weight_shape(weight if weight is not None else d_weight)
+    experts = offset.numel() - 1 if d_bias is None else d_bias.shape[0]
+    given = rows if rows is not None else d_rows
+    return experts, out_size, out_size if given is None else given.shape[-1]
 
 
 def moe_expert_gated(permuted_rows, weight, expert_first_token_offset, out, *,
@@ -259,7 +269,7 @@ def moe_expert_gated(permuted_rows, weight, expert_first_token_offset, out, *,
     optional (status word only).
     """
     R, dtype = permuted_rows.shape[0], weight.dtype
-    E, N, H = _expert_sizes(permuted_rows, R, _weight_shape(weight, None), dtype,
+    E, N, H = _expert_sizes(permuted_rows, R, _weight_shape(weight), dtype,
                             expert_first_token_offset, activation)
     if N % 2:
         raise ValueError("weight must hold as many up rows as gate rows")
@@ -278,11 +288,13 @@ def moe_expert_gated_backward(d_out, permuted_rows, weight, expert_first_token_o
 
     d_out [R, F], preact [R, 2F] as the forward pass wrote it; written:
     d_preact [R, 2F], d_rows [R, H] and d_weight [E_local, 2F, H] where given.
-    permuted_rows may be None without d_weight, weight without d_rows.
+    permuted_rows may be None without d_weight, weight without d_rows; without
+    both weight and d_weight there are as many experts as offsets less one.
     """
     R, dtype = d_out.shape[0], d_out.dtype
-    E, N, H = _expert_sizes(permuted_rows, R, _weight_shape(weight, d_weight), dtype,
-                            expert_first_token_offset, activation)
+    shape = _gradient_shape(weight, d_weight, 2 * d_out.shape[-1], expert_first_token_offset, None,
+                            permuted_rows, d_rows)
+    E, N, H = _expert_sizes(permuted_rows, R, shape, dtype, expert_first_token_offset, activation)
     if N % 2:
         raise ValueError("weight must hold as many up rows as gate rows")
     for t, cols, what in ((d_out, N // 2, "d_out"), (preact, N, "preact"),
@@ -309,7 +321,7 @@ def moe_expert_linear(rows, weight, expert_first_token_offset, out, *, bias=None
     (the activation's argument, kept for the backward pass).
     """
     R, dtype = rows.shape[0], weight.dtype
-    E, N, K = _expert_sizes(rows, R, _weight_shape(weight, None), dtype,
+    E, N, K = _expert_sizes(rows, R, _weight_shape(weight), dtype,
                             expert_first_token_offset, activation)
     for t, what in ((out, "out"), (residual, "residual"), (preact, "preact")):
         _matrix(t, R, N, dtype, what)
@@ -329,11 +341,13 @@ def moe_expert_linear_backward(d_out, rows, weight, expert_first_token_offset, *
     With an activation, preact [R, out] is what the forward pass wrote and
     d_preact [R, out] is written; without one both are None.  d_rows [R, in],
     d_weight [E_local, out, in] and d_bias [E_local, out] are written where
-    given; rows may be None without d_weight, weight without d_rows.
+    given; rows may be None without d_weight, weight without d_rows; without
+    weight, d_weight and d_bias there are as many experts as offsets less one.
     """
     R, dtype = d_out.shape[0], d_out.dtype
-    E, N, K = _expert_sizes(rows, R, _weight_shape(weight, d_weight), dtype,
-                            expert_first_token_offset, activation)
+    shape = _gradient_shape(weight, d_weight, d_out.shape[-1], expert_first_token_offset, d_bias,
+                            rows, d_rows)
+    E, N, K = _expert_sizes(rows, R, shape, dtype, expert_first_token_offset, activation)
     for t, cols, what in ((d_out, N, "d_out"), (preact, N, "preact"), (d_preact, N, "d_preact"),
                           (d_rows, K, "d_rows")):
         _matrix(t, R, cols, dtype, what)

@@ -1,0 +1,66 @@
+"""The backward passes' Python functions without a weight and without its
+gradient, which the C entry points take: the sizes come from what there is.  CPU
+tensors stand in for device ones, and the library's entry points for themselves.
+"""
+import pytest
+import torch
+
+import moe_token_permute_gb300 as mp
+from moe_token_permute_gb300 import _binding as b
+
+BF = torch.bfloat16
+
+
+@pytest.fixture
+def passed(monkeypatch):
+    """The sizes and pointers that a call passes on."""
+    seen = {}
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: seen.update({name: args}) or b.MOE_OK
+
+    monkeypatch.setattr(mp._b, "lib", lambda: Library())
+    monkeypatch.setattr(mp, "_ptr", lambda t: None if t is None else t.data_ptr())
+    return seen
+
+
+def tensors(R=5, K=16, N=24, E=3):
+    z = lambda *s: torch.zeros(*s, dtype=BF)  # noqa: E731
+    return z(R, N), z(R, K), z(R, N), z(E, N), torch.zeros(E + 1, dtype=torch.int64)
+
+
+def test_bias_gradient_alone(passed):
+    d, x, z, db, off = tensors()
+    mp.moe_expert_linear_backward(d, None, None, off, d_bias=db, stream=0)
+    args = passed["moe_expert_linear_backward"]
+    R, K, N, E = args[5:9]
+    assert (R, N, E) == (5, 24, 3) and K % 8 == 0 and K >= 8
+    assert args[14] == db.data_ptr() and args[12] is None and args[13] is None
+    mp.moe_expert_linear_backward(d, x, None, off, d_bias=db, activation="relu", preact=z,
+                                  d_preact=d, stream=0)
+    assert passed["moe_expert_linear_backward"][5:9] == (5, 16, 24, 3)
+
+
+def test_dz_alone(passed):
+    d, x, z, _, off = tensors()
+    mp.moe_expert_linear_backward(d, None, None, off, activation="gelu", preact=z, d_preact=z,
+                                  stream=0)
+    assert passed["moe_expert_linear_backward"][5::2][:2] == (5, 24)
+    assert passed["moe_expert_linear_backward"][8] == 3
+    mp.moe_expert_gated_backward(d[:, :12].contiguous(), x, None, off, z, z, stream=0)
+    assert passed["moe_expert_gated_backward"][5:9] == (5, 16, 12, 3)
+
+
+def test_what_needs_a_weight_is_still_refused(passed):
+    d, x, z, db, off = tensors()
+    for kw, match in ((dict(d_rows=x), "d_rows needs weight"),
+                      (dict(d_bias=db[:, :8]), "d_bias must hold"),
+                      (dict(d_bias=torch.zeros(4, 24, dtype=BF)), "holds 4 elements")):
+        with pytest.raises(ValueError, match=match):
+            mp.moe_expert_linear_backward(d, None, None, off, stream=0, **kw)
+    with pytest.raises(ValueError, match="d_rows needs weight"):
+        mp.moe_expert_gated_backward(d[:, :12].contiguous(), x, None, off, z, z, d_rows=x, stream=0)
+    with pytest.raises(ValueError, match=r"\[experts, out, in\]"):
+        mp.moe_expert_linear_backward(d, x, None, off, d_weight=z, stream=0)
+    assert not passed

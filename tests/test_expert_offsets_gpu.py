@@ -116,3 +116,17 @@ def test_malformed_offsets_are_flagged_without_a_product(values, what):
                                          workspace=ws)
         assert mp.moe_read_status(ws) == flags
         mp.moe_clear_status(ws)
+
+
+def test_bias_gradient_needs_no_weight():
+    g = torch.Generator(DEV).manual_seed(3)
+    d = torch.randn(50, 72, generator=g, device=DEV).to(BF)
+    offset = torch.tensor([0, 17, 17, 50], device=DEV)
+    db, beside = (torch.empty(3, 72, dtype=BF, device=DEV) for _ in range(2))
+    mp.moe_expert_linear_backward(d, None, None, offset, d_bias=db)
+    w = torch.zeros(3, 72, 8, dtype=BF, device=DEV)
+    mp.moe_expert_linear_backward(d, None, w, offset, d_bias=beside)
+    assert torch.equal(db, beside)
+    for e, (lo, hi) in enumerate(cut(offset.tolist(), 50)):
+        v = d[lo:hi].double()
+        ref.check(db[e], ref.Val(v.sum(0), max(1, hi - lo) * 2.0 ** -23 * v.abs().sum(0)), BF, e)
