@@ -74,7 +74,8 @@ MOE_API int moe_expert_gated(const void *permuted_rows, const void *weight, moe_
  *   d_rows = [d_gate, d_up] W[e], d_weight[e] = [d_gate, d_up]^T x over e's rows
  *
  *  d_out     [num_rows, F]
- *  preact    [num_rows, 2F] as moe_expert_gated wrote it
+ *  preact    [num_rows, 2F] as moe_expert_gated wrote it.  A gate that
+ *            overflowed to an infinity there takes the limits of act and act'.
  *  d_preact  [num_rows, 2F], written: d_gate then d_up, rounded to dtype (the
  *            operand of both products)
  *  d_rows    [num_rows, H] or NULL (weight may then be NULL)

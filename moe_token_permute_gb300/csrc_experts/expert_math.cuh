@@ -71,7 +71,10 @@ constexpr float kGeluB = 0.044715f;
 // sigmoid: an exponential and a reciprocal each.  Beyond |z| = 16 gelu's
 // sigmoid is 0 or 1 in fp32, so its polynomials take z cut to that range:
 // squares of larger z would overflow against the zero.
-__device__ __forceinline__ float gelu_cut(float z) { return fminf(fmaxf(z, -16.0f), 16.0f); }
+constexpr float kGeluCut = 16.0f;
+__device__ __forceinline__ float gelu_cut(float z) {
+  return fminf(fmaxf(z, -kGeluCut), kGeluCut);
+}
 
 __device__ __forceinline__ float gelu_sigmoid(float zc) {
   return sigmoid(2.0f * kGeluA * zc * (1.0f + kGeluB * zc * zc));
@@ -85,19 +88,25 @@ __device__ __forceinline__ float act(float z) {
   return z;
 }
 
-// a = act(z), and its derivative.
+// a = act(z), and its derivative.  z was rounded to 16 bits: an fp16 z beyond 65504 is
+// infinite here though it was not in the forward pass, and takes the limits (act -> 0
+// and act' -> 0 below, act' -> 1 above) instead of infinity times zero.  The cuts lie
+// where the sigmoid is 0 or 1 already, so they change no other value; NaN stays NaN (fmaxf would
+// lose it).
+constexpr float kSiluCut = 128.0f;
 template <int kAct>
 __device__ __forceinline__ float act_grad(float z, float& a) {
   if (kAct == MOE_ACT_SILU) {
     const float p = sigmoid(z);
-    a = z * p;
-    return p + a * (1.0f - p);
+    a = (z < -kSiluCut ? -kSiluCut : z) * p;
+    return p + (a > kSiluCut ? kSiluCut : a) * (1.0f - p);
   }
   if (kAct == MOE_ACT_GELU) {
     const float zc = gelu_cut(z);
     const float p = gelu_sigmoid(zc);
-    a = z * p;
-    return p + a * (1.0f - p) * (2.0f * kGeluA * (1.0f + 3.0f * kGeluB * zc * zc));
+    a = (z < -kGeluCut ? -kGeluCut : z) * p;
+    return p + (a > kGeluCut ? kGeluCut : a) * (1.0f - p) *
+                   (2.0f * kGeluA * (1.0f + 3.0f * kGeluB * zc * zc));
   }
   if (kAct == MOE_ACT_RELU) {
     a = z > 0.0f ? z : (z != z ? z : 0.0f);
