@@ -47,7 +47,8 @@ typedef enum {
 
 /* Device status bits of these operators (see MOE_FLAG_* in moe_permute.h;
  * MOE_FLAG_BARRIER_TIMEOUT is raised too if a kernel's bounded wait for its
- * own copies or products gave up, the outputs of that call being undefined). */
+ * own copies or products gave up after 2 s without progress, the outputs of
+ * that call being undefined). */
 #define MOE_FLAG_OFFSET_OUT_OF_RANGE 32u
 
 /*

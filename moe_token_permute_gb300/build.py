@@ -1,6 +1,6 @@
 """Build libmoe_permute.so (the C-ABI CUDA library) in-tree with nvcc, and
 beside it libmoe_permute_debug.so, the same sources with -DMOE_DEBUG_HOOKS
-(the test hook of include/moe_permute_debug.h).
+(the test hooks of include/moe_permute_debug.h and csrc_experts/debug_hooks.h).
 
 Each source compiles to an object of its own, all of them in parallel, and
 each library is linked from its objects.
@@ -48,7 +48,7 @@ def _cuda_lib_dir(nvcc: str) -> str:
 
 def _inputs():
     files = SOURCES + glob.glob(os.path.join(CSRC, "*.cuh"))
-    files += glob.glob(os.path.join(EXPERTS, "*.cuh"))
+    files += glob.glob(os.path.join(EXPERTS, "*.cuh")) + glob.glob(os.path.join(EXPERTS, "*.h"))
     files += glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
     return files
 
@@ -83,18 +83,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB_PATH
     nvcc = _nvcc()
     os.makedirs(OUT_DIR, exist_ok=True)
-    # Only the permute's source knows the debug hooks: the other objects are
-    # compiled once and linked into both libraries.
-    objects, jobs = {}, {}
+    objects, jobs = {}, []
     for path, defines in todo:
         objects[path] = []
         for src in SOURCES:
-            d = tuple(defines) if src == SOURCES[0] else ()
-            if (src, d) not in jobs:
-                obj = os.path.join(OUT_DIR, f"{os.path.basename(src)}.{len(jobs)}.{os.getpid()}.o")
-                jobs[src, d] = (subprocess.Popen(_compile_command(nvcc, src, obj, d, verbose)), obj)
-            objects[path].append(jobs[src, d][1])
-    failed = [src for (src, _), (proc, _) in jobs.items() if proc.wait() != 0]
+            obj = os.path.join(OUT_DIR, f"{os.path.basename(src)}.{len(jobs)}.{os.getpid()}.o")
+            command = _compile_command(nvcc, src, obj, defines, verbose)
+            jobs.append((src, subprocess.Popen(command), obj))
+            objects[path].append(obj)
+    failed = [src for src, proc, _ in jobs if proc.wait() != 0]
     if not failed:
         for path, objs in objects.items():
             tmp = path + f".tmp{os.getpid()}"
@@ -102,7 +99,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 failed.append(path)
             else:
                 os.replace(tmp, path)
-    for _, obj in jobs.values():
+    for _, _, obj in jobs:
         if os.path.exists(obj):
             os.remove(obj)
     if failed:

@@ -133,6 +133,7 @@ k_expert_decode(const __grid_constant__ CUtensorMap map, const T* __restrict__ x
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_full[kRing], s_empty[kRing], s_sums[2], s_read[2];
   __shared__ int s_gave_up, s_scan[32];
+  __shared__ uint32_t s_issued;  // stages that the producer has issued
   __shared__ DecodeGroup s_groups[kDecodeMaxRows];
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -140,6 +141,7 @@ k_expert_decode(const __grid_constant__ CUtensorMap map, const T* __restrict__ x
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     s_gave_up = 0;
+    s_issued = 0;
     for (int i = 0; i < kRing; ++i) {
       mbar_init(smem_addr(&s_full[i]), 1);
       mbar_init(smem_addr(&s_empty[i]), kDecodeSet);
@@ -203,10 +205,12 @@ k_expert_decode(const __grid_constant__ CUtensorMap map, const T* __restrict__ x
         for (int s = 0; s < n_slices; ++s, ++step) {
           const int st = step % kRing;
           const uint32_t full = smem_addr(&s_full[st]);
-          if (!mbar_wait(smem_addr(&s_empty[st]), (step / kRing & 1) ^ 1, gave_up)) {
+          if (withheld(step) ||
+              !mbar_wait(smem_addr(&s_empty[st]), (step / kRing & 1) ^ 1, gave_up)) {
             ok = false;
             break;
           }
+          *static_cast<volatile uint32_t*>(&s_issued) = step + 1;
           const int k = s * kDecodeSlice;
           const uint32_t bytes = min(kDecodeSlice, K - k) * 2;
           mbar_expect(full, Shape::kTiles * kDecodeTileBytes + task.rows * bytes);
@@ -290,7 +294,8 @@ k_expert_decode(const __grid_constant__ CUtensorMap map, const T* __restrict__ x
     for (Task t = start; t.group < groups; advance(t), ++turn) {
       const DecodeGroup task = s_groups[t.group];
       const int buf = turn & 1;
-      if (!warp_wait(smem_addr(&s_sums[buf]), turn / 2 & 1, gave_up)) break;
+      // (spans a task's contraction)
+      if (!warp_wait(smem_addr(&s_sums[buf]), turn / 2 & 1, gave_up, smem_addr(&s_issued))) break;
       // Value j of the lane: feature and row (j * 32 + lane) of the task.
       constexpr int kValues = kDecodeFeatures * kDecodeGroup / 32;
       const int f = lane % kDecodeFeatures, r0 = lane / kDecodeFeatures;

@@ -337,6 +337,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       s_clear[kStages], s_tail[kStages], s_parts;
   __shared__ uint32_t s_tmem;
   __shared__ int s_gave_up, s_cap;
+  __shared__ uint32_t s_issued;  // slices that this block's producer has issued
 
   uint8_t* stages = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -365,6 +366,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
     mbar_init(smem_addr(&s_parts), kEpiWarps);
     mbar_init_fence();
     s_gave_up = 0;
+    s_issued = 0;
     tma_prefetch_map(&map_a);
     tma_prefetch_map(&map_b);
   }
@@ -464,6 +466,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
   if (splits > 1) total = min(total, pairs);
   const uint32_t tmem = s_tmem;
   volatile int* gave_up = &s_gave_up;
+  const uint32_t progress = smem_addr(&s_issued);  // of the waits that span a contraction
 
   // A place in the ring of stages: stage and parity of the pass through them.
   struct Ring {
@@ -542,10 +545,11 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
         const uint32_t bytes = kTileABytes + b_boxes * kBoxBytes;
         for (int s = 0; s < n_slices; ++s, ++issued) {
           const int st = ring.at;
-          if (!mbar_wait(smem_addr(&s_empty[st]), ring.pass ^ 1, gave_up)) {
+          if (withheld(issued) || !mbar_wait(smem_addr(&s_empty[st]), ring.pass ^ 1, gave_up)) {
             ok = false;
             break;
           }
+          *static_cast<volatile uint32_t*>(&s_issued) = issued + 1;
           ring.advance();
           // Both blocks' loads report to the first block's barrier; those of a
           // tail slice to their own block's, where it is cleared first (s_clear).
@@ -653,7 +657,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           const int st = static_cast<int>(step % kStages);
           const uint32_t parity = tails >> st & 1;
           tails ^= 1u << st;
-          if (!warp_wait(smem_addr(&s_tail[st]), parity, gave_up)) break;
+          if (!warp_wait(smem_addr(&s_tail[st]), parity, gave_up, progress)) break;
           clear_tail(st, tile.rows % kSlice);
           if (lane == 0) mbar_arrive_cluster(clear0 + st * 8);
         }
@@ -688,7 +692,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       if (residual != nullptr && c0 < cols) load_block(ahead, residual_block(c0));
       const uint32_t buf = done & 1;
       if (any) {
-        if (!warp_wait(smem_addr(&s_done[buf]), done / 2 & 1, gave_up)) break;
+        if (!warp_wait(smem_addr(&s_done[buf]), done / 2 & 1, gave_up, progress)) break;
         ++done;
         tc_fence_after();
       }
@@ -709,7 +713,7 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
           if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&s_parts), rank));
           break;
         }
-        if (!warp_wait(smem_addr(&s_parts), 0, gave_up)) break;
+        if (!warp_wait(smem_addr(&s_parts), 0, gave_up, cluster_addr(progress, 2 + rank))) break;
       }
       if (kUse == kWeightGrad) {
         for (int c = warp / 4 * 64; c < cols; c += 128) {

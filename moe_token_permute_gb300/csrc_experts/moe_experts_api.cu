@@ -4,6 +4,9 @@
 // synchronises.  Each entry point is one launch, or for the backward passes
 // one launch per gradient.
 #include "moe_experts.h"
+#ifdef MOE_DEBUG_HOOKS
+#include "debug_hooks.h"
+#endif
 
 #include <algorithm>
 #include <type_traits>
@@ -456,5 +459,17 @@ int moe_unpermute_backward(const void* d_out, const void* permuted_rows, int64_t
   return finish(run(d_out, permuted_rows, num_rows, H, topk_weights, inv_permuted_idx, T, topk,
                     d_rows, d_topk_weights, status, sms, s));
 }
+
+#ifdef MOE_DEBUG_HOOKS
+int moe_debug_set_expert_wait(int slices, unsigned long long wait_ns) {
+  if (slices < 0 || wait_ns == 0) return MOE_ERR_INVALID_ARG;
+  if (cudaMemcpyToSymbol(g_debug_slices, &slices, sizeof(slices)) != cudaSuccess ||
+      cudaMemcpyToSymbol(g_debug_wait_ns, &wait_ns, sizeof(wait_ns)) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+#endif
 
 }  // extern "C"

@@ -107,9 +107,29 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// A wait gives up after kWaitNs, or as soon as another wait of the block has:
-// `gave_up` is the block's flag in shared memory.
+// A wait gives up when kWaitNs pass without progress, or as soon as another wait of
+// the block has: `gave_up` is the block's flag in shared memory.  A wait for one copy
+// or one slice's products has no other progress than its own end.  A wait that spans
+// a whole contraction (d_weight of one expert: as many slices as its rows fill, and
+// rows may be counted up to 2^31) names the count of what a producer has issued,
+// which moves with every slice: only where that stands still too has something gone
+// wrong.  The count is in shared memory of this block or of another of the cluster.
 constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr uint32_t kNoProgress = 0xffffffffu;
+
+#ifdef MOE_DEBUG_HOOKS
+// The debug build's own limit, and the slices after which a producer stops (0: none);
+// what lets copies in flight land keeps kWaitNs.
+__device__ unsigned long long g_debug_wait_ns = kWaitNs;
+__device__ int g_debug_slices = 0;
+__device__ __forceinline__ unsigned long long wait_ns() { return g_debug_wait_ns; }
+__device__ __forceinline__ bool withheld(uint32_t issued) {
+  return g_debug_slices > 0 && issued >= static_cast<uint32_t>(g_debug_slices);
+}
+#else
+__device__ __forceinline__ unsigned long long wait_ns() { return kWaitNs; }
+__device__ __forceinline__ bool withheld(uint32_t) { return false; }
+#endif
 
 __device__ __forceinline__ unsigned long long now_ns() {
   unsigned long long t;
@@ -117,29 +137,45 @@ __device__ __forceinline__ unsigned long long now_ns() {
   return t;
 }
 
+__device__ __forceinline__ uint32_t progress_at(uint32_t addr) {
+  uint32_t v = 0;
+  if (addr != kNoProgress)
+    asm volatile("ld.volatile.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity,
-                                                   volatile int* gave_up) {
-  const unsigned long long t0 = now_ns();
+                                                   volatile int* gave_up, uint32_t progress) {
+  unsigned long long t0 = now_ns();
+  uint32_t seen = progress_at(progress);
   for (unsigned i = 0; i < (1u << 26); ++i) {
     if (mbar_try(bar, parity)) return true;
     if (*gave_up != 0) return false;
-    if ((i & 63u) == 63u && now_ns() - t0 > kWaitNs) break;
+    if ((i & 63u) == 63u && now_ns() - t0 > wait_ns()) {
+      const uint32_t at = progress_at(progress);
+      if (at == seen) break;
+      seen = at;
+      t0 = now_ns();
+      i = 0;
+    }
   }
   *gave_up = 1;
   return false;
 }
 
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
+                                          uint32_t progress = kNoProgress) {
 #pragma unroll 1
   for (int i = 0; i < 8; ++i)
     if (mbar_try(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity, gave_up);
+  return mbar_wait_slow(bar, parity, gave_up, progress);
 }
 
 // One lane waits, the whole warp learns the outcome and is ordered behind it.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
+                                          uint32_t progress = kNoProgress) {
   bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, gave_up);
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, gave_up, progress);
   return __all_sync(0xffffffffu, ok);
 }
 

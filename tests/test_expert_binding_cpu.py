@@ -2,6 +2,8 @@
 gradient, which the C entry points take: the sizes come from what there is.  CPU
 tensors stand in for device ones, and the library's entry points for themselves.
 """
+import ctypes
+
 import pytest
 import torch
 
@@ -64,3 +66,13 @@ def test_what_needs_a_weight_is_still_refused(passed):
     with pytest.raises(ValueError, match=r"\[experts, out, in\]"):
         mp.moe_expert_linear_backward(d, x, None, off, d_weight=z, stream=0)
     assert not passed
+
+
+def test_wait_hook_is_in_the_debug_build_only():
+    from moe_token_permute_gb300 import build as cuda_build
+    cuda_build.build()
+    assert not hasattr(b.lib(), "moe_debug_set_expert_wait")
+    hook = b.debug_lib().moe_debug_set_expert_wait
+    hook.argtypes = [ctypes.c_int, ctypes.c_ulonglong]
+    assert hook(-1, 1000) == b.MOE_ERR_INVALID_ARG
+    assert hook(0, 0) == b.MOE_ERR_INVALID_ARG
