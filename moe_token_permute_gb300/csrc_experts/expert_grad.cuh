@@ -2,6 +2,8 @@
 // operators' backward passes.  All are memory traffic only.
 #pragma once
 
+#include <type_traits>
+
 #include "expert_math.cuh"
 #include "tcgen05.cuh"
 
@@ -33,40 +35,47 @@ k_act_grad(const T* __restrict__ d_out, const T* __restrict__ z, T* __restrict__
   const bool in_width = c < W / 8;  // (the whole warp stays for in_segment)
   const int64_t zw = kGatedForm ? 2 * W : W;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGradWarps;
-  for (int64_t r0 = range.lo + static_cast<int64_t>(blockIdx.x) * kGradWarps + (threadIdx.x >> 5);
-       r0 < range.hi; r0 += kRows * step) {
-    Vec8<T> d[kRows], g[kRows], u[kRows];
-    bool use[kRows];
+  const int64_t first = range.lo + static_cast<int64_t>(blockIdx.x) * kGradWarps + (threadIdx.x >> 5);
+  // Malformed offsets have a loop of their own, which asks for every row.
+  auto run = [&](auto gaps) {
+    for (int64_t r0 = first; r0 < range.hi; r0 += kRows * step) {
+      Vec8<T> d[kRows], g[kRows], u[kRows];
+      bool use[kRows];
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const int64_t r = r0 + j * step;
-      use[j] = r < range.hi && (!range.bad || in_segment(offset, E, num_rows, r)) && in_width;
-      if (!use[j]) continue;
-      d[j].v = ld_stream(reinterpret_cast<const uint4*>(d_out + r * W) + c);
-      g[j].v = ld_stream(reinterpret_cast<const uint4*>(z + r * zw) + c);
-      if (kGatedForm) u[j].v = ld_stream(reinterpret_cast<const uint4*>(z + r * zw + W) + c);
-    }
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const int64_t r = r0 + j * step;
-      if (!use[j]) continue;
-      Vec8<T> dg, du;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float a;
-        const float da = act_grad<kAct>(to_f(g[j].e[i]), a);
-        const float di = to_f(d[j].e[i]);
-        if (kGatedForm) {
-          dg.e[i] = from_f<T>(di * to_f(u[j].e[i]) * da);
-          du.e[i] = from_f<T>(di * a);
-        } else {
-          dg.e[i] = from_f<T>(di * da);
-        }
+      for (int j = 0; j < kRows; ++j) {
+        const int64_t r = r0 + j * step;
+        use[j] = r < range.hi && in_width;
+        if (decltype(gaps)::value && r < range.hi && !in_segment(offset, E, num_rows, r))
+          use[j] = false;
+        if (!use[j]) continue;
+        d[j].v = ld_stream(reinterpret_cast<const uint4*>(d_out + r * W) + c);
+        g[j].v = ld_stream(reinterpret_cast<const uint4*>(z + r * zw) + c);
+        if (kGatedForm) u[j].v = ld_stream(reinterpret_cast<const uint4*>(z + r * zw + W) + c);
       }
-      reinterpret_cast<uint4*>(dz + r * zw)[c] = dg.v;
-      if (kGatedForm) reinterpret_cast<uint4*>(dz + r * zw + W)[c] = du.v;
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        const int64_t r = r0 + j * step;
+        if (!use[j]) continue;
+        Vec8<T> dg, du;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float a;
+          const float da = act_grad<kAct>(to_f(g[j].e[i]), a);
+          const float di = to_f(d[j].e[i]);
+          if (kGatedForm) {
+            dg.e[i] = from_f<T>(di * to_f(u[j].e[i]) * da);
+            du.e[i] = from_f<T>(di * a);
+          } else {
+            dg.e[i] = from_f<T>(di * da);
+          }
+        }
+        reinterpret_cast<uint4*>(dz + r * zw)[c] = dg.v;
+        if (kGatedForm) reinterpret_cast<uint4*>(dz + r * zw + W)[c] = du.v;
+      }
     }
-  }
+  };
+  if (range.bad) run(std::true_type());
+  else run(std::false_type());
 }
 
 // d_bias[e] = column sums of dz over e's rows, in fp32 and in a fixed order: a
