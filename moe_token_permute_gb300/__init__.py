@@ -59,9 +59,17 @@ def _need_rows(t, T, what):
         raise ValueError(f"{what} must be 2-D with at least {T} rows (one per token)")
 
 
+# The current stream's handle itself: a torch.cuda.Stream takes 3 us to make.  The two
+# names are not public, so a torch without them is asked in the public way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
-    if stream is None:  # the handle itself: a Stream object takes 3 us to make
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if stream is None:
+        if _raw_stream is None or _raw_device is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_raw_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

@@ -1,6 +1,7 @@
 """The backward passes' Python functions without a weight and without its
 gradient, which the C entry points take: the sizes come from what there is.  CPU
-tensors stand in for device ones, and the library's entry points for themselves.
+tensors stand in for device ones, and a recorder for the library.  Also the test
+hook of the expert operators, and the current stream's handle.
 """
 import ctypes
 
@@ -76,3 +77,14 @@ def test_wait_hook_is_in_the_debug_build_only():
     hook.argtypes = [ctypes.c_int, ctypes.c_ulonglong]
     assert hook(-1, 1000) == b.MOE_ERR_INVALID_ARG
     assert hook(0, 0) == b.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name", ["_raw_stream", "_raw_device"])
+def test_current_stream_without_torchs_private_names(monkeypatch, name):
+    class Current:
+        cuda_stream = 0x1234
+
+    monkeypatch.setattr(mp, name, None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Current)
+    assert mp._stream(None) == 0x1234
+    assert mp._stream(77) == 77
