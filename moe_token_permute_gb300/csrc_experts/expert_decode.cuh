@@ -26,8 +26,8 @@
 // instructions take two words of each.  Gated: rows 8-15 of the instruction's tile
 // are the up rows, so that a thread has both of a feature; linear: they are zero
 // (16 features per task would balance worse).
-// On GB300: 2 rows of 8 x [14336 -> 4096] 40 us, 5.8 TB/s (87% of the measured copy
-// bandwidth); 8 rows of 128 x [2048 -> 2 x 768] 13.8 us for 7.5 us of weights: 5.05
+// On GB300: 2 rows of 8 x [14336 -> 4096] 38.8 us, 6.1 TB/s (90% of the measured copy
+// bandwidth); 8 rows of 128 x [2048 -> 2 x 768] 14.8 us for 7.5 us of weights: 5.05
 // tasks per SM are 6 rounds, and about 4 us pass before the first loads arrive.
 #pragma once
 
@@ -68,17 +68,22 @@ struct DecodeShape {
 // Rows up to which these kernels are used; a call has no more groups than rows.
 constexpr int kDecodeMaxRows = 32;
 
-// Which calls.  us, this kernel / large tiles, on GB300 (E experts, in -> features):
-//   gated 64 x 7168 -> 2048, 8 / 16 / 32 rows    72 / 78    110 / 119    212 / 230
-//   gated 8 x 4096 -> 14336, 2 / 8 / 32 rows     70 / 74    164 / 179    260 / 272
-//   gated 128 x 2048 -> 768, 8 / 16 / 32 rows    14 / 15     22 / 23      29 / 29
-//   linear 8 x 14336 -> 4096, 2 / 8 / 32 rows    41 / 44     89 / 132    141 / 149
-//   linear 8 x 4096 -> 4096, 2 / 8 rows          15 / 15     33 / 43
-//   linear 1 x 4096 -> 4096, 1 / 8 / 16 rows     11 / 13     12 / 13      18 / 13
-//   linear 64 x 2048 -> 7168, 8 rows             75 / 42
-//   linear 128 x 768 -> 2048, 8 / 32 rows        23 / 11     56 / 17
+// Which calls.  us from a graph, this kernel / large tiles, on GB300 (E experts, in ->
+// features; the rows go to as many experts as there are; weights not in L2):
+//   gated 64 x 7168 -> 2048, 8 / 16 / 32 rows    70 / 84    132 / 150   257 / 275
+//   gated 8 x 4096 -> 14336, 2 / 8 / 32 rows     69 / 74    257 / 304   258 / 271
+//   gated 128 x 2048 -> 768, 8 / 16 / 32 rows  14.8 / 16.9  22.6 / 25.6  39 / 37
+//   gated 128 x 1984 -> 768, 8 / 16 rows       14.4 / 17.2  22.5 / 24.9
+//   linear 8 x 14336 -> 4096, 2 / 8 / 32 rows    39 / 45    136 / 147   137 / 148
+//   linear 8 x 4096 -> 4096, 2 / 8 rows        15.8 / 17.3  46.3 / 48.1
+//   linear 8 x 4032 -> 4096, 2 / 8 rows        16.0 / 17.0  46.3 / 45.5
+//   linear 1 x 4096 -> 4096, 1 / 8 / 16 rows   11.1 / 14.1  12.3 / 13.5  17.9 / 13.5
+//   linear 64 x 2048 -> 7168, 8 rows             73 / 40
+//   linear 128 x 768 -> 2048, 8 / 32 rows        23 / 10     78 / 25
 // A task costs about 0.7 us beside its loads, so its weights have to be long; more
-// than 8 rows of one expert read its weights again.
+// than 8 rows of one expert read its weights again.  The steps are at 2048 and 4096
+// inputs gated, 4096 and 8192 linear; just below the lower one (1984, 4032) the large
+// tiles are taken, which costs up to 16%.
 inline bool decode_pays(bool gated, int64_t rows, int64_t E, int64_t K) {
   const int64_t task_bytes = (gated ? 2 : 1) * kDecodeFeatures * K * 2;
   const int64_t most = task_bytes >= 128 * 1024  ? kDecodeMaxRows

@@ -29,11 +29,13 @@
 // 6.2 TB/s.  Rows that are not whole 128-byte lines make every load touch two lines
 // for one (a contraction of 792 takes 1.65 times as long as one of 768).
 // The grid is persistent; tiles are numbered expert by expert, in panels.
-// Where the tiles are at most half as many as the pairs (a dense layer and few
-// rows), two pairs make a cluster and share a tile's contraction: each takes half
-// of its slices, the second leaves its sums in its own shared memory, and the
+// Where the tiles of a forward product or d_rows are at most half as many as the pairs
+// (a dense layer and few rows; counted as if every expert had rows), two pairs make a
+// cluster and share a tile's contraction: each takes half of its slices, the second leaves its sums in its own shared memory, and the
 // first adds them to its own through the cluster.  Dense 4096 -> 4096, 64 rows: 16
-// us instead of 22; four pairs, whose clusters do not all run at once, 26.
+// us instead of 22; four pairs, whose clusters do not all run at once, 26.  d_weight
+// is not shared: one expert of 512 x 256 is two tiles, and its rows go through two of
+// the 76 pairs.
 #pragma once
 
 #include "expert_math.cuh"
@@ -68,7 +70,11 @@ struct ProductArgs {
   int E;
   int act;
   // The launch before is another of the same call and reads what this one reads:
-  // nothing is waited for at the start, and that launch at the end.
+  // nothing is waited for at the start, and that launch at the end.  What both read was
+  // written before that launch: it must wait (pdl_wait) ahead of letting this one start
+  // (pdl_launch_dependents) in every block, so that all earlier launches are over and
+  // their writes performed when this one begins.  k_bias_grad and the products do;
+  // so must whatever else is ever put in front of such a launch.
   bool beside_previous;
   const void* bias;
   const void* residual;

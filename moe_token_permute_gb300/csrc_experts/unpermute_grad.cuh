@@ -4,7 +4,7 @@
 // written once.  A warp takes a few consecutive (t, k), drops those without a row
 // at once, and passes over the others' rows one by one: a row's dot product stays
 // in one warp, and the rows of a token read its d_out from L1.
-// T = 4096, K = 8, H = 7168 on GB300: 152 us, 98% of the measured copy bandwidth.
+// T = 4096, K = 8, H = 7168 on GB300: 150 us, the measured copy bandwidth.
 // (With a block's threads across the columns of one row after another, each row's
 // sum was a round of shuffles through the block that held the loads back: 203 us.
 // With a warp for every (t, k) the warps without a row left most of the SM idle
