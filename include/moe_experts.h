@@ -19,11 +19,14 @@
  *  - Matrix bases are 16-byte aligned and the sizes hidden_size, ffn_size,
  *    in_size and out_size are multiples of 8 (16-byte rows); num_rows is
  *    any up to 2^31 - 1024.
- *  - Rows at and behind expert_first_token_offset[num_local_experts] belong to
- *    no expert: they are not written, and what they hold (infinities and NaN
+ *  - Rows ahead of expert_first_token_offset[0] and rows at and behind
+ *    expert_first_token_offset[num_local_experts] belong to no expert: they are
+ *    not written, and what they hold (infinities and NaN
  *    too) reaches no output.
- *  - Offsets outside [0, num_rows] or decreasing are cut to a valid range
- *    and raise MOE_FLAG_OFFSET_OUT_OF_RANGE.
+ *  - Offsets outside [0, num_rows] or decreasing are cut to segments within
+ *    the rows, [lo, hi) with hi at least lo, and raise
+ *    MOE_FLAG_OFFSET_OUT_OF_RANGE.  Where such segments overlap, a row of
+ *    two experts holds the result of either.
  *  - workspace is optional (may be NULL): only its status word is used.
  *  - Results do not depend on timing: no atomic adds.
  *  - Outputs overlap no other buffer of the call, except where noted.
