@@ -21,12 +21,11 @@
  *    any up to 2^31 - 1024.
  *  - Rows ahead of expert_first_token_offset[0] and rows at and behind
  *    expert_first_token_offset[num_local_experts] belong to no expert: they are
- *    not written, and what they hold (infinities and NaN
- *    too) reaches no output.
+ *    not written, and what they hold (infinities and NaN too) reaches no output.
  *  - Offsets outside [0, num_rows] or decreasing are cut to segments within
  *    the rows, [lo, hi) with hi at least lo, and raise
- *    MOE_FLAG_OFFSET_OUT_OF_RANGE.  Where such segments overlap, a row of
- *    two experts holds the result of either.
+ *    MOE_FLAG_OFFSET_OUT_OF_RANGE.  Where such segments overlap, the call's
+ *    outputs are undefined; nothing outside of them is written.
  *  - workspace is optional (may be NULL): only its status word is used.
  *  - Results do not depend on timing: no atomic adds.
  *  - Outputs overlap no other buffer of the call, except where noted.
