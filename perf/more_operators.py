@@ -158,7 +158,9 @@ def work(case):
 def _quantised(x, form, dims):
     """Codes of x (fp32) and the scales that the maxima over `dims` give."""
     amax = x.abs().amax(dim=dims, keepdim=True)
-    scale = torch.where(amax > 0, amax / LARGEST[form], torch.ones_like(amax))
+    # (divided by a tensor: by a number, torch multiplies with its reciprocal)
+    scale = torch.where(amax > 0, amax / torch.full_like(amax, LARGEST[form]),
+                        torch.ones_like(amax))
     q = x / scale
     q = q.clamp(-448, 448) if form == "fp8" else q.round().clamp(-127, 127)
     return q.to(CODES[form]), scale
