@@ -70,7 +70,8 @@ typedef enum {
     MOE_DTYPE_FP16 = 1,
     MOE_DTYPE_FP8_E4M3 = 2,
     MOE_DTYPE_FP8_E5M2 = 3,
-    MOE_DTYPE_FP32 = 4
+    MOE_DTYPE_FP32 = 4,
+    MOE_DTYPE_INT8 = 5
 } moe_dtype_t;
 
 /* Storage type of topk_ids. */

@@ -1,9 +1,9 @@
 """GB300 (sm_103a) MoE token permute / unpermute, the expert products between
-them and their gradients, behind a C ABI.
+them in 16 and 8 bits and their gradients, behind a C ABI.
 
 The Python functions below carry the names of the C entry points declared in
-include/moe_permute.h and include/moe_experts.h and only marshal torch tensors
-into pointers and sizes; all work runs in libmoe_permute.so.  Every output
+include/moe_permute.h, include/moe_experts.h and include/moe_quant.h and only
+marshal torch tensors into pointers and sizes; all work runs in libmoe_permute.so.  Every output
 buffer and the workspace are supplied by the caller, so no call allocates (vLLM
 PR #43014 digest, "implementation breakdown": scratch allocated once and
 reused).
@@ -27,6 +27,7 @@ _DTYPES = {
     torch.float8_e4m3fn: _b.MOE_DTYPE_FP8_E4M3,
     torch.float8_e5m2: _b.MOE_DTYPE_FP8_E5M2,
     torch.float32: _b.MOE_DTYPE_FP32,
+    torch.int8: _b.MOE_DTYPE_INT8,
 }
 _INDEX = {torch.int32: _b.MOE_INDEX_INT32, torch.int64: _b.MOE_INDEX_INT64}
 
@@ -370,6 +371,134 @@ def moe_expert_linear_backward(d_out, rows, weight, expert_first_token_offset, *
         _ptr(d_out), _ptr(rows), _ptr(weight), _DTYPES[dtype], _ptr(expert_first_token_offset),
         R, K, N, E, _ACTIVATIONS[activation], _ptr(preact), _ptr(d_preact), _ptr(d_rows),
         _ptr(d_weight), _ptr(d_bias), _ptr(workspace), _stream(stream)))
+
+
+def _here(*tensors):
+    """The library works on the current device: tensors of another are refused."""
+    device = None
+    for t in tensors:
+        if t is None or not t.is_cuda:  # (_ptr refuses the latter)
+            continue
+        if device is None:
+            device = torch.cuda.current_device() if _raw_device is None else _raw_device()
+        if t.get_device() != device:
+            raise ValueError(f"expected tensors on the current device (cuda:{device}); "
+                             f"one is on {t.device}")
+
+
+def _code_groups(codes_dtype, cols, what):
+    """Scales of a row of `cols` codes."""
+    if codes_dtype == torch.int8:
+        return 1
+    if codes_dtype != torch.float8_e4m3fn:
+        raise ValueError(f"{what} must be float8_e4m3fn or int8; it is {codes_dtype}")
+    return -(-cols // _b.MOE_QUANT_GROUP)
+
+
+def moe_quant_rows(rows, codes, scales, *, expert_first_token_offset=None, workspace=None,
+                   stream=None) -> None:
+    """8-bit codes and scales of 16-bit rows (see include/moe_quant.h).
+
+    rows [R, H] bf16 or fp16; codes [R, H] float8_e4m3fn or int8, written;
+    scales fp32, written: [R, ceil(H / 128)] for float8_e4m3fn, [R, 1] for
+    int8.  With expert_first_token_offset int64 [E_local+1] only the experts'
+    rows are read and written.  H a multiple of 16.
+    """
+    if rows.dtype not in (torch.bfloat16, torch.float16) or rows.dim() != 2:
+        raise ValueError("rows must be [R, H], bfloat16 or float16")
+    R, H = rows.shape
+    groups = _code_groups(codes.dtype, H, "codes")
+    _matrix(codes, R, H, codes.dtype, "codes")
+    _matrix(scales, R, groups, torch.float32, "scales")
+    experts = 0
+    if expert_first_token_offset is not None:
+        if expert_first_token_offset.dtype != torch.int64:
+            raise ValueError("expert_first_token_offset must be int64")
+        _need(expert_first_token_offset, 2, "expert_first_token_offset")
+        experts = expert_first_token_offset.numel() - 1
+    _here(rows, codes, scales, expert_first_token_offset, workspace)
+    _b.check("moe_quant_rows", _b.lib().moe_quant_rows(
+        _ptr(rows), _DTYPES[rows.dtype], _ptr(expert_first_token_offset), R, H, experts,
+        _DTYPES[codes.dtype], _ptr(codes), _ptr(scales), _ptr(workspace), _stream(stream)))
+
+
+def _quant_operands(codes, scales, weight, weight_scales, offset, out, parts):
+    """Sizes of a product of 8-bit rows and weights, whose scales count the blocks
+    of `parts` equal parts of the weight's rows apart."""
+    E, N, K = _weight_shape(weight)
+    if codes.dim() != 2:
+        raise ValueError("the codes must be [R, in]")
+    if N % parts:
+        raise ValueError("weight must hold as many up rows as gate rows")
+    groups = _code_groups(weight.dtype, K, "weight")
+    R = codes.shape[0]
+    _matrix(codes, R, K, weight.dtype, "the codes")
+    _matrix(scales, R, groups, torch.float32, "the rows' scales")
+    if weight.dtype == torch.int8:
+        _matrix(weight_scales, E, N, torch.float32, "weight_scales")
+    else:
+        blocks = parts * -(-(N // parts) // _b.MOE_QUANT_GROUP)
+        _matrix(weight_scales, E * blocks, groups, torch.float32, "weight_scales")
+    if offset.dtype != torch.int64:
+        raise ValueError("expert_first_token_offset must be int64")
+    _need(offset, E + 1, "expert_first_token_offset")
+    if out.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("out must be bfloat16 or float16")
+    _matrix(out, R, N // parts, out.dtype, "out")
+    return R, E, N, K
+
+
+def moe_expert_gated_quant(permuted_codes, permuted_scales, weight, weight_scales,
+                           expert_first_token_offset, out, *, activation="silu", workspace=None,
+                           stream=None) -> None:
+    """moe_expert_gated on 8-bit rows and weights (see include/moe_quant.h):
+    out = act(x Wg[e]^T) * (x Wu[e]^T).
+
+    permuted_codes [R, H] float8_e4m3fn or int8 in moe_permute's order, weight
+    [E_local, 2F, H] of the same type (an expert's F gate rows, then its F up
+    rows), out [R, F] bf16 or fp16.  Scales are fp32.
+    float8_e4m3fn: permuted_scales [R, ceil(H / 128)], weight_scales
+    [E_local, 2 * ceil(F / 128), ceil(H / 128)], the gate rows' blocks of
+    128 x 128, then the up rows'.  int8: permuted_scales [R, 1], weight_scales
+    [E_local, 2F].  H a multiple of 16, F of 8.
+    """
+    R, E, N, H = _quant_operands(permuted_codes, permuted_scales, weight, weight_scales,
+                                 expert_first_token_offset, out, 2)
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
+    _here(permuted_codes, permuted_scales, weight, weight_scales, expert_first_token_offset, out,
+          workspace)
+    _b.check("moe_expert_gated_quant", _b.lib().moe_expert_gated_quant(
+        _ptr(permuted_codes), _ptr(permuted_scales), _ptr(weight), _ptr(weight_scales),
+        _DTYPES[weight.dtype], _DTYPES[out.dtype], _ptr(expert_first_token_offset), R, H, N // 2,
+        E, _ACTIVATIONS[activation], _ptr(out), _ptr(workspace), _stream(stream)))
+
+
+def moe_expert_linear_quant(codes, scales, weight, weight_scales, expert_first_token_offset, out,
+                            *, bias=None, activation="none", residual=None, workspace=None,
+                            stream=None) -> None:
+    """moe_expert_linear on 8-bit rows and weights (see include/moe_quant.h):
+    out = act(x W[e]^T + bias[e]) + residual.
+
+    codes [R, in] float8_e4m3fn or int8, weight [E_local, out, in] of the same
+    type, out [R, out] bf16 or fp16, bias [E_local, out] and residual [R, out]
+    (may be out itself) of out's type or None.  Scales are fp32.
+    float8_e4m3fn: scales [R, ceil(in / 128)], weight_scales
+    [E_local, ceil(out / 128), ceil(in / 128)].  int8: scales [R, 1],
+    weight_scales [E_local, out].  in a multiple of 16, out of 8.
+    """
+    R, E, N, K = _quant_operands(codes, scales, weight, weight_scales, expert_first_token_offset,
+                                 out, 1)
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
+    _matrix(bias, E, N, out.dtype, "bias")
+    _matrix(residual, R, N, out.dtype, "residual")
+    _here(codes, scales, weight, weight_scales, expert_first_token_offset, out, bias, residual,
+          workspace)
+    _b.check("moe_expert_linear_quant", _b.lib().moe_expert_linear_quant(
+        _ptr(codes), _ptr(scales), _ptr(weight), _ptr(weight_scales), _DTYPES[weight.dtype],
+        _DTYPES[out.dtype], _ptr(expert_first_token_offset), R, K, N, E, _ptr(bias),
+        _ACTIVATIONS[activation], _ptr(residual), _ptr(out), _ptr(workspace), _stream(stream)))
 
 
 def moe_unpermute_backward(d_out, permuted_rows, topk_weights, inv_permuted_idx, d_rows,

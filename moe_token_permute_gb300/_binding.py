@@ -1,5 +1,5 @@
-"""ctypes binding of libmoe_permute.so (include/moe_permute.h and
-include/moe_experts.h).
+"""ctypes binding of libmoe_permute.so (include/moe_permute.h,
+include/moe_experts.h and include/moe_quant.h).
 
 Argument marshalling only: every step of permute and unpermute runs in the
 CUDA library.  If the library has not been built this module raises on first
@@ -24,6 +24,7 @@ MOE_DTYPE_FP16 = 1
 MOE_DTYPE_FP8_E4M3 = 2
 MOE_DTYPE_FP8_E5M2 = 3
 MOE_DTYPE_FP32 = 4
+MOE_DTYPE_INT8 = 5
 
 MOE_INDEX_INT32 = 0
 MOE_INDEX_INT64 = 1
@@ -43,13 +44,14 @@ MOE_ACT_RELU = 3
 MOE_MAX_TOPK = 32
 MOE_MAX_LOCAL_EXPERTS = 1024
 MOE_QUANT_GROUP = 128
+MOE_INT8_MAX_IN = 131056
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 
-# name -> (restype, argtypes); mirrors include/moe_permute.h and include/moe_experts.h
+# name -> (restype, argtypes); mirrors include/moe_permute.h, moe_experts.h and moe_quant.h
 SIGNATURES = {
     "moe_permute_supported": (ctypes.c_int, [ctypes.c_int]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -81,6 +83,13 @@ SIGNATURES = {
                                                   _P]),
     "moe_unpermute_backward": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I64, _I64, _I32, _P, _P, _P,
                                               _P]),
+    "moe_quant_rows": (ctypes.c_int, [_P, ctypes.c_int, _P, _I64, _I64, _I32, ctypes.c_int, _P,
+                                      _P, _P, _P]),
+    "moe_expert_gated_quant": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, ctypes.c_int, _P,
+                                              _I64, _I64, _I64, _I32, ctypes.c_int, _P, _P, _P]),
+    "moe_expert_linear_quant": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, ctypes.c_int, _P,
+                                               _I64, _I64, _I64, _I32, _P, ctypes.c_int, _P, _P,
+                                               _P, _P]),
 }
 
 MOE_NOALLOC_SCRATCH_BYTES = (1 << 20) + 256

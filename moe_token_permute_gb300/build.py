@@ -26,7 +26,8 @@ LIB_NAME = "libmoe_permute.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 DEBUG_LIB_PATH = os.path.join(OUT_DIR, "libmoe_permute_debug.so")
 EXPERTS = os.path.join(PKG, "csrc_experts")
-SOURCES = [os.path.join(CSRC, "moe_permute_api.cu"), os.path.join(EXPERTS, "moe_experts_api.cu")]
+SOURCES = [os.path.join(CSRC, "moe_permute_api.cu"), os.path.join(EXPERTS, "moe_experts_api.cu"),
+           os.path.join(EXPERTS, "moe_quant_api.cu")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

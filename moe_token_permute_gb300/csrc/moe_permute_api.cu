@@ -611,7 +611,8 @@ int elem_bytes(moe_dtype_t dt) {
     case MOE_DTYPE_BF16:
     case MOE_DTYPE_FP16: return 2;
     case MOE_DTYPE_FP8_E4M3:
-    case MOE_DTYPE_FP8_E5M2: return 1;
+    case MOE_DTYPE_FP8_E5M2:
+    case MOE_DTYPE_INT8: return 1;
     case MOE_DTYPE_FP32: return 4;
     default: return 0;
   }
