@@ -138,6 +138,59 @@ __device__ __forceinline__ void place_in_panels(int local, int m_blocks, int n_b
   n = panel * kPanel + local - m * width;
 }
 
+// Run by one warp: in how many blocks of each size the experts' rows are cut; the
+// choice of the most columns of a tile, returned; and each expert's first tile,
+// first[E] being the number of tiles.  With `widest` tiles have kMaxN columns.
+__device__ __forceinline__ int scan_tiles(int E, const Segment* segments, int* first, bool widest,
+                                          int m_blocks, int slices, int pairs) {
+  const int lane = threadIdx.x & 31;
+  int cap = kMaxN;
+  if (!widest) {
+    int blocks[kCaps] = {}, all = 0;
+    for (int e = lane; e < E; e += 32) {
+      const int rows = segments[e].hi - segments[e].lo;
+      all += rows;
+#pragma unroll
+      for (int i = 0; i < kCaps; ++i) blocks[i] += row_blocks(rows, cap_of(i));
+    }
+    all = __reduce_add_sync(kFullMask, all);
+    int mine = 0, most = 0;  // lane i: with cap_of(i)
+#pragma unroll
+    for (int i = 0; i < kCaps; ++i) {
+      const int n = __reduce_add_sync(kFullMask, blocks[i]);
+      if (i == 0) most = n;
+      if (lane == i) mine = n;
+    }
+    float cost = INFINITY;
+    if (lane == 0 || (lane < kCaps && most < (6 * pairs + m_blocks - 1) / m_blocks))
+      cost = cap_cost(mine, all, m_blocks, slices, pairs);
+    float best = cost;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) best = fminf(best, __shfl_xor_sync(kFullMask, best, d));
+    cap = cap_of(__ffs(__ballot_sync(kFullMask, cost == best)) - 1);
+  }
+  // The host has made sure that the tiles of num_rows rows can be counted; where
+  // bad offsets make segments overlap, those beyond kMostTiles are left out.
+  constexpr int64_t kMostTiles = INT32_MAX / 2;
+  int64_t before = 0;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int e = e0 + lane;
+    const int64_t n =
+        e < E ? static_cast<int64_t>(row_blocks(segments[e].hi - segments[e].lo, cap)) * m_blocks
+              : 0;
+    int64_t sum = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(kFullMask, sum, d);
+      if (lane >= d) sum += x;
+    }
+    if (e < E) first[e] = static_cast<int>(min(kMostTiles, before + sum - n));
+    before += __shfl_sync(kFullMask, sum, 31);
+  }
+  if (lane == 0) first[E] = static_cast<int>(min(kMostTiles, before));
+  return cap;
+}
+
 template <int kUse>
 __device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const int* first, int t,
                                           int m_blocks, int n_blocks, int n_size, int cap) {
@@ -176,6 +229,19 @@ __device__ __forceinline__ Tile find_tile(int E, const Segment* segments, const 
   r.cols = r.rows;
   return r;
 }
+
+// The pair's tiles: one of every `pairs`, in turn from the front and the back.
+struct Walk {
+  int t, up, down;
+  __device__ __forceinline__ Walk(int pair, int pairs)
+      : t(pair), up(2 * (pairs - pair) - 1), down(2 * pair + 1) {}
+  __device__ __forceinline__ void next() {
+    t += up;
+    const int s = up;
+    up = down;
+    down = s;
+  }
+};
 
 template <int kCount, int kAct>
 __device__ __forceinline__ void apply_act(float* v) {
@@ -412,55 +478,8 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       first[before] = e;
     }
   } else if (warp == 0) {
-    // In how many blocks of each size the experts' rows are cut; the choice; and
-    // each expert's first tile.
-    int cap = kMaxN;
-    if (splits == 1) {
-      int blocks[kCaps] = {}, all = 0;
-      for (int e = lane; e < a.E; e += 32) {
-        const int rows = segments[e].hi - segments[e].lo;
-        all += rows;
-#pragma unroll
-        for (int i = 0; i < kCaps; ++i) blocks[i] += row_blocks(rows, cap_of(i));
-      }
-      all = __reduce_add_sync(kFullMask, all);
-      int mine = 0, most = 0;  // lane i: with cap_of(i)
-#pragma unroll
-      for (int i = 0; i < kCaps; ++i) {
-        const int n = __reduce_add_sync(kFullMask, blocks[i]);
-        if (i == 0) most = n;
-        if (lane == i) mine = n;
-      }
-      float cost = INFINITY;
-      if (lane == 0 || (lane < kCaps && most < (6 * pairs + m_blocks - 1) / m_blocks))
-        cost = cap_cost(mine, all, m_blocks, all_slices, pairs);
-      float best = cost;
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) best = fminf(best, __shfl_xor_sync(kFullMask, best, d));
-      cap = cap_of(__ffs(__ballot_sync(kFullMask, cost == best)) - 1);
-    }
-    // The host has made sure that the tiles of num_rows rows can be counted; where
-    // bad offsets make segments overlap, those beyond kMostTiles are left out.
-    constexpr int64_t kMostTiles = INT32_MAX / 2;
-    int64_t before = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int64_t n = e < a.E ? static_cast<int64_t>(
-                                      row_blocks(segments[e].hi - segments[e].lo, cap)) * m_blocks
-                                : 0;
-      int64_t sum = n;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t x = __shfl_up_sync(kFullMask, sum, d);
-        if (lane >= d) sum += x;
-      }
-      if (e < a.E) first[e] = static_cast<int>(min(kMostTiles, before + sum - n));
-      before += __shfl_sync(kFullMask, sum, 31);
-    }
-    if (lane == 0) {
-      first[a.E] = static_cast<int>(min(kMostTiles, before));
-      s_cap = cap;
-    }
+    const int cap = scan_tiles(a.E, segments, first, splits > 1, m_blocks, all_slices, pairs);
+    if (lane == 0) s_cap = cap;
   }
   tc_fence_before();
   __syncthreads();
@@ -491,18 +510,6 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       --r.at;
       while (!mbar_try(smem_addr(&s_empty[r.at]), r.pass) && now_ns() - t0 < kWaitNs) {
       }
-    }
-  };
-  // The pair's tiles: one of every `pairs`, in turn from the front and the back.
-  struct Walk {
-    int t, up, down;
-    __device__ __forceinline__ Walk(int pair, int pairs)
-        : t(pair), up(2 * (pairs - pair) - 1), down(2 * pair + 1) {}
-    __device__ __forceinline__ void next() {
-      t += up;
-      const int s = up;
-      up = down;
-      down = s;
     }
   };
   auto tile_at = [&](int t) {

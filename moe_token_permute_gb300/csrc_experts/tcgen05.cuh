@@ -144,8 +144,8 @@ __device__ __forceinline__ uint32_t progress_at(uint32_t addr) {
   return v;
 }
 
-static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity,
-                                                   volatile int* gave_up, uint32_t progress) {
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* gave_up,
+                                               uint32_t progress) {
   unsigned long long t0 = now_ns();
   uint32_t seen = progress_at(progress);
   for (unsigned i = 0; i < (1u << 26); ++i) {
@@ -163,19 +163,29 @@ static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity
   return false;
 }
 
+// Out of line, where the kernel does not change its registers (setmaxnreg), which allows
+// no calls.
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity,
+                                                   volatile int* gave_up, uint32_t progress) {
+  return mbar_wait_long(bar, parity, gave_up, progress);
+}
+
+template <bool kCalls = true>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
                                           uint32_t progress = kNoProgress) {
 #pragma unroll 1
   for (int i = 0; i < 8; ++i)
     if (mbar_try(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity, gave_up, progress);
+  return kCalls ? mbar_wait_slow(bar, parity, gave_up, progress)
+                : mbar_wait_long(bar, parity, gave_up, progress);
 }
 
 // One lane waits, the whole warp learns the outcome and is ordered behind it.
+template <bool kCalls = true>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
                                           uint32_t progress = kNoProgress) {
   bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, gave_up, progress);
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait<kCalls>(bar, parity, gave_up, progress);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -271,6 +281,16 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1 : 0)
       : "memory");
 }
+// The same of 8-bit operands, e4m3: 32 values of the contraction.  The instruction
+// descriptor's types are 0, as fp16's.
+__device__ __forceinline__ void tc_mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1 : 0)
+      : "memory");
+}
 // The barrier at this address in the cluster's blocks of `mask` (the pair) gets one
 // arrival when every tcgen05.mma issued before is done.
 __device__ __forceinline__ void tc_commit(uint32_t bar, uint16_t mask) {
@@ -356,8 +376,41 @@ __device__ __forceinline__ void load_matrices_transposed(uint32_t addr, uint32_t
                : "memory");
 }
 
+// Two fp32 at a time.
+__device__ __forceinline__ uint64_t pack_f32x2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Registers of the threads of four warps; the block's shares together are at most what
+// it was launched with.
+template <int kRegisters>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegisters));
+}
+template <int kRegisters>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegisters));
+}
+
 // Shared memory descriptor of a 128-byte-swizzled operand tile.
-//   K-major:  8 rows of 64 k-values make a 1024-byte block; sbo = the step to
+//   K-major:  8 rows of 128 bytes (64 k-values of 16 bits) make a 1024-byte block; sbo = the step to
 //             the next 8 rows, lbo unused.
 //   MN-major: 8 k-rows of 64 m- or n-values make a 1024-byte block; sbo = the
 //             step to the next 8 k, lbo = the step to the next 64 m or n.
