@@ -8,10 +8,10 @@
 
 #include "expert_math.cuh"
 #include "host_util.cuh"
+#include "int8_product.cuh"
 #include "product_host.cuh"
 #include "quant_product.cuh"
 #include "quant_rows.cuh"
-#include "quant_simple.cuh"
 
 namespace moe {
 namespace experts {
@@ -47,31 +47,35 @@ cudaError_t launch_quant_rows(const QuantRowsArgs& a, int sms, cudaStream_t s) {
 }
 
 template <typename T, bool kGatedForm>
-cudaError_t launch_int8(const QuantArgs& a, int, cudaStream_t s) {
-  const int64_t width = kGatedForm ? a.N / 2 : a.N;
-  return launch(k_quant_simple<T, false, kGatedForm>,
-                dim3(static_cast<unsigned>(ceil_div(width, 64)), static_cast<unsigned>(a.E)), 256,
-                0, s, a);
-}
-
-template <typename T, bool kGatedForm>
-cudaError_t launch_fp8(const QuantArgs& args, int sms, cudaStream_t s) {
+cudaError_t launch_int8(const QuantArgs& a, int sms, cudaStream_t s) {
   constexpr int kUse = kGatedForm ? kGated : kForward;
-  QuantArgs a = args;
   CUtensorMap map_a, map_b;
   if (!(kGatedForm ? make_gated_map<uint8_t>(&map_a, a.weight, a.E, a.N / 2, a.K)
                    : make_map<uint8_t>(&map_a, a.weight, a.E, a.N, a.K, 128)) ||
       !make_map<uint8_t>(&map_b, a.codes, 0, a.num_rows, a.K, 64))
     return cudaErrorInvalidValue;
   const int64_t pairs = sms / 2;
-  const int splits =
-      tile_splits(most_tiles<kUse>(a, kMaxN), ceil_div(a.K, kGroupSlice), pairs);
+  const int splits = tile_splits(most_tiles<kUse>(a, kMaxN), ceil_div(a.K, kRawSlice), pairs);
   const int64_t tiles = most_tiles<kUse>(a, splits > 1 ? kMaxN : kLeastCap);
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
-  a.stages = quant_product_smem(a.E, kStages) <= kQuantProductMost ? kStages : kStages - 1;
+  const unsigned blocks = 2 * splits * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
+  return launch_clusters(k_int8_product<T, kUse>, dim3(blocks), dim3(2 * splits), kInt8Threads,
+                         int8_product_smem(a.E), s, map_a, map_b, a);
+}
+
+template <typename T, bool kGatedForm>
+cudaError_t launch_fp8(const QuantArgs& a, int sms, cudaStream_t s) {
+  constexpr int kUse = kGatedForm ? kGated : kForward;
+  CUtensorMap map_rows, map_weight;
+  if (!make_map<uint8_t>(&map_rows, a.codes, 0, a.num_rows, a.K, 64) ||
+      !make_map<uint8_t>(&map_weight, a.weight, a.E, a.N, a.K, 64))
+    return cudaErrorInvalidValue;
+  const int64_t pairs = sms / 2, tiles = most_tiles<kUse>(a, kTileRows);
+  if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
+  const int splits = tile_splits(tiles, ceil_div(a.K, kGroupSlice), pairs);
   const unsigned blocks = 2 * splits * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
   return launch_clusters(k_quant_product<T, kUse>, dim3(blocks), dim3(2 * splits),
-                         kQuantProductThreads, quant_product_smem(a.E, a.stages), s, map_a, map_b,
+                         kQuantProductThreads, quant_product_smem(a.E), s, map_rows, map_weight,
                          a);
 }
 
@@ -142,7 +146,7 @@ int moe_expert_gated_quant(const void* permuted_codes, const float* permuted_sca
   if (ffn_size < 0 || ffn_size > INT32_MAX / 4) return MOE_ERR_INVALID_ARG;
   const QuantArgs a = {expert_first_token_offset, num_rows, hidden_size, 2 * ffn_size,
                        num_local_experts, activation, permuted_codes, permuted_scales, weight,
-                       weight_scales, nullptr, nullptr, out, status_of(workspace), 0};
+                       weight_scales, nullptr, nullptr, out, status_of(workspace)};
   return product<true>(a, code_dtype, out_dtype, activation, ffn_size, workspace, stream);
 }
 
@@ -155,7 +159,7 @@ int moe_expert_linear_quant(const void* codes, const float* scales, const void* 
                             void* workspace, moe_stream_t stream) {
   const QuantArgs a = {expert_first_token_offset, num_rows, in_size, out_size, num_local_experts,
                        activation, codes, scales, weight, weight_scales, bias, residual, out,
-                       status_of(workspace), 0};
+                       status_of(workspace)};
   return product<false>(a, code_dtype, out_dtype, activation, out_size, workspace, stream);
 }
 

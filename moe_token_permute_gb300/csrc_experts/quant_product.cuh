@@ -3,21 +3,26 @@
 //   z[r, n] = sum over groups g of 128 columns of
 //             xs[r, g] ws[n / 128, g] sum_{k in g} x[r, k] w[n, k]
 //
-// The tiles are those of expert_product.cuh: a pair of SMs makes 256 x (up to 256)
-// outputs, weights being the A operand, and a slice is again 128 bytes deep, which here
-// is one group of scales.  A group's sum is scaled by a number of its own before it
-// joins the others, so each slice's products go to a tensor memory buffer of their own
-// (two, of 256 columns each) and the epilogue warps add it, scaled, to sums that stay in
-// their registers (128 a thread) while the next slice is multiplied.
+// A group's sum is scaled by a number of its own before it joins the others, so each
+// slice's products (128 deep: one group) go to a tensor memory buffer of their own, and
+// the epilogue warps add it, scaled, to sums that stay in their registers (128 a thread)
+// while the next slice is multiplied.
+//
+// Rows are the A operand here, so that a thread, which has one lane of tensor memory,
+// has one row: its scale is one number a slice (gated: two), and what is left is one
+// fused multiply-add a value.  A pair of SMs makes 256 rows x 256 features (gated: 128
+// gate and 128 up features, a block's half of B each); an expert's last rows pay for
+// 256, but up to 256 rows its weights' way from memory (700 cycles of a slice at the
+// copy bandwidth) is longer than the products' 512.  (With the weights as A the scales
+// lie along a thread's registers: they come from shared memory, by fragments, and a slice
+// took 1900 cycles instead of NNN.)
 //   warps 0-7    tensor memory -> registers, scaled; then the epilogue
 //   warp 8       TMA producer: 128-deep slices into a ring of 32 KB each
 //   warp 9       tcgen05.mma issue (first block), tensor memory allocation
-//   warps 10-11  the rows' scales, four slices at a time, into a ring of 12 slices
-// Fragments (tcgen05.ld.16x256b) give a thread 4 weight rows by 8 columns of a 32 x 32
-// block, so that it needs 8 scales for 32 values, and pairs of columns go through
-// fma.f32x2: a slice is about 100 instructions of a warp, 2 warps a scheduler, beside
-// 512 cycles of products.
+//   warps 10-11  fill up the warpgroup that gives its registers to warps 0-7
 #pragma once
+
+#include <type_traits>
 
 #include "expert_product.cuh"
 
@@ -25,12 +30,10 @@ namespace moe {
 namespace experts {
 
 constexpr int kGroupSlice = 128;   // contraction depth of one stage: a group of scales
-constexpr int kScaleChunk = 4;     // slices whose scales are loaded at once
-constexpr int kScaleChunks = 3;    // of the ring
-constexpr int kScaleSlots = kScaleChunk * kScaleChunks;
-constexpr int kScaleSlotBytes = kMaxN * 4;
+constexpr int kTileRows = 256;     // rows of a pair's tile
+constexpr int kBuffers = 2;        // of tensor memory, a slice's products each
 constexpr int kQuantProductThreads = 384;
-constexpr int kQuantEpilogueRegisters = 216, kQuantOtherRegisters = 72;
+constexpr int kQuantEpilogueRegisters = 224, kQuantOtherRegisters = 56;
 static_assert(2 * kQuantEpilogueRegisters + kQuantOtherRegisters <= 65536 / 384 / 8 * 8 * 3,
               "registers at launch: 168 a thread");
 
@@ -48,54 +51,92 @@ struct QuantArgs {
   const void* residual;
   void* out;
   unsigned* status;
-  int stages;  // of the ring
 };
 
-// Dynamic shared memory: stages (1024-byte aligned), staging, scales, then each
-// expert's rows and its first tile.
-inline size_t quant_product_smem(int E, int stages) {
-  return 1024 + static_cast<size_t>(stages) * kStageBytes + kStagingBytes +
-         kScaleSlots * kScaleSlotBytes + static_cast<size_t>(E) * 12 + 4;
+// Dynamic shared memory: stages (1024-byte aligned), then each expert's rows and its
+// first tile.
+inline size_t quant_product_smem(int E) {
+  return 1024 + kStages * kStageBytes + static_cast<size_t>(E) * 12 + 4;
 }
-// What a block may have beside its static shared memory.
-constexpr size_t kQuantProductMost = 227 * 1024 - 1024;
-static_assert(1024 + (kStages - 1) * kStageBytes + kStagingBytes + kScaleSlots * kScaleSlotBytes +
-                      MOE_MAX_LOCAL_EXPERTS * 12 + 4 <=
-                  kQuantProductMost,
+static_assert(1024 + kStages * kStageBytes + MOE_MAX_LOCAL_EXPERTS * 12 + 4 + 1024 <= 227 * 1024,
               "shared memory of one block");
 
-__device__ __forceinline__ float2 shared_load_f2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void shared_store_f(uint32_t addr, float v) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Up to 256 rows of one expert by the features from f0 on.
+struct QuantTile {
+  int e, lo, rows, f0;
+};
+
+__device__ __forceinline__ QuantTile find_quant_tile(int E, const Segment* segments,
+                                                     const int* first, int t, int f_blocks,
+                                                     int features) {
+  int lo = 0, hi = E;  // first[lo] <= t < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (first[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  const Segment s = segments[lo];
+  const int rows = s.hi - s.lo;
+  int f, n;
+  place_in_panels(t - first[lo], f_blocks, row_blocks(rows, kTileRows), f, n);
+  return {lo, s.lo + n * kTileRows, min(kTileRows, rows - n * kTileRows), f * features};
 }
 
-// map_a: the weight as TMA tiles of 128 bytes by 128 rows (gated: make_gated_map);
-// map_b: the rows, by 64 rows.
+// 32 bytes of a row; kWide: in one access, where rows are 32-byte aligned.
+template <bool kWide>
+__device__ __forceinline__ void store_32_bytes(void* at, const uint32_t (&v)[8]) {
+  if (kWide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(at)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    static_cast<uint4*>(at)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// z[0, 16), rounded, to columns c + [0, 16) of the row at `row`, of `width` (a multiple
+// of 8).
+template <typename T>
+__device__ __forceinline__ void store_16(T* row, const float* z, int64_t c, int64_t width,
+                                         bool wide) {
+  uint32_t p[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p[i] = pack2<T>(z[2 * i], z[2 * i + 1]);
+  if (c + 16 <= width) {
+    if (wide) store_32_bytes<true>(row + c, p);
+    else store_32_bytes<false>(row + c, p);
+  } else if (c + 8 <= width) {
+    *reinterpret_cast<uint4*>(row + c) = make_uint4(p[0], p[1], p[2], p[3]);
+  }
+}
+
+// A load that stays where it is written, ahead of its use.
+__device__ __forceinline__ float load_early(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
+// map_rows: the rows' codes, map_weight: the weight's [E, N, K], both as TMA tiles of 128
+// bytes by 64 rows.
 template <typename T, int kUse>
 __global__ void __launch_bounds__(kQuantProductThreads, 1)
-k_quant_product(const __grid_constant__ CUtensorMap map_a,
-                const __grid_constant__ CUtensorMap map_b, const QuantArgs a) {
+k_quant_product(const __grid_constant__ CUtensorMap map_rows,
+                const __grid_constant__ CUtensorMap map_weight, const QuantArgs a) {
   constexpr bool kGatedForm = kUse == kGated;
+  constexpr int kFeatures = m_step<kUse>();  // of a tile
   extern __shared__ uint8_t smem_raw[];
   // s_full and s_free are used in a pair's first block only, s_parts in the cluster's
   // first pair.
-  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_done[2], s_free[2],
-      s_scaled[kScaleChunks], s_used[kScaleChunks], s_parts;
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_done[kBuffers], s_free[kBuffers], s_parts;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_gave_up, s_cap;
+  __shared__ int s_gave_up;
   __shared__ uint32_t s_issued;  // slices that this block's producer has issued
-  __shared__ float s_block_scale[kScaleSlots][2];  // gated: the slice's gate and up blocks'
 
-  const int n_stages = a.stages;
   uint8_t* stages = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* staging = stages + n_stages * kStageBytes;
-  uint8_t* scale_ring = staging + kStagingBytes;
-  Segment* segments = reinterpret_cast<Segment*>(scale_ring + kScaleSlots * kScaleSlotBytes);
+  Segment* segments = reinterpret_cast<Segment*>(stages + kStages * kStageBytes);
   int* first = reinterpret_cast<int*>(segments + a.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Clusters of `splits` pairs; the block's place in its pair; the rank of the
@@ -106,24 +147,20 @@ k_quant_product(const __grid_constant__ CUtensorMap map_a,
   const int pair = blockIdx.x / (2 * splits), pairs = gridDim.x / (2 * splits);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < n_stages; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_addr(&s_full[i]), 1);
       mbar_init(smem_addr(&s_empty[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kBuffers; ++i) {
       mbar_init(smem_addr(&s_done[i]), 1);
       mbar_init(smem_addr(&s_free[i]), 2 * kEpiWarps);
-    }
-    for (int i = 0; i < kScaleChunks; ++i) {
-      mbar_init(smem_addr(&s_scaled[i]), 2);
-      mbar_init(smem_addr(&s_used[i]), kEpiWarps);
     }
     mbar_init(smem_addr(&s_parts), kEpiWarps);
     mbar_init_fence();
     s_gave_up = 0;
     s_issued = 0;
-    tma_prefetch_map(&map_a);
-    tma_prefetch_map(&map_b);
+    tma_prefetch_map(&map_rows);
+    tma_prefetch_map(&map_weight);
   }
   __syncthreads();
   cluster_arrive();  // this block's barriers exist
@@ -132,7 +169,7 @@ k_quant_product(const __grid_constant__ CUtensorMap map_a,
   pdl_launch_dependents();
 
   const int width = static_cast<int>(kGatedForm ? a.N / 2 : a.N);
-  const int m_blocks = (width + m_step<kUse>() - 1) / m_step<kUse>();
+  const int f_blocks = (width + kFeatures - 1) / kFeatures;
   const int groups = static_cast<int>((a.K + kGroupSlice - 1) / kGroupSlice);  // and slices
   for (int e = threadIdx.x; e < a.E; e += kQuantProductThreads) {
     bool bad;
@@ -141,15 +178,11 @@ k_quant_product(const __grid_constant__ CUtensorMap map_a,
       atomicOr(a.status, MOE_FLAG_OFFSET_OUT_OF_RANGE);
   }
   __syncthreads();
-  if (warp == 0) {
-    const int cap = scan_tiles(a.E, segments, first, splits > 1, m_blocks, groups, pairs);
-    if (lane == 0) s_cap = cap;
-  }
+  if (warp == 0) scan_tiles(a.E, segments, first, true, f_blocks, groups, pairs);
   tc_fence_before();
   __syncthreads();
   cluster_wait();  // the other blocks' barriers exist too
   tc_fence_after();
-  const int cap = s_cap;
   int total = first[a.E];
   // (More tiles than pairs only where bad offsets make segments overlap.)
   if (splits > 1) total = min(total, pairs);
@@ -160,30 +193,29 @@ k_quant_product(const __grid_constant__ CUtensorMap map_a,
   struct Ring {
     int at = 0;
     uint32_t pass = 0;
-    __device__ __forceinline__ void advance(int n) {
-      if (++at == n) at = 0, pass ^= 1;
+    __device__ __forceinline__ void advance() {
+      if (++at == kStages) at = 0, pass ^= 1;
     }
   };
   // After a wait gave up: what was issued last at each stage is given the time of
   // one wait to be used up, so that nothing is in flight when the block ends.
   auto drain = [&](Ring r, uint32_t issued) {
     const unsigned long long t0 = now_ns();
-    for (int i = 0; i < n_stages && static_cast<uint32_t>(i) < issued; ++i) {
-      if (r.at == 0) r.at = n_stages, r.pass ^= 1;
+    for (int i = 0; i < kStages && static_cast<uint32_t>(i) < issued; ++i) {
+      if (r.at == 0) r.at = kStages, r.pass ^= 1;
       --r.at;
       while (!mbar_try(smem_addr(&s_empty[r.at]), r.pass) && now_ns() - t0 < kWaitNs) {
       }
     }
   };
   auto tile_at = [&](int t) {
-    return find_tile<kUse>(a.E, segments, first, t, m_blocks, 0, 0, cap);
+    return find_quant_tile(a.E, segments, first, t, f_blocks, kFeatures);
   };
   const int first_slice = groups * split / splits;
   const int n_slices = groups * (split + 1) / splits - first_slice;
-  // Columns of a tile's product (each block holds half of B).
-  auto mma_n = [](int cols) { return (cols + 15) / 16 * 16; };
-  // First feature of the block's A tile.
-  auto feature = [&](const Tile& t) { return t.m0 + rank * (m_step<kUse>() / 2); };
+  // Rows of a tile in the pair's block r, and 64-row loads of them.
+  auto rows_of = [](const QuantTile& t, int r) { return min(128, t.rows - 128 * r); };
+  auto loads_of = [&](const QuantTile& t, int r) { return (max(0, rows_of(t, r)) + 63) / 64; };
 
   if (warp >= kEpiWarps) {
     fewer_registers<kQuantOtherRegisters>();
@@ -194,28 +226,29 @@ k_quant_product(const __grid_constant__ CUtensorMap map_a,
         bool ok = true;
         const uint32_t full0 = cluster_addr(smem_addr(&s_full[0]), leader);
         for (Walk walk(pair, pairs); walk.t < total && ok; walk.next()) {
-          const Tile tile = tile_at(walk.t);
-          const int half_n = mma_n(tile.cols) / 2;
-          const int b_boxes = (half_n + 63) / 64;
-          const uint32_t bytes = kTileABytes + b_boxes * kBoxBytes;
-          const int m = feature(tile), n = tile.lo + rank * half_n;
+          const QuantTile tile = tile_at(walk.t);
+          const int loads = loads_of(tile, rank);
+          const uint32_t bytes =
+              2 * kTileBBytes + (loads_of(tile, 0) + loads_of(tile, 1)) * kBoxBytes;
+          const int row = tile.lo + rank * 128;
+          const int f = kGatedForm ? tile.f0 + rank * width : tile.f0 + rank * 128;
           for (int s = 0; s < n_slices; ++s, ++issued) {
             const int st = ring.at;
-            if (withheld(issued) || !mbar_wait<false>(smem_addr(&s_empty[st]), ring.pass ^ 1, gave_up)) {
+            if (withheld(issued) || !mbar_wait_here(smem_addr(&s_empty[st]), ring.pass ^ 1, gave_up)) {
               ok = false;
               break;
             }
             *static_cast<volatile uint32_t*>(&s_issued) = issued + 1;
-            ring.advance(n_stages);
+            ring.advance();
             // Both blocks' loads report to the first block's barrier.
             const uint32_t full = full0 + st * 8;
-            if (rank == 0) mbar_expect(smem_addr(&s_full[st]), 2 * bytes);
-            const uint32_t sa = smem_addr(stages + st * kStageBytes);
+            if (rank == 0) mbar_expect(smem_addr(&s_full[st]), bytes);
+            const uint32_t sa = smem_addr(stages + st * kStageBytes), sb = sa + kTileABytes;
             const int k = (first_slice + s) * kGroupSlice;
-            if (kGatedForm) tma_load_5d(sa, &map_a, k, 0, 0, m / 8, tile.e, full);
-            else tma_load_3d(sa, &map_a, k, m, tile.e, full);
-            for (int i = 0; i < b_boxes; ++i)
-              tma_load_2d(sa + kTileABytes + i * kBoxBytes, &map_b, k, n + i * 64, full);
+            tma_load_3d(sb, &map_weight, k, f, tile.e, full);
+            tma_load_3d(sb + kBoxBytes, &map_weight, k, f + 64, tile.e, full);
+            for (int i = 0; i < loads; ++i)
+              tma_load_2d(sa + i * kBoxBytes, &map_rows, k, row + i * 64, full);
           }
         }
         if (*gave_up != 0) drain(ring, issued);
@@ -226,15 +259,14 @@ k_quant_product(const __grid_constant__ CUtensorMap map_a,
         Ring ring;
         uint32_t issued = 0;
         const uint16_t both = static_cast<uint16_t>(3u << leader);
+        const uint32_t idesc = instr_desc(false, false, false, 256, kMaxN);
         bool ok = true;
         for (Walk walk(pair, pairs); walk.t < total && ok; walk.next()) {
-          const Tile tile = tile_at(walk.t);
-          const uint32_t idesc = instr_desc(false, false, false, 256, mma_n(tile.cols));
           for (int s = 0; s < n_slices; ++s) {
-            const uint32_t buf = issued & 1, acc = tmem + buf * kMaxN;
             const int st = ring.at;
-            if (!mbar_wait<false>(smem_addr(&s_full[st]), ring.pass, gave_up) ||
-                !mbar_wait<false>(smem_addr(&s_free[buf]), (issued / 2 & 1) ^ 1, gave_up)) {
+            const uint32_t buf = issued & 1;
+            if (!mbar_wait_here(smem_addr(&s_full[st]), ring.pass, gave_up) ||
+                !mbar_wait_here(smem_addr(&s_free[buf]), (issued / 2 & 1) ^ 1, gave_up)) {
               ok = false;
               break;
             }
@@ -242,236 +274,182 @@ k_quant_product(const __grid_constant__ CUtensorMap map_a,
             const uint32_t pa = smem_addr(stages + st * kStageBytes), pb = pa + kTileABytes;
 #pragma unroll
             for (int i = 0; i < kGroupSlice / 32; ++i)
-              tc_mma_fp8(acc, smem_desc(pa + i * 32, 16, 1024), smem_desc(pb + i * 32, 16, 1024),
-                         idesc, i > 0);
+              tc_mma_fp8(tmem + buf * kMaxN, smem_desc(pa + i * 32, 16, 1024),
+                         smem_desc(pb + i * 32, 16, 1024), idesc, i > 0);
             tc_commit(smem_addr(&s_done[buf]), both);
             tc_commit(smem_addr(&s_empty[st]), both);
             ++issued;
-            ring.advance(n_stages);
+            ring.advance();
           }
         }
         // The products are over before the memory they read and write is given up.
         if (*gave_up != 0) drain(ring, issued);
       }
       __syncwarp();
-    } else {
-      // Scales of the tile's columns lane + 32 i of this warp's half, kScaleChunk
-      // slices of them in flight while those before are written.
-      const int c0 = (warp - kEpiWarps - 2) * (kMaxN / 2);
-      const int blocks = (width + kGroupSlice - 1) / kGroupSlice;
-      const bool whole = groups % kScaleChunk == 0 && first_slice % kScaleChunk == 0 &&
-                         (reinterpret_cast<uintptr_t>(a.scales) & 15) == 0;
-      constexpr int kMine = kMaxN / 2 / 32;
-      uint32_t step = 0;  // chunks so far
-      bool ok = true;
-      for (Walk walk(pair, pairs); walk.t < total && ok; walk.next()) {
-        const Tile tile = tile_at(walk.t);
-        const int64_t plane = static_cast<int64_t>(tile.e) * (kGatedForm ? 2 : 1) * blocks;
-        const int block = min(feature(tile) / kGroupSlice, blocks - 1);
-        const float* ws = a.weight_scales + (plane + block) * groups + first_slice;
-        const float* rows = a.scales + static_cast<int64_t>(tile.lo + c0 + lane) * groups + first_slice;
-        // w: lane k the block's scale of slice k of the chunk; gated, lane 4 + k the up
-        // block's.
-        float x[kMine][kScaleChunk], w;
-        ws += lane % kScaleChunk;
-        if (kGatedForm && lane / kScaleChunk == 1) ws += static_cast<int64_t>(blocks) * groups;
-        auto fetch = [&](int s) {
-          w = s + lane % kScaleChunk < n_slices ? __ldg(ws + s) : 0.f;
-#pragma unroll
-          for (int i = 0; i < kMine; ++i) {
-            const float* at = rows + static_cast<int64_t>(32 * i) * groups + s;
-            const bool in = c0 + lane + 32 * i < tile.cols;
-            if (whole && s + kScaleChunk <= n_slices) {
-              const float4 v = in ? __ldg(reinterpret_cast<const float4*>(at))
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-              x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
-            } else {
-#pragma unroll
-              for (int k = 0; k < kScaleChunk; ++k)
-                x[i][k] = in && s + k < n_slices ? __ldg(at + k) : 0.f;
-            }
-          }
-        };
-        fetch(0);
-        for (int s = 0; s < n_slices; s += kScaleChunk, ++step) {
-          const int chunk = static_cast<int>(step % kScaleChunks);
-          if (!warp_wait<false>(smem_addr(&s_used[chunk]), (step / kScaleChunks & 1) ^ 1, gave_up)) {
-            ok = false;
-            break;
-          }
-          const uint32_t to = smem_addr(scale_ring) + chunk * kScaleChunk * kScaleSlotBytes;
-#pragma unroll
-          for (int k = 0; k < kScaleChunk; ++k) {
-            const float by = kGatedForm ? 1.f : __shfl_sync(kFullMask, w, k);
-#pragma unroll
-            for (int i = 0; i < kMine; ++i)
-              shared_store_f(to + k * kScaleSlotBytes + (c0 + lane + 32 * i) * 4, x[i][k] * by);
-          }
-          if (kGatedForm && c0 == 0 && lane < 2 * kScaleChunk)
-            s_block_scale[chunk * kScaleChunk + lane % kScaleChunk][lane / kScaleChunk] = w;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&s_scaled[chunk]));
-          if (s + kScaleChunk < n_slices) fetch(s + kScaleChunk);
-        }
-      }
     }
   } else {
     more_registers<kQuantEpilogueRegisters>();
-    const int quad = warp & 3, q = lane & 3;
-    const uint32_t stage = smem_addr(staging + warp * kStagingWarpBytes);
-    T* out = static_cast<T*>(a.out);
-    T* residual = kGatedForm ? nullptr : static_cast<T*>(const_cast<void*>(a.residual));
-    uint32_t done = 0, step = 0;  // slices and chunks of scales so far
+    const int quad = warp & 3, half = warp / 4;
+    uint32_t done = 0;  // slices so far
     const uint32_t free0 = cluster_addr(smem_addr(&s_free[0]), leader);
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    // The warp's 32 features, its columns c0 + 64 j + [0, 32).
-    const int c0 = warp / 4 * 32;
+    // The warp's columns: four blocks of 32, two of each block's features.
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 64;
+    auto block_column = [](int j) { return (j >> 1) * 128 + (j & 1) * 32; };
     // Pairs that share a tile have one tile at most: its sums may lie over the
-    // stages, which are through.  A lane's 32 values of block j: 8 steps of 512 bytes.
-    const uint32_t part = smem_addr(stages + warp * 4 * 4096) + lane * 16;
+    // stages, which are through.  A lane's 128 values: 32 steps of 512 bytes.
+    const uint32_t part = smem_addr(stages + warp * 32 * 512) + lane * 16;
     const uint32_t other_part = splits > 1 ? cluster_addr(part, 2 + rank) : 0;
-    bool ok = true;
-    for (Walk walk(pair, pairs); walk.t < total && ok; walk.next()) {
-      const Tile tile = tile_at(walk.t);
-      const int cols = tile.cols;
-      uint64_t sums[4][16];  // z of block j: sums[j][8 h + 2 i + s], two columns each
+    const bool wide = width % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+    float d0[32], d1[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) d0[i] = d1[i] = 0.f;
+    for (Walk walk(pair, pairs); walk.t < total; walk.next()) {
+      const QuantTile tile = tile_at(walk.t);
+      const int rows = rows_of(tile, rank);
+      const bool any = quad * 32 < rows;
+      const int64_t row = tile.lo + rank * 128 + quad * 32 + lane;
+      float sums[4][32];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sums[j][i] = 0;
-      for (int s = 0; s < n_slices; ++s) {
-        const int within = s % kScaleChunk, chunk = static_cast<int>(step % kScaleChunks);
-        if (within == 0 && !warp_wait<false>(smem_addr(&s_scaled[chunk]), step / kScaleChunks & 1, gave_up)) {
-          ok = false;
-          break;
+        for (int i = 0; i < 32; ++i) sums[j][i] = 0.f;
+      bool ok = true;
+      if (!any) {  // no rows: only makes room
+        for (int s = 0; ok && s < n_slices; ++s, ++done) {
+          ok = warp_wait_here(smem_addr(&s_done[done & 1]), done / 2 & 1, gave_up);
+          if (ok && lane == 0) mbar_arrive_relaxed_cluster(free0 + (done & 1) * 8);
         }
-        const int slot = chunk * kScaleChunk + within;
-        const uint32_t scale = smem_addr(scale_ring) + slot * kScaleSlotBytes + (c0 + 2 * q) * 4;
-        uint64_t by_gate = 0, by_up = 0;
-        if (kGatedForm) {
-          const float gate = s_block_scale[slot][0], up = s_block_scale[slot][1];
-          by_gate = pack_f32x2(gate, gate), by_up = pack_f32x2(up, up);
+      } else {
+        // The row's scales and those of the weight's two blocks (gated: of gate and up),
+        // two slices ahead: behind the tiles' loads they take more than one.  (Lanes
+        // without a row take the last row's.)
+        const int blocks = (width + kGroupSlice - 1) / kGroupSlice, block = tile.f0 / kGroupSlice;
+        const int last = n_slices - 1;
+        const int64_t scaled = min(row, static_cast<int64_t>(tile.lo) + rank * 128 + rows - 1);
+        const float* xs = a.scales + scaled * groups + first_slice;
+        const float* ws =
+            a.weight_scales + first_slice +
+            (static_cast<int64_t>(tile.e) * (kGatedForm ? 2 : 1) * blocks + block) * groups;
+        const float* us = ws + static_cast<int64_t>(kGatedForm ? blocks : block + 1 < blocks) * groups;
+        float x[2], w[2], u[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int at = min(i, last);
+          x[i] = load_early(xs + at), w[i] = load_early(ws + at), u[i] = load_early(us + at);
         }
-        const uint32_t buf = done & 1, acc = lanes + buf * kMaxN + c0;
-        if (!warp_wait<false>(smem_addr(&s_done[buf]), done / 2 & 1, gave_up)) {
-          ok = false;
-          break;
-        }
-        ++done;
+        // Two blocks are on their way from tensor memory while two are added.
+        // (Behind the last slice what is loaded is not used.)
+        ok = warp_wait_here(smem_addr(&s_done[done & 1]), done / 2 & 1, gave_up);
         tc_fence_after();
-        // 16 lanes at a time, the next 16 being loaded meanwhile.
-        float d[32];
-        if (c0 < cols) tmem_load_16x32<0>(acc, d);
+        tmem_load_row32(lanes + (done & 1) * kMaxN, d0);
+        tmem_load_row32(lanes + (done & 1) * kMaxN + 32, d1);
+        for (int s = 0; ok && s < n_slices; ++s) {
+          const uint32_t acc = lanes + (done & 1) * kMaxN;
+          const float by_w = x[0] * w[0], by_u = x[0] * u[0];
+          x[0] = x[1], w[0] = w[1], u[0] = u[1];
+          const int ahead = min(s + 2, last);
+          x[1] = load_early(xs + ahead), w[1] = load_early(ws + ahead), u[1] = load_early(us + ahead);
+          tmem_wait_load(d0);
+          tmem_wait_load(d1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (c0 + 64 * j >= cols) break;
-          uint64_t by0[4], by1[4];
+          for (int i = 0; i < 32; ++i) sums[0][i] = fmaf(d0[i], by_w, sums[0][i]);
+          tmem_load_row32(acc + block_column(2), d0);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = shared_load_f2(scale + (64 * j + 8 * i) * 4);
-            const uint64_t xs = pack_f32x2(f.x, f.y);
-            by0[i] = kGatedForm ? mul_f32x2(xs, by_gate) : xs;
-            by1[i] = kGatedForm ? mul_f32x2(xs, by_up) : xs;
+          for (int i = 0; i < 32; ++i) sums[1][i] = fmaf(d1[i], by_w, sums[1][i]);
+          tmem_load_row32(acc + block_column(3), d1);
+          tmem_wait_load(d0);
+          tmem_wait_load(d1);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_relaxed_cluster(free0 + (done & 1) * 8);
+          ++done;
+          const bool more = s + 1 < n_slices;
+          const uint32_t bar = smem_addr(&s_done[done & 1]), parity = done / 2 & 1;
+          const bool over = !more || mbar_test_here(bar, parity);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sums[2][i] = fmaf(d0[i], by_u, sums[2][i]);
+          if (!__all_sync(kFullMask, over) && !warp_wait_here(bar, parity, gave_up)) {
+            ok = false;
+            break;
           }
-          auto add = [&](int h) {
+          tc_fence_after();
+          tmem_load_row32(lanes + (done & 1) * kMaxN, d0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float* v = d + 16 * h + 4 * i;
-              uint64_t* z = &sums[j][8 * h + 2 * i];
-              z[0] = fma_f32x2(pack_f32x2(v[0], v[1]), by0[i], z[0]);
-              z[1] = fma_f32x2(pack_f32x2(v[2], v[3]), by1[i], z[1]);
-            }
-          };
-          tmem_wait_load(d);
-          tmem_load_16x32<16>(acc + 64 * j + (16u << 16), d);
-          add(0);
-          tmem_wait_load(d);
-          if (j < 3 && c0 + 64 * (j + 1) < cols) tmem_load_16x32<0>(acc + 64 * (j + 1), d);
-          add(1);
+          for (int i = 0; i < 32; ++i) sums[3][i] = fmaf(d1[i], by_u, sums[3][i]);
+          tmem_load_row32(lanes + (done & 1) * kMaxN + 32, d1);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_relaxed_cluster(free0 + buf * 8);
-          if (within == kScaleChunk - 1 || s == n_slices - 1) mbar_arrive(smem_addr(&s_used[chunk]));
-        }
-        if (within == kScaleChunk - 1 || s == n_slices - 1) ++step;
+        tmem_wait_load(d0);
+        tmem_wait_load(d1);
       }
       if (!ok) break;
       if (splits > 1) {
         if (split > 0) {
+          if (any) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (c0 + 64 * j >= cols) break;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 x = unpack_f32x2(sums[j][2 * i]), y = unpack_f32x2(sums[j][2 * i + 1]);
-              shared_store16(part + j * 4096 + i * 512,
-                             make_uint4(__float_as_uint(x.x), __float_as_uint(x.y),
-                                        __float_as_uint(y.x), __float_as_uint(y.y)));
-            }
+            for (int j = 0; j < 32; ++j)
+              shared_store16(part + j * 512,
+                             make_uint4(__float_as_uint(sums[j / 8][j % 8 * 4]),
+                                        __float_as_uint(sums[j / 8][j % 8 * 4 + 1]),
+                                        __float_as_uint(sums[j / 8][j % 8 * 4 + 2]),
+                                        __float_as_uint(sums[j / 8][j % 8 * 4 + 3])));
           }
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&s_parts), rank));
           break;
         }
-        if (!warp_wait<false>(smem_addr(&s_parts), 0, gave_up,
-                       cluster_addr(smem_addr(&s_issued), 2 + rank)))
+        if (!warp_wait_here<false>(smem_addr(&s_parts), 0, gave_up,
+                              cluster_addr(smem_addr(&s_issued), 2 + rank)))
           break;
+        if (any) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float4 v = cluster_load4(other_part + j * 512);
+            float* z = &sums[j / 8][j % 8 * 4];
+            z[0] += v.x, z[1] += v.y, z[2] += v.z, z[3] += v.w;
+          }
+        }
       }
-      const int64_t m = feature(tile) + quad * (kGatedForm ? 16 : 32);
+      if (quad * 32 + lane >= rows) continue;
+      T* out = static_cast<T*>(a.out) + row * width;
+      if (kGatedForm) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = c0 + 64 * j;
-        if (c >= cols) break;
-        const int64_t row = tile.lo + c;
-        float z[32];
+        for (int j = 0; j < 2; ++j) {
+          apply_act<32>(a.act, sums[j]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 x = unpack_f32x2(sums[j][i]);
-          z[2 * i] = x.x, z[2 * i + 1] = x.y;
+          for (int i = 0; i < 32; ++i) sums[j][i] *= sums[2 + j][i];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            store_16(out, &sums[j][16 * i], tile.f0 + half * 64 + j * 32 + i * 16, width, wide);
         }
-        if (splits > 1) {
+      } else {
+        const T* bias = static_cast<const T*>(a.bias);
+        if (bias != nullptr) bias += static_cast<int64_t>(tile.e) * a.N;
+        const T* residual = static_cast<const T*>(a.residual);
+        if (residual != nullptr) residual += row * width;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 x = cluster_load4(other_part + j * 4096 + i * 512);
-            z[4 * i] += x.x, z[4 * i + 1] += x.y, z[4 * i + 2] += x.z, z[4 * i + 3] += x.w;
-          }
-        }
-        if (kGatedForm) {
-          // z[16 h + 4 i + 2 s + b]: gate (s = 0) or up of feature 8 h + g, row 8 i + 2 q + b.
-          float gate[16], up[16];
+        for (int j = 0; j < 4; ++j) {
+          // v += the 32 values from c on that exist
+          auto add = [&](float* v, const T* from, int64_t c) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {  // k = 4 i + 2 h + b
-            gate[k] = z[k / 2 % 2 * 16 + k / 4 * 4 + k % 2];
-            up[k] = z[k / 2 % 2 * 16 + k / 4 * 4 + 2 + k % 2];
-          }
-          apply_act<16>(a.act, gate);
+            for (int i = 0; i < 4; ++i) {
+              if (c + 8 * i >= width) break;
+              Vec8<T> p;
+              p.v = *reinterpret_cast<const uint4*>(from + c + 8 * i);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) gate[k] *= up[k];
-          write_half_block(gate, Block<T, 16>(out, width, row, cols - c, m, width, stage));
-        } else {
-          if (a.bias != nullptr) {
-            const T* bias = static_cast<const T*>(a.bias) + static_cast<int64_t>(tile.e) * a.N;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {  // z[16 h + 4 i + 2 s + b]: feature 16 h + 8 s + g
-              const int64_t f = m + k * 8 + (lane >> 2);
-              const float x = f < a.N ? to_f(bias[f]) : 0.f;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) z[k / 2 * 16 + i / 2 * 4 + k % 2 * 2 + i % 2] += x;
+              for (int k = 0; k < 8; ++k) v[8 * i + k] += to_f(p.e[k]);
             }
-          }
-          apply_act<32>(a.act, z);
-          if (residual != nullptr) {
-            uint4 r[4];
-            const Block<T> b(residual, a.N, row, cols - c, m, a.N, stage);
-            load_block(r, b);
-            add_block(z, r, b);
-          }
-          write_block(z, Block<T>(out, a.N, row, cols - c, m, a.N, stage));
+          };
+          const int64_t c = tile.f0 + half * 64 + block_column(j);
+          if (c >= width) break;
+          if (bias != nullptr) add(sums[j], bias, c);
+          apply_act<32>(a.act, sums[j]);
+          if (residual != nullptr) add(sums[j], residual, c);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) store_16(out, &sums[j][16 * i], c + 16 * i, width, wide);
         }
       }
     }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();

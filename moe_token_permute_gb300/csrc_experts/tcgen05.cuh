@@ -106,6 +106,32 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// The same for what the asynchronous engines did (copies, products), which is not read
+// through L1: an acquire of the cluster empties that, and takes 300 cycles.
+__device__ __forceinline__ bool mbar_try_here(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kNapNs)
+      : "memory");
+  return ok != 0;
+}
+
+// Whether the phase is over by now, without sleeping for it.
+__device__ __forceinline__ bool mbar_test_here(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
 // A wait gives up when kWaitNs pass without progress, or as soon as another wait of
 // the block has: `gave_up` is the block's flag in shared memory.  A wait for one copy
@@ -144,12 +170,13 @@ __device__ __forceinline__ uint32_t progress_at(uint32_t addr) {
   return v;
 }
 
+template <bool kHere>
 __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* gave_up,
                                                uint32_t progress) {
   unsigned long long t0 = now_ns();
   uint32_t seen = progress_at(progress);
   for (unsigned i = 0; i < (1u << 26); ++i) {
-    if (mbar_try(bar, parity)) return true;
+    if (kHere ? mbar_try_here(bar, parity) : mbar_try(bar, parity)) return true;
     if (*gave_up != 0) return false;
     if ((i & 63u) == 63u && now_ns() - t0 > wait_ns()) {
       const uint32_t at = progress_at(progress);
@@ -163,29 +190,44 @@ __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, vo
   return false;
 }
 
-// Out of line, where the kernel does not change its registers (setmaxnreg), which allows
-// no calls.
 static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity,
                                                    volatile int* gave_up, uint32_t progress) {
-  return mbar_wait_long(bar, parity, gave_up, progress);
+  return mbar_wait_long<false>(bar, parity, gave_up, progress);
 }
 
-template <bool kCalls = true>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
                                           uint32_t progress = kNoProgress) {
 #pragma unroll 1
   for (int i = 0; i < 8; ++i)
     if (mbar_try(bar, parity)) return true;
-  return kCalls ? mbar_wait_slow(bar, parity, gave_up, progress)
-                : mbar_wait_long(bar, parity, gave_up, progress);
+  return mbar_wait_slow(bar, parity, gave_up, progress);
+}
+
+// With mbar_try_here, and in line: a kernel that changes its registers (setmaxnreg) may
+// have no calls.  kHere false: with mbar_try.
+template <bool kHere = true>
+__device__ __forceinline__ bool mbar_wait_here(uint32_t bar, uint32_t parity,
+                                               volatile int* gave_up,
+                                               uint32_t progress = kNoProgress) {
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i)
+    if (kHere ? mbar_try_here(bar, parity) : mbar_try(bar, parity)) return true;
+  return mbar_wait_long<kHere>(bar, parity, gave_up, progress);
 }
 
 // One lane waits, the whole warp learns the outcome and is ordered behind it.
-template <bool kCalls = true>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
                                           uint32_t progress = kNoProgress) {
   bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait<kCalls>(bar, parity, gave_up, progress);
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, gave_up, progress);
+  return __all_sync(0xffffffffu, ok);
+}
+template <bool kHere = true>
+__device__ __forceinline__ bool warp_wait_here(uint32_t bar, uint32_t parity,
+                                               volatile int* gave_up,
+                                               uint32_t progress = kNoProgress) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait_here<kHere>(bar, parity, gave_up, progress);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -321,6 +363,24 @@ __device__ __forceinline__ void tmem_load_32x32(uint32_t addr, float (&v)[32]) {
   tmem_load_16x32<0>(addr, v);
   tmem_load_16x32<16>(addr + (16u << 16), v);
 }
+// 32 columns of the lane's own row of tensor memory.  Nothing may read v ahead of
+// tmem_wait_load.  (Read and written as far as the compiler knows, so that loads into the
+// same v in a loop keep to one set of registers: with copies between two, which wait for
+// the load, a slice of the fp8 products took twice as long.)
+__device__ __forceinline__ void tmem_load_row32(uint32_t addr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, "
+      "%8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, "
+      "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+        "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+        "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]),
+        "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]),
+        "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+      : "r"(addr));
+}
 // 64 columns of 16 of the warp's 32 lanes: v[4 i + 2 s + b] = D[lane 8 s + g][column
 // 8 i + 2 q + b].
 __device__ __forceinline__ void tmem_load_16x64(uint32_t addr, float (&v)[32]) {
@@ -374,28 +434,6 @@ __device__ __forceinline__ void load_matrices_transposed(uint32_t addr, uint32_t
                : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
                : "r"(addr)
                : "memory");
-}
-
-// Two fp32 at a time.
-__device__ __forceinline__ uint64_t pack_f32x2(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 
 // Registers of the threads of four warps; the block's shares together are at most what
