@@ -195,8 +195,7 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
           if (!mbar_wait_here(smem_addr(&s_free[buf]), (done / 2 & 1) ^ 1, gave_up, progress)) break;
           for (int s = 0; s < 2 * n_slices; ++s, ++issued) {
             const uint32_t st = issued % kWideStages;
-            // (the other block's warps wrote half of what is multiplied)
-            if (!mbar_wait_here<false>(smem_addr(&s_wide[st]), issued / kWideStages & 1, gave_up)) {
+            if (!mbar_wait_here(smem_addr(&s_wide[st]), issued / kWideStages & 1, gave_up)) {
               ok = false;
               break;
             }
@@ -265,7 +264,7 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
           }
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive_cluster(wide0 + at * 8);
+            mbar_arrive_written(wide0 + at * 8);
             if (h == 1) mbar_arrive(smem_addr(&s_read[st]));
           }
         }

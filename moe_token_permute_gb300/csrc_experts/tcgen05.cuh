@@ -51,6 +51,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
+// Behind writes to this block's shared memory and fence_async_shared: what the peer then
+// starts are products, which read them where they lie.  The cluster's release waits until
+// all that went before is performed everywhere, which here is nothing (an int8 product's
+// slice took 2800 cycles so).
+__device__ __forceinline__ void mbar_arrive_written(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 // Says only that this warp is through with reading, its values being in
 // registers: unlike a release it does not wait until the global stores before it
 // are performed, 1500 cycles.
