@@ -24,8 +24,9 @@ constexpr int kRawStages = 2;
 constexpr int kRawSlice = 128;     // codes of a raw stage
 constexpr int kWideStages = 4;     // of fp16, 64 deep
 constexpr int kInt8Threads = 640;
-constexpr int kInt8EpilogueRegisters = 168, kInt8OtherRegisters = 48;
-static_assert(2 * kInt8EpilogueRegisters + 3 * kInt8OtherRegisters <= 65536 / 640 / 8 * 8 * 5,
+constexpr int kInt8EpilogueRegisters = 144, kInt8ConvertRegisters = 72, kInt8OtherRegisters = 48;
+static_assert(2 * kInt8EpilogueRegisters + 2 * kInt8ConvertRegisters + kInt8OtherRegisters <=
+                  65536 / 640 / 8 * 8 * 5,
               "registers at launch: 96 a thread");
 
 // Dynamic shared memory: raw and fp16 stages (1024-byte aligned), staging, then each
@@ -158,7 +159,7 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
           for (int s = 0; s < n_slices; ++s, ++issued) {
             const uint32_t st = issued % kRawStages;
             if (withheld(issued) ||
-                !mbar_wait_here(smem_addr(&s_read[st]), (issued / kRawStages & 1) ^ 1, gave_up)) {
+                !mbar_wait_as<kWaitAwake>(smem_addr(&s_read[st]), (issued / kRawStages & 1) ^ 1, gave_up)) {
               ok = false;
               break;
             }
@@ -192,10 +193,10 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
           const Tile tile = tile_at(walk.t);
           const uint32_t idesc = instr_desc(false, false, false, 256, mma_n(tile.cols));
           const uint32_t buf = done & 1, acc = tmem + buf * kMaxN;
-          if (!mbar_wait_here(smem_addr(&s_free[buf]), (done / 2 & 1) ^ 1, gave_up, progress)) break;
+          if (!mbar_wait_as<kWaitAwake>(smem_addr(&s_free[buf]), (done / 2 & 1) ^ 1, gave_up, progress)) break;
           for (int s = 0; s < 2 * n_slices; ++s, ++issued) {
             const uint32_t st = issued % kWideStages;
-            if (!mbar_wait_here(smem_addr(&s_wide[st]), issued / kWideStages & 1, gave_up)) {
+            if (!mbar_wait_as<kWaitAwake>(smem_addr(&s_wide[st]), issued / kWideStages & 1, gave_up)) {
               ok = false;
               break;
             }
@@ -222,9 +223,10 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
       __syncwarp();
     }
   } else if (warp >= kConvert) {
-    fewer_registers<kInt8OtherRegisters>();
+    fewer_registers<kInt8ConvertRegisters>();
     // Warps 0-3 have the 128 rows of A, 4-7 those of B, a lane one row: chunk c of 16
-    // codes lies at c ^ (row % 8), and makes the chunks 2 c and 2 c + 1 of 8 numbers.
+    // codes lies at c ^ (row % 8), and makes the chunks 2 c and 2 c + 1 of 8 numbers.  A
+    // slice is read whole, so that the next copy into its stage starts at once.
     const int w = warp - kConvert, row = (w & 3) * 32 + lane, turn = lane & 7;
     const uint32_t offset = (w >> 2) * kTileABytes + row * 128;
     const uint32_t wide0 = cluster_addr(smem_addr(&s_wide[0]), leader);
@@ -235,19 +237,23 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
       const bool any = w < 4 || (w & 3) * 32 < mma_n(tile.cols) / 2;
       for (int s = 0; s < n_slices && ok; ++s, ++step) {
         const uint32_t st = step % kRawStages;
-        if (!warp_wait_here(smem_addr(&s_raw[st]), step / kRawStages & 1, gave_up)) {
+        if (!warp_wait_as<kWaitAwake>(smem_addr(&s_raw[st]), step / kRawStages & 1, gave_up)) {
           ok = false;
           break;
         }
         const uint32_t from = smem_addr(raw + st * kStageBytes) + offset;
+        uint4 c[8];
+        if (any) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) c[i] = shared_load16(from + ((i ^ turn) << 4));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&s_read[st]));
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t slice = 2 * step + h, at = slice % kWideStages;
-          uint4 c[4];
-          if (any) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) c[i] = shared_load16(from + (((4 * h + i) ^ turn) << 4));
-          }
-          if (!warp_wait_here(smem_addr(&s_empty[at]), (slice / kWideStages & 1) ^ 1, gave_up)) {
+          if (!warp_wait_as<kWaitAwake>(smem_addr(&s_empty[at]), (slice / kWideStages & 1) ^ 1,
+                                        gave_up)) {
             ok = false;
             break;
           }
@@ -255,18 +261,16 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
             const uint32_t to = smem_addr(stages + at * kStageBytes) + offset;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint2 x = codes_to_fp16(c[i].x), y = codes_to_fp16(c[i].y);
-              const uint2 z = codes_to_fp16(c[i].z), u = codes_to_fp16(c[i].w);
+              const uint4 v = c[4 * h + i];
+              const uint2 x = codes_to_fp16(v.x), y = codes_to_fp16(v.y);
+              const uint2 z = codes_to_fp16(v.z), u = codes_to_fp16(v.w);
               shared_store16(to + (((2 * i) ^ turn) << 4), make_uint4(x.x, x.y, y.x, y.y));
               shared_store16(to + (((2 * i + 1) ^ turn) << 4), make_uint4(z.x, z.y, u.x, u.y));
             }
             fence_async_shared();
           }
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive_written(wide0 + at * 8);
-            if (h == 1) mbar_arrive(smem_addr(&s_read[st]));
-          }
+          if (lane == 0) mbar_arrive_written(wide0 + at * 8);
         }
       }
     }
@@ -300,7 +304,7 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
                           : 0.f;
       }
       const uint32_t buf = done & 1;
-      if (!warp_wait_here(smem_addr(&s_done[buf]), done / 2 & 1, gave_up, progress)) break;
+      if (!warp_wait_as<kWaitNap>(smem_addr(&s_done[buf]), done / 2 & 1, gave_up, progress)) break;
       tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kMaxN;
       if (splits > 1) {
@@ -319,7 +323,7 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
           if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&s_parts), rank));
           break;
         }
-        if (!warp_wait_here<false>(smem_addr(&s_parts), 0, gave_up, cluster_addr(progress, 2 + rank)))
+        if (!warp_wait_as<kWaitCluster>(smem_addr(&s_parts), 0, gave_up, cluster_addr(progress, 2 + rank)))
           break;
       }
       for (int c = c0; c < cols; c += 64) {

@@ -234,7 +234,7 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
           const int f = kGatedForm ? tile.f0 + rank * width : tile.f0 + rank * 128;
           for (int s = 0; s < n_slices; ++s, ++issued) {
             const int st = ring.at;
-            if (withheld(issued) || !mbar_wait_here(smem_addr(&s_empty[st]), ring.pass ^ 1, gave_up)) {
+            if (withheld(issued) || !mbar_wait_as<kWaitHere>(smem_addr(&s_empty[st]), ring.pass ^ 1, gave_up)) {
               ok = false;
               break;
             }
@@ -265,8 +265,8 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
           for (int s = 0; s < n_slices; ++s) {
             const int st = ring.at;
             const uint32_t buf = issued & 1;
-            if (!mbar_wait_here(smem_addr(&s_full[st]), ring.pass, gave_up) ||
-                !mbar_wait_here(smem_addr(&s_free[buf]), (issued / 2 & 1) ^ 1, gave_up)) {
+            if (!mbar_wait_as<kWaitHere>(smem_addr(&s_full[st]), ring.pass, gave_up) ||
+                !mbar_wait_as<kWaitHere>(smem_addr(&s_free[buf]), (issued / 2 & 1) ^ 1, gave_up)) {
               ok = false;
               break;
             }
@@ -316,7 +316,7 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
       bool ok = true;
       if (!any) {  // no rows: only makes room
         for (int s = 0; ok && s < n_slices; ++s, ++done) {
-          ok = warp_wait_here(smem_addr(&s_done[done & 1]), done / 2 & 1, gave_up);
+          ok = warp_wait_as<kWaitHere>(smem_addr(&s_done[done & 1]), done / 2 & 1, gave_up);
           if (ok && lane == 0) mbar_arrive_relaxed_cluster(free0 + (done & 1) * 8);
         }
       } else {
@@ -339,7 +339,7 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
         }
         // Two blocks are on their way from tensor memory while two are added.
         // (Behind the last slice what is loaded is not used.)
-        ok = warp_wait_here(smem_addr(&s_done[done & 1]), done / 2 & 1, gave_up);
+        ok = warp_wait_as<kWaitHere>(smem_addr(&s_done[done & 1]), done / 2 & 1, gave_up);
         tc_fence_after();
         tmem_load_row32(lanes + (done & 1) * kMaxN, d0);
         tmem_load_row32(lanes + (done & 1) * kMaxN + 32, d1);
@@ -368,7 +368,7 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
           const bool over = !more || mbar_test_here(bar, parity);
 #pragma unroll
           for (int i = 0; i < 32; ++i) sums[2][i] = fmaf(d0[i], by_u, sums[2][i]);
-          if (!__all_sync(kFullMask, over) && !warp_wait_here(bar, parity, gave_up)) {
+          if (!__all_sync(kFullMask, over) && !warp_wait_as<kWaitHere>(bar, parity, gave_up)) {
             ok = false;
             break;
           }
@@ -397,7 +397,7 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
           if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&s_parts), rank));
           break;
         }
-        if (!warp_wait_here<false>(smem_addr(&s_parts), 0, gave_up,
+        if (!warp_wait_as<kWaitCluster>(smem_addr(&s_parts), 0, gave_up,
                               cluster_addr(smem_addr(&s_issued), 2 + rank)))
           break;
         if (any) {

@@ -177,13 +177,28 @@ __device__ __forceinline__ uint32_t progress_at(uint32_t addr) {
   return v;
 }
 
-template <bool kHere>
+// How a wait polls:
+//   kWaitCluster, kWaitHere  asleep for kNapNs, with the cluster's acquire or this block's;
+//                            a warp that fell asleep takes up to 1000 cycles to wake up
+//   kWaitAwake               all the time
+//   kWaitNap                 twice a microsecond
+enum Wait { kWaitCluster, kWaitHere, kWaitAwake, kWaitNap };
+template <Wait kHow>
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
+  if (kHow == kWaitCluster) return mbar_try(bar, parity);
+  if (kHow == kWaitHere) return mbar_try_here(bar, parity);
+  if (mbar_test_here(bar, parity)) return true;
+  __nanosleep(kHow == kWaitNap ? 500 : 20);
+  return false;
+}
+
+template <Wait kHow>
 __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* gave_up,
                                                uint32_t progress) {
   unsigned long long t0 = now_ns();
   uint32_t seen = progress_at(progress);
   for (unsigned i = 0; i < (1u << 26); ++i) {
-    if (kHere ? mbar_try_here(bar, parity) : mbar_try(bar, parity)) return true;
+    if (mbar_poll<kHow>(bar, parity)) return true;
     if (*gave_up != 0) return false;
     if ((i & 63u) == 63u && now_ns() - t0 > wait_ns()) {
       const uint32_t at = progress_at(progress);
@@ -199,7 +214,7 @@ __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, vo
 
 static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity,
                                                    volatile int* gave_up, uint32_t progress) {
-  return mbar_wait_long<false>(bar, parity, gave_up, progress);
+  return mbar_wait_long<kWaitCluster>(bar, parity, gave_up, progress);
 }
 
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
@@ -210,16 +225,14 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   return mbar_wait_slow(bar, parity, gave_up, progress);
 }
 
-// With mbar_try_here, and in line: a kernel that changes its registers (setmaxnreg) may
-// have no calls.  kHere false: with mbar_try.
-template <bool kHere = true>
-__device__ __forceinline__ bool mbar_wait_here(uint32_t bar, uint32_t parity,
-                                               volatile int* gave_up,
-                                               uint32_t progress = kNoProgress) {
+// The same in line: a kernel that changes its registers (setmaxnreg) may have no calls.
+template <Wait kHow>
+__device__ __forceinline__ bool mbar_wait_as(uint32_t bar, uint32_t parity, volatile int* gave_up,
+                                             uint32_t progress = kNoProgress) {
 #pragma unroll 1
   for (int i = 0; i < 8; ++i)
-    if (kHere ? mbar_try_here(bar, parity) : mbar_try(bar, parity)) return true;
-  return mbar_wait_long<kHere>(bar, parity, gave_up, progress);
+    if (mbar_poll<kHow>(bar, parity)) return true;
+  return mbar_wait_long<kHow>(bar, parity, gave_up, progress);
 }
 
 // One lane waits, the whole warp learns the outcome and is ordered behind it.
@@ -229,12 +242,14 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, gave_up, progress);
   return __all_sync(0xffffffffu, ok);
 }
-template <bool kHere = true>
-__device__ __forceinline__ bool warp_wait_here(uint32_t bar, uint32_t parity,
-                                               volatile int* gave_up,
-                                               uint32_t progress = kNoProgress) {
+template <Wait kHow>
+__device__ __forceinline__ bool warp_wait_as(uint32_t bar, uint32_t parity, volatile int* gave_up,
+                                             uint32_t progress = kNoProgress) {
+  // The whole warp asks once: without the split into lanes, a wait that is over costs a
+  // third.
+  if (kHow >= kWaitAwake && __all_sync(0xffffffffu, mbar_test_here(bar, parity))) return true;
   bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait_here<kHere>(bar, parity, gave_up, progress);
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait_as<kHow>(bar, parity, gave_up, progress);
   return __all_sync(0xffffffffu, ok);
 }
 
