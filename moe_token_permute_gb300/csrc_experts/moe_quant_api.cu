@@ -10,6 +10,7 @@
 #include "host_util.cuh"
 #include "int8_product.cuh"
 #include "product_host.cuh"
+#include "quant_decode.cuh"
 #include "quant_product.cuh"
 #include "quant_rows.cuh"
 
@@ -79,6 +80,22 @@ cudaError_t launch_fp8(const QuantArgs& a, int sms, cudaStream_t s) {
                          a);
 }
 
+template <typename T, bool kFp8, bool kGatedForm>
+cudaError_t launch_quant_product(const QuantArgs& a, int sms, cudaStream_t s) {
+  if (!quant_decode_pays(kGatedForm, a.num_rows, a.E, a.K))
+    return kFp8 ? launch_fp8<T, kGatedForm>(a, sms, s) : launch_int8<T, kGatedForm>(a, sms, s);
+  // Tasks at most: every expert with rows has one group, and each further
+  // kDecodeGroup rows one more.
+  const int64_t groups = std::min<int64_t>(a.E, a.num_rows) + a.num_rows / kDecodeGroup;
+  const int64_t tasks = groups * ((kGatedForm ? a.N / 2 : a.N) / kDecodeFeatures);
+  if (tasks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  CUtensorMap map;
+  if (!make_decode_map<uint8_t>(&map, a.weight, a.E, a.N, a.K)) return cudaErrorInvalidValue;
+  return launch(k_quant_decode<T, kFp8, kGatedForm>,
+                dim3(static_cast<unsigned>(std::min<int64_t>(tasks, sms))), kDecodeThreads,
+                DecodeShape<kGatedForm>::kSmem, s, map, a);
+}
+
 template <bool kGatedForm>
 int product(const QuantArgs& a, moe_dtype_t code_dtype, moe_dtype_t out_dtype,
             moe_activation_t activation, int64_t width, void* workspace, moe_stream_t stream) {
@@ -97,8 +114,10 @@ int product(const QuantArgs& a, moe_dtype_t code_dtype, moe_dtype_t out_dtype,
   if (sms == 0) return MOE_ERR_UNSUPPORTED_DEVICE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool fp8 = code_dtype == MOE_DTYPE_FP8_E4M3, bf = out_dtype == MOE_DTYPE_BF16;
-  auto run = fp8 ? (bf ? launch_fp8<__nv_bfloat16, kGatedForm> : launch_fp8<__half, kGatedForm>)
-                 : (bf ? launch_int8<__nv_bfloat16, kGatedForm> : launch_int8<__half, kGatedForm>);
+  auto run = fp8 ? (bf ? launch_quant_product<__nv_bfloat16, true, kGatedForm>
+                       : launch_quant_product<__half, true, kGatedForm>)
+                 : (bf ? launch_quant_product<__nv_bfloat16, false, kGatedForm>
+                       : launch_quant_product<__half, false, kGatedForm>);
   return finish(run(a, sms, s));
 }
 

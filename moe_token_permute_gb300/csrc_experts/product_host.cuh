@@ -78,11 +78,13 @@ bool make_map(CUtensorMap* map, const void* base, int64_t planes, int64_t rows, 
                             {kLineValues<T>, box_rows, 1});
 }
 
-// The weight [E, N, K] as [E, K/64, N, 64], tiles of blocks x rows x 64.
+// The weight [E, N, K] as [E, K/64, N, 64] (8 bits: 128 for 64), tiles of blocks x rows
+// x 64.
 template <typename T>
 bool make_decode_map(CUtensorMap* map, const void* base, int64_t E, int64_t N, int64_t K) {
-  return make_map_nd<T, 4>(map, base, {64, N, K / 64, E}, {K, 64, N * K},
-                           {64, kDecodeFeatures, kDecodeBlocks, 1});
+  constexpr int kLine = kLineValues<T>;
+  return make_map_nd<T, 4>(map, base, {kLine, N, K / kLine, E}, {K, kLine, N * K},
+                           {kLine, kDecodeFeatures, kDecodeBlocks, 1});
 }
 
 // The gated weight [E, 2, F, K] as [E, F/8, 2, 8, K], tiles of 8 x 2 x 8 rows by 64: in
