@@ -2,15 +2,15 @@
 // experts that have rows are streamed once, and that is the time.
 //
 // The kernel is expert_decode.cuh's with 128 codes in the place of 64 values of 16 bits:
-// the same tasks, ring, copies and reads, byte for byte.  A 128-byte line is a group of
-// scales, and falls to one warp: four instructions of mma.sync m16n8k32 in sums of their
-// own, which then join the task's, scaled.  int8 sums are whole numbers until the end.
+// the same tasks, ring, copies and reads, byte for byte.  Both kinds of codes become fp16,
+// which holds them exactly, and go through mma.sync m16n8k16: the 8-bit forms of mma.sync
+// are too slow on GB300 to keep up with the loads (2 rows of 8 x [14336 -> 4096]: int8
+// 34 us at 81% of that pipe, fp8 31).  A 128-byte line is a group of scales, and falls to
+// one warp: its products go to sums of their own, which then join the task's, scaled.
 #pragma once
 
-#include <type_traits>
-
 #include "expert_decode.cuh"
-#include "quant_product.cuh"
+#include "int8_product.cuh"
 
 namespace moe {
 namespace experts {
@@ -26,28 +26,29 @@ inline bool quant_decode_pays(bool gated, int64_t rows, int64_t E, int64_t K) {
   return rows <= std::min<int64_t>(most, kDecodeGroup * E) && K % 128 == 0;
 }
 
-__device__ __forceinline__ void mma_16832(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// 4 codes as fp16, two in each register.
+template <bool kFp8>
+__device__ __forceinline__ uint2 widen(uint32_t c) {
+  if (!kFp8) return codes_to_fp16(c);
+  uint2 r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(c));
+  return r;
 }
-__device__ __forceinline__ void mma_16832(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// 4 codes of 8 (gated: 16) weight rows and of 8 rows of x.
+template <bool kFp8, bool kGatedForm>
+__device__ __forceinline__ void multiply_codes(float (&c)[4], uint32_t v, uint32_t w, uint32_t u) {
+  const uint2 a = widen<kFp8>(v), x = widen<kFp8>(u);
+  const uint2 b = kGatedForm ? widen<kFp8>(w) : make_uint2(0, 0);
+  mma_16816<__half>(c, a.x, b.x, a.y, b.y, x.x, x.y);
 }
 
 // map: the weight as [E, K/128, N, 128], tiles of kDecodeBlocks x 8 x 128.
 template <typename T, bool kFp8, bool kGatedForm>
 __global__ void __launch_bounds__(kDecodeThreads, 1)
 k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
-  using Sum = typename std::conditional<kFp8, float, int>::type;
   const uint8_t* x = static_cast<const uint8_t*>(a.codes);
   using Shape = DecodeShape<kGatedForm>;
   constexpr int kRing = Shape::kRing;
@@ -58,7 +59,7 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
   __shared__ DecodeGroup s_groups[kDecodeMaxRows];
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Sum* parts = reinterpret_cast<Sum*>(ring + kRing * Shape::kStageBytes);
+  float* parts = reinterpret_cast<float*>(ring + kRing * Shape::kStageBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     s_gave_up = 0;
@@ -177,7 +178,7 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
              (static_cast<int64_t>(task.e) * (kGatedForm ? 2 : 1) * blocks +
               t.part * kDecodeFeatures / kGroupSlice) * scale_groups;
       }
-      Sum acc[kDecodeStep][4] = {};  // int8: chains of their own; fp8: blocks i and i + 1 in turn
+      float acc[kDecodeStep][4] = {};  // int8: chains of their own; fp8: blocks i and i + 1 in turn
       for (int s = 0; s < n_slices; ++s, ++step) {
         if ((step & 1) != warp / kDecodeSet) continue;
         const int st = step % kRing;
@@ -218,11 +219,13 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
         if (kFp8) {
 #pragma unroll
           for (int i = 0; i < kDecodeStep; i += 2) {
-            Sum part[2][4] = {};
+            float part[2][4] = {};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              mma_16832(part[j], v[i + j].x, w[i + j].x, v[i + j].y, w[i + j].y, u[i + j].x, u[i + j].y);
-              mma_16832(part[j], v[i + j].z, w[i + j].z, v[i + j].w, w[i + j].w, u[i + j].z, u[i + j].w);
+              multiply_codes<kFp8, kGatedForm>(part[j], v[i + j].x, w[i + j].x, u[i + j].x);
+              multiply_codes<kFp8, kGatedForm>(part[j], v[i + j].y, w[i + j].y, u[i + j].y);
+              multiply_codes<kFp8, kGatedForm>(part[j], v[i + j].z, w[i + j].z, u[i + j].z);
+              multiply_codes<kFp8, kGatedForm>(part[j], v[i + j].w, w[i + j].w, u[i + j].w);
             }
             // (a block behind K has zeros and the last block's scales)
 #pragma unroll
@@ -231,8 +234,10 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
         } else {
 #pragma unroll
           for (int i = 0; i < kDecodeStep; ++i) {
-            mma_16832(acc[i], v[i].x, w[i].x, v[i].y, w[i].y, u[i].x, u[i].y);
-            mma_16832(acc[i], v[i].z, w[i].z, v[i].w, w[i].w, u[i].z, u[i].w);
+            multiply_codes<kFp8, kGatedForm>(acc[i], v[i].x, w[i].x, u[i].x);
+            multiply_codes<kFp8, kGatedForm>(acc[i], v[i].y, w[i].y, u[i].y);
+            multiply_codes<kFp8, kGatedForm>(acc[i], v[i].z, w[i].z, u[i].z);
+            multiply_codes<kFp8, kGatedForm>(acc[i], v[i].w, w[i].w, u[i].w);
           }
         }
         __syncwarp();
@@ -241,7 +246,7 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
       if (!ok) break;
       const int buf = turn & 1;
       if (!warp_wait(smem_addr(&s_read[buf]), (turn / 2 & 1) ^ 1, gave_up)) break;
-      Sum* part = parts + buf * Shape::kPartFloats + warp * Shape::kWarpPitch +
+      float* part = parts + buf * Shape::kPartFloats + warp * Shape::kWarpPitch +
                     g * Shape::kRowPitch + q * 2;
       static_assert(kDecodeStep == 4, "the sum below");
 #pragma unroll
@@ -274,12 +279,12 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
       }
       // (spans a task's contraction)
       if (!warp_wait(smem_addr(&s_sums[buf]), turn / 2 & 1, gave_up, smem_addr(&s_issued))) break;
-      Sum z[kValues], up[kValues];
+      float z[kValues], up[kValues];
 #pragma unroll
       for (int j = 0; j < kValues; ++j) {
-        const Sum* part = parts + buf * Shape::kPartFloats + f * Shape::kRowPitch + r0 +
+        const float* part = parts + buf * Shape::kPartFloats + f * Shape::kRowPitch + r0 +
                           j * (32 / kDecodeFeatures);
-        z[j] = up[j] = 0;
+        z[j] = up[j] = 0.f;
 #pragma unroll
         for (int k = 0; k < kDecodeWarps; ++k) {
           z[j] += part[k * Shape::kWarpPitch];
@@ -295,9 +300,9 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
         const int r = r0 + j * (32 / kDecodeFeatures);
         if (r >= task.rows) break;
         const int64_t row = task.lo + r;
-        float v = kFp8 ? z[j] : static_cast<float>(z[j]) * by[j];
+        float v = kFp8 ? z[j] : z[j] * by[j];
         if (kGatedForm) {
-          const float y = kFp8 ? up[j] : static_cast<float>(up[j]) * by_up[j];
+          const float y = kFp8 ? up[j] : up[j] * by_up[j];
           out[row * F + c] = from_f<T>(act_of(a.act, v) * y);
         } else {
           if (a.bias != nullptr)
