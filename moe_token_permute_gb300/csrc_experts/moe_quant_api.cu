@@ -93,7 +93,7 @@ cudaError_t launch_quant_product(const QuantArgs& a, int sms, cudaStream_t s) {
   if (!make_decode_map<uint8_t>(&map, a.weight, a.E, a.N, a.K)) return cudaErrorInvalidValue;
   return launch(k_quant_decode<T, kFp8, kGatedForm>,
                 dim3(static_cast<unsigned>(std::min<int64_t>(tasks, sms))), kDecodeThreads,
-                DecodeShape<kGatedForm>::kSmem, s, map, a);
+                DecodeShape<true>::kSmem, s, map, a);
 }
 
 template <bool kGatedForm>

@@ -2,15 +2,20 @@
 // experts that have rows are streamed once, and that is the time.
 //
 // The kernel is expert_decode.cuh's with 128 codes in the place of 64 values of 16 bits:
-// the same tasks, ring, copies and reads, byte for byte.  Both kinds of codes become fp16,
-// which holds them exactly, and go through mma.sync m16n8k16: the 8-bit forms of mma.sync
-// are too slow on GB300 to keep up with the loads (2 rows of 8 x [14336 -> 4096]: int8
-// 34 us at 81% of that pipe, fp8 31).  A 128-byte line is a group of scales, and falls to
-// one warp: its products go to sums of their own, which then join the task's, scaled.
+// the same ring, copies and reads, byte for byte.  A 128-byte line is a group of
+// scales, and falls to one warp: four instructions of mma.sync m16n8k32 in sums of their
+// own, which then join the task's, scaled.  int8 sums are whole numbers until the end.
+// The 8-bit forms of mma.sync are slow on GB300, so all 16 rows of their A tile are used:
+// a task of the linear product has two tiles of 8 features where it can, and an SM an
+// even share of the tiles, one after another.  (2 rows of 8 x [14336 -> 4096], int8: with 8 features
+// a task 34 us, at 81% of that pipe; with the codes made fp16 for m16n8k16 32, bound by
+// the instructions.)
 #pragma once
 
+#include <type_traits>
+
 #include "expert_decode.cuh"
-#include "int8_product.cuh"
+#include "quant_product.cuh"
 
 namespace moe {
 namespace experts {
@@ -26,31 +31,30 @@ inline bool quant_decode_pays(bool gated, int64_t rows, int64_t E, int64_t K) {
   return rows <= std::min<int64_t>(most, kDecodeGroup * E) && K % 128 == 0;
 }
 
-// 4 codes as fp16, two in each register.
-template <bool kFp8>
-__device__ __forceinline__ uint2 widen(uint32_t c) {
-  if (!kFp8) return codes_to_fp16(c);
-  uint2 r;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(r.x), "=r"(r.y)
-      : "r"(c));
-  return r;
+__device__ __forceinline__ void mma_16832(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// 4 codes of 8 (gated: 16) weight rows and of 8 rows of x.
-template <bool kFp8, bool kGatedForm>
-__device__ __forceinline__ void multiply_codes(float (&c)[4], uint32_t v, uint32_t w, uint32_t u) {
-  const uint2 a = widen<kFp8>(v), x = widen<kFp8>(u);
-  const uint2 b = kGatedForm ? widen<kFp8>(w) : make_uint2(0, 0);
-  mma_16816<__half>(c, a.x, b.x, a.y, b.y, x.x, x.y);
+__device__ __forceinline__ void mma_16832(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // map: the weight as [E, K/128, N, 128], tiles of kDecodeBlocks x 8 x 128.
 template <typename T, bool kFp8, bool kGatedForm>
 __global__ void __launch_bounds__(kDecodeThreads, 1)
 k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
+  using Sum = typename std::conditional<kFp8, float, int>::type;
   const uint8_t* x = static_cast<const uint8_t*>(a.codes);
-  using Shape = DecodeShape<kGatedForm>;
+  using Shape = DecodeShape<true>;
   constexpr int kRing = Shape::kRing;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_full[kRing], s_empty[kRing], s_sums[2], s_read[2];
@@ -59,7 +63,7 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
   __shared__ DecodeGroup s_groups[kDecodeMaxRows];
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float* parts = reinterpret_cast<float*>(ring + kRing * Shape::kStageBytes);
+  Sum* parts = reinterpret_cast<Sum*>(ring + kRing * Shape::kStageBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     s_gave_up = 0;
@@ -102,16 +106,24 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
 
   const int F = static_cast<int>(kGatedForm ? a.N / 2 : a.N);
   const int per_group = F / kDecodeFeatures;  // F is a multiple of 8
-  // The block's tasks: t = blockIdx.x, blockIdx.x + gridDim.x, ... as (group,
-  // features), without a division.
+  // The block's tasks: its share of the tiles of 8 features, group by group; two at a time
+  // in the linear product.
   struct Task {
-    int group, part;
+    int group, part, tiles, left;  // `left` ahead of the task's own
   };
-  const Task start = {static_cast<int>(blockIdx.x) / per_group,
-                      static_cast<int>(blockIdx.x) % per_group};
+  const int64_t all = static_cast<int64_t>(groups) * per_group;
+  const int64_t begin = all * blockIdx.x / gridDim.x, end = all * (blockIdx.x + 1) / gridDim.x;
+  auto take = [&](Task& t) {
+    t.tiles = kGatedForm ? min(1, t.left) : min(min(2, per_group - t.part), t.left);
+  };
+  Task start = {static_cast<int>(begin / per_group), static_cast<int>(begin % per_group), 0,
+                static_cast<int>(end - begin)};
+  take(start);
   auto advance = [&](Task& t) {
-    t.part += gridDim.x;
-    while (t.part >= per_group) t.part -= per_group, ++t.group;
+    t.left -= t.tiles;
+    t.part += t.tiles;
+    if (t.part == per_group) t.part = 0, ++t.group;
+    take(t);
   };
   const int K = static_cast<int>(a.K);
   const int n_slices = (K + kDecodeCodes - 1) / kDecodeCodes;
@@ -122,7 +134,7 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
     if (elect_one()) {
       int step = 0;
       bool ok = true;
-      for (Task t = start; t.group < groups && ok; advance(t)) {
+      for (Task t = start; t.left > 0 && ok; advance(t)) {
         const DecodeGroup task = s_groups[t.group];
         const int f0 = t.part * kDecodeFeatures;
         const uint8_t* rows = x + static_cast<int64_t>(task.lo) * a.K;
@@ -130,21 +142,21 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
           const int st = step % kRing;
           const uint32_t full = smem_addr(&s_full[st]);
           if (withheld(step) ||
-              !mbar_wait(smem_addr(&s_empty[st]), (step / kRing & 1) ^ 1, gave_up)) {
+              !mbar_wait_as<kWaitAwake>(smem_addr(&s_empty[st]), (step / kRing & 1) ^ 1, gave_up)) {
             ok = false;
             break;
           }
           *static_cast<volatile uint32_t*>(&s_issued) = step + 1;
           const int k = s * kDecodeCodes;
           const uint32_t bytes = min(kDecodeCodes, K - k);
-          mbar_expect(full, Shape::kTiles * kDecodeTileBytes + task.rows * bytes);
+          mbar_expect(full, (kGatedForm ? 2 : t.tiles) * kDecodeTileBytes + task.rows * bytes);
           uint32_t dst = smem_addr(ring + st * Shape::kStageBytes);
           tma_load_4d_single(dst, &map, 0, f0, s * kDecodeBlocks, task.e, full);
           dst += kDecodeTileBytes;
-          if (kGatedForm) {
-            tma_load_4d_single(dst, &map, 0, F + f0, s * kDecodeBlocks, task.e, full);
-            dst += kDecodeTileBytes;
-          }
+          if (kGatedForm || t.tiles > 1)
+            tma_load_4d_single(dst, &map, 0, (kGatedForm ? F : kDecodeFeatures) + f0,
+                               s * kDecodeBlocks, task.e, full);
+          dst += kDecodeTileBytes;
           for (int i = 0; i < task.rows; ++i, dst += kDecodePitch)
             bulk_load(dst, rows + i * a.K + k, bytes, full);
         }
@@ -164,12 +176,13 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
     const uint4 zero = make_uint4(0, 0, 0, 0);
     int step = 0, turn = 0;
     bool ok = true;
-    for (Task t = start; t.group < groups && ok; advance(t), ++turn) {
+    for (Task t = start; t.left > 0 && ok; advance(t), ++turn) {
       const DecodeGroup task = s_groups[t.group];
       const int rows = task.rows;
-      // fp8: scales of rows 2 q and 2 q + 1 of x, and of the task's block of features.
+      const bool second = kGatedForm || t.tiles > 1;
+      // fp8: scales of rows 2 q and 2 q + 1 of x, and of the blocks of the tiles' features.
       const float* xs[2];
-      const float* ws = nullptr;
+      const float *ws = nullptr, *us = nullptr;
       if (kFp8) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -177,8 +190,12 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
         ws = a.weight_scales +
              (static_cast<int64_t>(task.e) * (kGatedForm ? 2 : 1) * blocks +
               t.part * kDecodeFeatures / kGroupSlice) * scale_groups;
+        const int next = kGatedForm ? blocks
+                                    : (t.part + t.tiles - 1) * kDecodeFeatures / kGroupSlice -
+                                          t.part * kDecodeFeatures / kGroupSlice;
+        us = ws + static_cast<int64_t>(next) * scale_groups;
       }
-      float acc[kDecodeStep][4] = {};  // int8: chains of their own; fp8: blocks i and i + 1 in turn
+      Sum acc[kDecodeStep][4] = {};  // int8: chains of their own; fp8: blocks i and i + 1 in turn
       for (int s = 0; s < n_slices; ++s, ++step) {
         if ((step & 1) != warp / kDecodeSet) continue;
         const int st = step % kRing;
@@ -187,8 +204,7 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
 #pragma unroll
           for (int i = 0; i < kDecodeStep / 2; ++i) {
             const int k = min(s * kDecodeBlocks + i * kDecodeSet + warp % kDecodeSet, scale_groups - 1);
-            const float w = __ldg(ws + k);
-            const float u = kGatedForm ? __ldg(ws + static_cast<int64_t>(blocks) * scale_groups + k) : 0.f;
+            const float w = __ldg(ws + k), u = __ldg(us + k);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const float v = __ldg(xs[j] + k);
@@ -196,7 +212,7 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
             }
           }
         }
-        if (!warp_wait(smem_addr(&s_full[st]), step / kRing & 1, gave_up)) {
+        if (!warp_wait_as<kWaitAwake>(smem_addr(&s_full[st]), step / kRing & 1, gave_up)) {
           ok = false;
           break;
         }
@@ -208,7 +224,7 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
           const int b = i / 2 * kDecodeSet + warp % kDecodeSet, c = 2 * q + (i & 1);
           const uint8_t* at = stage + (b * 8 + g) * 128 + ((c ^ g) << 4);
           v[i] = *reinterpret_cast<const uint4*>(at);
-          w[i] = kGatedForm ? *reinterpret_cast<const uint4*>(at + kDecodeTileBytes) : zero;
+          w[i] = second ? *reinterpret_cast<const uint4*>(at + kDecodeTileBytes) : zero;
           // Behind K the weights' tile is zero; the rows of x, there and behind
           // the last row, are older values.
           u[i] = g < rows && s * kDecodeCodes + b * 128 + c * 16 < K
@@ -219,13 +235,11 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
         if (kFp8) {
 #pragma unroll
           for (int i = 0; i < kDecodeStep; i += 2) {
-            float part[2][4] = {};
+            Sum part[2][4] = {};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              multiply_codes<kFp8, kGatedForm>(part[j], v[i + j].x, w[i + j].x, u[i + j].x);
-              multiply_codes<kFp8, kGatedForm>(part[j], v[i + j].y, w[i + j].y, u[i + j].y);
-              multiply_codes<kFp8, kGatedForm>(part[j], v[i + j].z, w[i + j].z, u[i + j].z);
-              multiply_codes<kFp8, kGatedForm>(part[j], v[i + j].w, w[i + j].w, u[i + j].w);
+              mma_16832(part[j], v[i + j].x, w[i + j].x, v[i + j].y, w[i + j].y, u[i + j].x, u[i + j].y);
+              mma_16832(part[j], v[i + j].z, w[i + j].z, v[i + j].w, w[i + j].w, u[i + j].z, u[i + j].w);
             }
             // (a block behind K has zeros and the last block's scales)
 #pragma unroll
@@ -234,10 +248,8 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
         } else {
 #pragma unroll
           for (int i = 0; i < kDecodeStep; ++i) {
-            multiply_codes<kFp8, kGatedForm>(acc[i], v[i].x, w[i].x, u[i].x);
-            multiply_codes<kFp8, kGatedForm>(acc[i], v[i].y, w[i].y, u[i].y);
-            multiply_codes<kFp8, kGatedForm>(acc[i], v[i].z, w[i].z, u[i].z);
-            multiply_codes<kFp8, kGatedForm>(acc[i], v[i].w, w[i].w, u[i].w);
+            mma_16832(acc[i], v[i].x, w[i].x, v[i].y, w[i].y, u[i].x, u[i].y);
+            mma_16832(acc[i], v[i].z, w[i].z, v[i].w, w[i].w, u[i].z, u[i].w);
           }
         }
         __syncwarp();
@@ -245,8 +257,8 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
       }
       if (!ok) break;
       const int buf = turn & 1;
-      if (!warp_wait(smem_addr(&s_read[buf]), (turn / 2 & 1) ^ 1, gave_up)) break;
-      float* part = parts + buf * Shape::kPartFloats + warp * Shape::kWarpPitch +
+      if (!warp_wait_as<kWaitAwake>(smem_addr(&s_read[buf]), (turn / 2 & 1) ^ 1, gave_up)) break;
+      Sum* part = parts + buf * Shape::kPartFloats + warp * Shape::kWarpPitch +
                     g * Shape::kRowPitch + q * 2;
       static_assert(kDecodeStep == 4, "the sum below");
 #pragma unroll
@@ -259,7 +271,7 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
   } else {
     T* out = static_cast<T*>(a.out);
     int turn = 0;
-    for (Task t = start; t.group < groups; advance(t), ++turn) {
+    for (Task t = start; t.left > 0; advance(t), ++turn) {
       const DecodeGroup task = s_groups[t.group];
       const int buf = turn & 1;
       // Value j of the lane: feature and row (j * 32 + lane) of the task.
@@ -269,7 +281,9 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
       float by[kValues], by_up[kValues];
       if (!kFp8) {
         const float* ws = a.weight_scales + static_cast<int64_t>(task.e) * a.N + c;
-        const float w = __ldg(ws), u = kGatedForm ? __ldg(ws + F) : 0.f;
+        const float w = __ldg(ws), u = kGatedForm    ? __ldg(ws + F)
+                                         : t.tiles > 1 ? __ldg(ws + kDecodeFeatures)
+                                                       : 0.f;
 #pragma unroll
         for (int j = 0; j < kValues; ++j) {
           const int r = min(r0 + j * (32 / kDecodeFeatures), task.rows - 1);
@@ -279,16 +293,16 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
       }
       // (spans a task's contraction)
       if (!warp_wait(smem_addr(&s_sums[buf]), turn / 2 & 1, gave_up, smem_addr(&s_issued))) break;
-      float z[kValues], up[kValues];
+      Sum z[kValues], up[kValues];
 #pragma unroll
       for (int j = 0; j < kValues; ++j) {
-        const float* part = parts + buf * Shape::kPartFloats + f * Shape::kRowPitch + r0 +
+        const Sum* part = parts + buf * Shape::kPartFloats + f * Shape::kRowPitch + r0 +
                           j * (32 / kDecodeFeatures);
-        z[j] = up[j] = 0.f;
+        z[j] = up[j] = 0;
 #pragma unroll
         for (int k = 0; k < kDecodeWarps; ++k) {
           z[j] += part[k * Shape::kWarpPitch];
-          if (kGatedForm) up[j] += part[k * Shape::kWarpPitch + kDecodeFeatures * Shape::kRowPitch];
+          up[j] += part[k * Shape::kWarpPitch + kDecodeFeatures * Shape::kRowPitch];
         }
       }
       // Before the results are stored: an arrival waits until the stores before
@@ -300,17 +314,21 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
         const int r = r0 + j * (32 / kDecodeFeatures);
         if (r >= task.rows) break;
         const int64_t row = task.lo + r;
-        float v = kFp8 ? z[j] : z[j] * by[j];
+        const float v = kFp8 ? z[j] : static_cast<float>(z[j]) * by[j];
+        const float y = kFp8 ? up[j] : static_cast<float>(up[j]) * by_up[j];
         if (kGatedForm) {
-          const float y = kFp8 ? up[j] : up[j] * by_up[j];
           out[row * F + c] = from_f<T>(act_of(a.act, v) * y);
         } else {
-          if (a.bias != nullptr)
-            v += to_f(static_cast<const T*>(a.bias)[static_cast<int64_t>(task.e) * a.N + c]);
-          v = act_of(a.act, v);
-          if (a.residual != nullptr)
-            v += to_f(static_cast<const T*>(a.residual)[row * a.N + c]);
-          out[row * a.N + c] = from_f<T>(v);
+          auto store = [&](float z, int64_t f) {
+            if (a.bias != nullptr)
+              z += to_f(static_cast<const T*>(a.bias)[static_cast<int64_t>(task.e) * a.N + f]);
+            z = act_of(a.act, z);
+            if (a.residual != nullptr)
+              z += to_f(static_cast<const T*>(a.residual)[row * a.N + f]);
+            out[row * a.N + f] = from_f<T>(z);
+          };
+          store(v, c);
+          if (t.tiles > 1) store(y, c + kDecodeFeatures);
         }
       }
     }
