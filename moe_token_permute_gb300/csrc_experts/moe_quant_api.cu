@@ -5,6 +5,7 @@
 #include "moe_quant.h"
 
 #include <algorithm>
+#include <type_traits>
 
 #include "expert_math.cuh"
 #include "host_util.cuh"
@@ -41,10 +42,28 @@ int finish(cudaError_t err) {
   return MOE_ERR_CUDA;
 }
 
-template <typename T, bool kFp8>
-cudaError_t launch_quant_rows(const QuantRowsArgs& a, int sms, cudaStream_t s) {
-  const int64_t grid = std::min<int64_t>(a.num_rows, 8 * static_cast<int64_t>(sms));
-  return launch(k_quant_rows<T, kFp8>, dim3(static_cast<unsigned>(grid)), kQuantThreads, 0, s, a);
+template <typename T, bool kWide>
+cudaError_t launch_quant_fp8(const QuantRowsArgs& a, int sms, cudaStream_t s) {
+  // As many blocks as there are rounds of 4 pieces a thread, up to 8 an SM.
+  const int64_t slots = a.num_rows * ceil_div(a.H, kQuantGroup) * 8;
+  const int64_t grid = std::min<int64_t>(ceil_div(slots, kQuantThreads), 8 * static_cast<int64_t>(sms));
+  return launch(k_quant_rows_fp8<T, kWide>, dim3(static_cast<unsigned>(grid)), kQuantThreads, 0, s,
+                a);
+}
+
+template <typename T, bool kWide>
+cudaError_t launch_quant_int8(const QuantRowsArgs& a, int sms, cudaStream_t s) {
+  // A warp a row up to 2048 columns, unless there are too few rows for that to fill the
+  // SMs; a block beyond 4096.
+  const int64_t pieces = a.H / 16;
+  const bool few = a.num_rows < 16 * static_cast<int64_t>(sms);
+  const int threads = pieces <= (few ? 32 : 128) ? 32 : pieces <= (few ? 128 : 256) ? 64 : 256;
+  auto kern = threads == 32   ? k_quant_rows_int8<T, kWide, 32, 4>
+              : threads == 64 ? k_quant_rows_int8<T, kWide, 64, 4>
+                              : k_quant_rows_int8<T, kWide, 256, 4>;
+  const int64_t grid = std::min<int64_t>(ceil_div(a.num_rows, kQuantThreads / threads),
+                                         8 * static_cast<int64_t>(sms));
+  return launch(kern, dim3(static_cast<unsigned>(grid)), kQuantThreads, 0, s, a);
 }
 
 template <typename T, bool kGatedForm>
@@ -149,10 +168,15 @@ int moe_quant_rows(const void* rows, moe_dtype_t dtype, const int64_t* expert_fi
   const QuantRowsArgs a = {rows, expert_first_token_offset, num_rows, hidden_size,
                            num_local_experts, codes, scales, status_of(workspace)};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool fp8 = code_dtype == MOE_DTYPE_FP8_E4M3, bf = dtype == MOE_DTYPE_BF16;
-  auto run = fp8 ? (bf ? launch_quant_rows<__nv_bfloat16, true> : launch_quant_rows<__half, true>)
-                 : (bf ? launch_quant_rows<__nv_bfloat16, false>
-                       : launch_quant_rows<__half, false>);
+  auto pick = [&](auto type, auto wide) {
+    using T = decltype(type);
+    return code_dtype == MOE_DTYPE_FP8_E4M3 ? launch_quant_fp8<T, decltype(wide)::value>
+                                            : launch_quant_int8<T, decltype(wide)::value>;
+  };
+  const bool wide = aligned(rows, 32);
+  auto run = dtype == MOE_DTYPE_BF16
+                 ? (wide ? pick(__nv_bfloat16(), std::true_type()) : pick(__nv_bfloat16(), std::false_type()))
+                 : (wide ? pick(__half(), std::true_type()) : pick(__half(), std::false_type()));
   return finish(run(a, sms, s));
 }
 
