@@ -44,9 +44,8 @@ int finish(cudaError_t err) {
 
 template <typename T, bool kWide>
 cudaError_t launch_quant_fp8(const QuantRowsArgs& a, int sms, cudaStream_t s) {
-  // As many blocks as there are rounds of 4 pieces a thread, up to 8 an SM.
   const int64_t slots = a.num_rows * ceil_div(a.H, kQuantGroup) * 8;
-  const int64_t grid = std::min<int64_t>(ceil_div(slots, kQuantThreads), 8 * static_cast<int64_t>(sms));
+  const int64_t grid = std::min<int64_t>(ceil_div(slots, kQuantThreads), kFp8Blocks * static_cast<int64_t>(sms));
   return launch(k_quant_rows_fp8<T, kWide>, dim3(static_cast<unsigned>(grid)), kQuantThreads, 0, s,
                 a);
 }
@@ -58,11 +57,12 @@ cudaError_t launch_quant_int8(const QuantRowsArgs& a, int sms, cudaStream_t s) {
   const int64_t pieces = a.H / 16;
   const bool few = a.num_rows < 16 * static_cast<int64_t>(sms);
   const int threads = pieces <= (few ? 32 : 128) ? 32 : pieces <= (few ? 128 : 256) ? 64 : 256;
-  auto kern = threads == 32   ? k_quant_rows_int8<T, kWide, 32, 4>
-              : threads == 64 ? k_quant_rows_int8<T, kWide, 64, 4>
-                              : k_quant_rows_int8<T, kWide, 256, 4>;
+  auto kern = pieces <= 64 && threads == 32 ? k_quant_rows_int8<T, kWide, 32, 2>
+              : threads == 32               ? k_quant_rows_int8<T, kWide, 32, 4>
+              : threads == 64               ? k_quant_rows_int8<T, kWide, 64, 4>
+                                            : k_quant_rows_int8<T, kWide, 256, 4>;
   const int64_t grid = std::min<int64_t>(ceil_div(a.num_rows, kQuantThreads / threads),
-                                         8 * static_cast<int64_t>(sms));
+                                         kInt8Blocks * static_cast<int64_t>(sms));
   return launch(kern, dim3(static_cast<unsigned>(grid)), kQuantThreads, 0, s, a);
 }
 
