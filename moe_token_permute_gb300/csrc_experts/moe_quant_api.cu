@@ -88,13 +88,13 @@ cudaError_t launch_fp8(const QuantArgs& a, int sms, cudaStream_t s) {
   constexpr int kUse = kGatedForm ? kGated : kForward;
   CUtensorMap map_rows, map_weight;
   if (!make_map<uint8_t>(&map_rows, a.codes, 0, a.num_rows, a.K, 64) ||
-      !make_map<uint8_t>(&map_weight, a.weight, a.E, a.N, a.K, 64))
+      !make_map<uint8_t>(&map_weight, a.weight, a.E, a.N, a.K, 128))
     return cudaErrorInvalidValue;
-  const int64_t pairs = sms / 2, tiles = most_tiles<kUse>(a, kTileRows);
+  const int64_t tiles = most_tiles<kUse>(a, kTileRows);
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
-  const int splits = tile_splits(tiles, ceil_div(a.K, kGroupSlice), pairs);
-  const unsigned blocks = 2 * splits * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
-  return launch_clusters(k_quant_product<T, kUse>, dim3(blocks), dim3(2 * splits),
+  const int splits = tile_splits(tiles, ceil_div(a.K, kGroupSlice), sms);
+  const unsigned blocks = splits * static_cast<unsigned>(std::min<int64_t>(tiles, sms / splits));
+  return launch_clusters(k_quant_product<T, kUse>, dim3(blocks), dim3(splits),
                          kQuantProductThreads, quant_product_smem(a.E), s, map_rows, map_weight,
                          a);
 }

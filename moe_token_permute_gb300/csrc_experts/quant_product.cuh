@@ -10,15 +10,14 @@
 //
 // Rows are the A operand here, so that a thread, which has one lane of tensor memory,
 // has one row: its scale is one number a slice (gated: two), and what is left is one
-// fused multiply-add a value.  A pair of SMs makes 256 rows x 256 features (gated: 128
-// gate and 128 up features, a block's half of B each); an expert's last rows pay for
-// 256, but up to 256 rows its weights' way from memory (700 cycles of a slice at the
-// copy bandwidth) is longer than the products' 512.  (With the weights as A the scales
-// lie along a thread's registers: they come from shared memory, by fragments, and a slice
-// took 1900 cycles instead of NNN.)
+// fused multiply-add a value.  A block makes 128 rows x 256 features (gated: 128 gate and
+// 128 up features).  (With the weights as A the scales lie along a thread's registers: they
+// come from shared memory, by fragments, and a slice took 1900 cycles.  Pairs of SMs with
+// 256 rows load a third less, but each buffer's way from products to sums and back crosses
+// between them, and few rows leave half of a pair idle.)
 //   warps 0-7    tensor memory -> registers, scaled; then the epilogue
-//   warp 8       TMA producer: 128-deep slices into a ring of 32 KB each
-//   warp 9       tcgen05.mma issue (first block), tensor memory allocation
+//   warp 8       TMA producer: 128-deep slices into a ring of 4 x 48 KB
+//   warp 9       tcgen05.mma issue, tensor memory allocation
 //   warps 10-11  fill up the warpgroup that gives its registers to warps 0-7
 #pragma once
 
@@ -30,7 +29,11 @@ namespace moe {
 namespace experts {
 
 constexpr int kGroupSlice = 128;   // contraction depth of one stage: a group of scales
-constexpr int kTileRows = 256;     // rows of a pair's tile
+constexpr int kTileRows = 128;
+constexpr int kTileFeatures = 256;  // rows of the weight
+constexpr int kRowsBytes = kTileRows * kGroupSlice, kWeightBytes = kTileFeatures * kGroupSlice;
+constexpr int kFp8StageBytes = kRowsBytes + kWeightBytes;
+constexpr int kFp8Stages = 4;
 constexpr int kBuffers = 2;        // of tensor memory, a slice's products each
 constexpr int kQuantProductThreads = 384;
 constexpr int kQuantEpilogueRegisters = 224, kQuantOtherRegisters = 56;
@@ -56,12 +59,13 @@ struct QuantArgs {
 // Dynamic shared memory: stages (1024-byte aligned), then each expert's rows and its
 // first tile.
 inline size_t quant_product_smem(int E) {
-  return 1024 + kStages * kStageBytes + static_cast<size_t>(E) * 12 + 4;
+  return 1024 + kFp8Stages * kFp8StageBytes + static_cast<size_t>(E) * 12 + 4;
 }
-static_assert(1024 + kStages * kStageBytes + MOE_MAX_LOCAL_EXPERTS * 12 + 4 + 1024 <= 227 * 1024,
+static_assert(1024 + kFp8Stages * kFp8StageBytes + MOE_MAX_LOCAL_EXPERTS * 12 + 4 + 1024 <=
+                  227 * 1024,
               "shared memory of one block");
 
-// Up to 256 rows of one expert by the features from f0 on.
+// Up to 128 rows of one expert by the features from f0 on.
 struct QuantTile {
   int e, lo, rows, f0;
 };
@@ -118,8 +122,34 @@ __device__ __forceinline__ float load_early(const float* p) {
   return v;
 }
 
-// map_rows: the rows' codes, map_weight: the weight's [E, N, K], both as TMA tiles of 128
-// bytes by 64 rows.
+// Each expert's first tile, of 128 rows by f_blocks blocks of features, and their number
+// (one warp).  The host has made sure that the tiles of num_rows rows can be counted; where
+// bad offsets make segments overlap, those beyond kMostTiles are left out.
+__device__ __forceinline__ void count_quant_tiles(int E, const Segment* segments, int* first,
+                                                  int f_blocks) {
+  constexpr int64_t kMostTiles = INT32_MAX / 2;
+  const int lane = threadIdx.x & 31;
+  int64_t before = 0;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int e = e0 + lane;
+    const int64_t n = e < E ? static_cast<int64_t>(row_blocks(
+                                  segments[e].hi - segments[e].lo, kTileRows)) * f_blocks
+                            : 0;
+    int64_t sum = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(kFullMask, sum, d);
+      if (lane >= d) sum += x;
+    }
+    if (e < E) first[e] = static_cast<int>(min(kMostTiles, before + sum - n));
+    before += __shfl_sync(kFullMask, sum, 31);
+  }
+  if (lane == 0) first[E] = static_cast<int>(min(kMostTiles, before));
+}
+
+// map_rows: the rows' codes as TMA tiles of 128 bytes by 64 rows, map_weight: the
+// weight's [E, N, K] by 128 rows.  A block, or two in a cluster, which share a tile's
+// contraction.
 template <typename T, int kUse>
 __global__ void __launch_bounds__(kQuantProductThreads, 1)
 k_quant_product(const __grid_constant__ CUtensorMap map_rows,
@@ -127,33 +157,29 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
   constexpr bool kGatedForm = kUse == kGated;
   constexpr int kFeatures = m_step<kUse>();  // of a tile
   extern __shared__ uint8_t smem_raw[];
-  // s_full and s_free are used in a pair's first block only, s_parts in the cluster's
-  // first pair.
-  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_done[kBuffers], s_free[kBuffers], s_parts;
+  // s_parts is used in the cluster's first block only.
+  __shared__ __align__(8) uint64_t s_full[kFp8Stages], s_empty[kFp8Stages], s_done[kBuffers],
+      s_free[kBuffers], s_parts;
   __shared__ uint32_t s_tmem;
   __shared__ int s_gave_up;
   __shared__ uint32_t s_issued;  // slices that this block's producer has issued
 
   uint8_t* stages = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Segment* segments = reinterpret_cast<Segment*>(stages + kStages * kStageBytes);
+  Segment* segments = reinterpret_cast<Segment*>(stages + kFp8Stages * kFp8StageBytes);
   int* first = reinterpret_cast<int*>(segments + a.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // Clusters of `splits` pairs; the block's place in its pair; the rank of the
-  // pair's first block.
-  const uint32_t place = cluster_rank(), leader = place & ~1u;
-  const int rank = static_cast<int>(place & 1u), split = static_cast<int>(place / 2);
-  const int splits = static_cast<int>(cluster_size() / 2);
-  const int pair = blockIdx.x / (2 * splits), pairs = gridDim.x / (2 * splits);
+  const int split = static_cast<int>(cluster_rank()), splits = static_cast<int>(cluster_size());
+  const int worker = blockIdx.x / splits, workers = gridDim.x / splits;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kFp8Stages; ++i) {
       mbar_init(smem_addr(&s_full[i]), 1);
       mbar_init(smem_addr(&s_empty[i]), 1);
     }
     for (int i = 0; i < kBuffers; ++i) {
       mbar_init(smem_addr(&s_done[i]), 1);
-      mbar_init(smem_addr(&s_free[i]), 2 * kEpiWarps);
+      mbar_init(smem_addr(&s_free[i]), kEpiWarps);
     }
     mbar_init(smem_addr(&s_parts), kEpiWarps);
     mbar_init_fence();
@@ -164,7 +190,7 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
   }
   __syncthreads();
   cluster_arrive();  // this block's barriers exist
-  if (warp == kEpiWarps + 1) tmem_alloc(smem_addr(&s_tmem), 512);
+  if (warp == kEpiWarps + 1) tmem_alloc_single(smem_addr(&s_tmem), 512);
   pdl_wait();
   pdl_launch_dependents();
 
@@ -178,14 +204,14 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
       atomicOr(a.status, MOE_FLAG_OFFSET_OUT_OF_RANGE);
   }
   __syncthreads();
-  if (warp == 0) scan_tiles(a.E, segments, first, true, f_blocks, groups, pairs);
+  if (warp == 0) count_quant_tiles(a.E, segments, first, f_blocks);
   tc_fence_before();
   __syncthreads();
-  cluster_wait();  // the other blocks' barriers exist too
+  cluster_wait();  // the other block's barriers exist too
   tc_fence_after();
   int total = first[a.E];
-  // (More tiles than pairs only where bad offsets make segments overlap.)
-  if (splits > 1) total = min(total, pairs);
+  // (More tiles than workers only where bad offsets make segments overlap.)
+  if (splits > 1) total = min(total, workers);
   const uint32_t tmem = s_tmem;
   volatile int* gave_up = &s_gave_up;
 
@@ -194,17 +220,17 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
     int at = 0;
     uint32_t pass = 0;
     __device__ __forceinline__ void advance() {
-      if (++at == kStages) at = 0, pass ^= 1;
+      if (++at == kFp8Stages) at = 0, pass ^= 1;
     }
   };
   // After a wait gave up: what was issued last at each stage is given the time of
   // one wait to be used up, so that nothing is in flight when the block ends.
   auto drain = [&](Ring r, uint32_t issued) {
     const unsigned long long t0 = now_ns();
-    for (int i = 0; i < kStages && static_cast<uint32_t>(i) < issued; ++i) {
-      if (r.at == 0) r.at = kStages, r.pass ^= 1;
+    for (int i = 0; i < kFp8Stages && static_cast<uint32_t>(i) < issued; ++i) {
+      if (r.at == 0) r.at = kFp8Stages, r.pass ^= 1;
       --r.at;
-      while (!mbar_try(smem_addr(&s_empty[r.at]), r.pass) && now_ns() - t0 < kWaitNs) {
+      while (!mbar_try_here(smem_addr(&s_empty[r.at]), r.pass) && now_ns() - t0 < kWaitNs) {
       }
     }
   };
@@ -213,9 +239,6 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
   };
   const int first_slice = groups * split / splits;
   const int n_slices = groups * (split + 1) / splits - first_slice;
-  // Rows of a tile in the pair's block r, and 64-row loads of them.
-  auto rows_of = [](const QuantTile& t, int r) { return min(128, t.rows - 128 * r); };
-  auto loads_of = [&](const QuantTile& t, int r) { return (max(0, rows_of(t, r)) + 63) / 64; };
 
   if (warp >= kEpiWarps) {
     fewer_registers<kQuantOtherRegisters>();
@@ -224,60 +247,56 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
         Ring ring;
         uint32_t issued = 0;
         bool ok = true;
-        const uint32_t full0 = cluster_addr(smem_addr(&s_full[0]), leader);
-        for (Walk walk(pair, pairs); walk.t < total && ok; walk.next()) {
+        for (Walk walk(worker, workers); walk.t < total && ok; walk.next()) {
           const QuantTile tile = tile_at(walk.t);
-          const int loads = loads_of(tile, rank);
-          const uint32_t bytes =
-              2 * kTileBBytes + (loads_of(tile, 0) + loads_of(tile, 1)) * kBoxBytes;
-          const int row = tile.lo + rank * 128;
-          const int f = kGatedForm ? tile.f0 + rank * width : tile.f0 + rank * 128;
+          const int loads = (tile.rows + 63) / 64;
+          const uint32_t bytes = kWeightBytes + loads * kBoxBytes;
           for (int s = 0; s < n_slices; ++s, ++issued) {
             const int st = ring.at;
-            if (withheld(issued) || !mbar_wait_as<kWaitHere>(smem_addr(&s_empty[st]), ring.pass ^ 1, gave_up)) {
+            const uint32_t full = smem_addr(&s_full[st]);
+            if (withheld(issued) ||
+                !mbar_wait_as<kWaitHere>(smem_addr(&s_empty[st]), ring.pass ^ 1, gave_up)) {
               ok = false;
               break;
             }
             *static_cast<volatile uint32_t*>(&s_issued) = issued + 1;
             ring.advance();
-            // Both blocks' loads report to the first block's barrier.
-            const uint32_t full = full0 + st * 8;
-            if (rank == 0) mbar_expect(smem_addr(&s_full[st]), bytes);
-            const uint32_t sa = smem_addr(stages + st * kStageBytes), sb = sa + kTileABytes;
+            mbar_expect(full, bytes);
+            const uint32_t sw = smem_addr(stages + st * kFp8StageBytes), sx = sw + kWeightBytes;
             const int k = (first_slice + s) * kGroupSlice;
-            tma_load_3d(sb, &map_weight, k, f, tile.e, full);
-            tma_load_3d(sb + kBoxBytes, &map_weight, k, f + 64, tile.e, full);
+            tma_load_3d_single(sw, &map_weight, k, tile.f0, tile.e, full);
+            tma_load_3d_single(sw + kWeightBytes / 2, &map_weight, k,
+                               tile.f0 + (kGatedForm ? width : 128), tile.e, full);
             for (int i = 0; i < loads; ++i)
-              tma_load_2d(sa + i * kBoxBytes, &map_rows, k, row + i * 64, full);
+              tma_load_2d_single(sx + i * kBoxBytes, &map_rows, k, tile.lo + i * 64, full);
           }
         }
         if (*gave_up != 0) drain(ring, issued);
       }
       __syncwarp();
     } else if (warp == kEpiWarps + 1) {
-      if (rank == 0 && elect_one()) {
+      if (elect_one()) {
         Ring ring;
         uint32_t issued = 0;
-        const uint16_t both = static_cast<uint16_t>(3u << leader);
-        const uint32_t idesc = instr_desc(false, false, false, 256, kMaxN);
+        const uint32_t idesc = instr_desc(false, false, false, kTileRows, kTileFeatures);
         bool ok = true;
-        for (Walk walk(pair, pairs); walk.t < total && ok; walk.next()) {
+        for (Walk walk(worker, workers); walk.t < total && ok; walk.next()) {
           for (int s = 0; s < n_slices; ++s) {
+            const uint32_t buf = issued & 1, acc = tmem + buf * kTileFeatures;
             const int st = ring.at;
-            const uint32_t buf = issued & 1;
             if (!mbar_wait_as<kWaitHere>(smem_addr(&s_full[st]), ring.pass, gave_up) ||
                 !mbar_wait_as<kWaitHere>(smem_addr(&s_free[buf]), (issued / 2 & 1) ^ 1, gave_up)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t pa = smem_addr(stages + st * kStageBytes), pb = pa + kTileABytes;
+            const uint32_t pw = smem_addr(stages + st * kFp8StageBytes), px = pw + kWeightBytes;
 #pragma unroll
             for (int i = 0; i < kGroupSlice / 32; ++i)
-              tc_mma_fp8(tmem + buf * kMaxN, smem_desc(pa + i * 32, 16, 1024),
-                         smem_desc(pb + i * 32, 16, 1024), idesc, i > 0);
-            tc_commit(smem_addr(&s_done[buf]), both);
-            tc_commit(smem_addr(&s_empty[st]), both);
+              tc_mma_fp8_single(acc, smem_desc(px + i * 32, 16, 1024),
+                                smem_desc(pw + i * 32, 16, 1024), idesc, i > 0);
+            tc_commit_single(smem_addr(&s_done[buf]));
+            tc_commit_single(smem_addr(&s_empty[st]));
             ++issued;
             ring.advance();
           }
@@ -291,60 +310,67 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
     more_registers<kQuantEpilogueRegisters>();
     const int quad = warp & 3, half = warp / 4;
     uint32_t done = 0;  // slices so far
-    const uint32_t free0 = cluster_addr(smem_addr(&s_free[0]), leader);
-    // The warp's columns: four blocks of 32, two of each block's features.
+    // The warp's columns: four blocks of 32, two of each 128 rows of the weight.
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 64;
     auto block_column = [](int j) { return (j >> 1) * 128 + (j & 1) * 32; };
-    // Pairs that share a tile have one tile at most: its sums may lie over the
-    // stages, which are through.  A lane's 128 values: 32 steps of 512 bytes.
+    // Blocks that share a tile have one tile at most: its sums may lie over the stages,
+    // which are through.  A lane's 128 values: 32 steps of 512 bytes.
     const uint32_t part = smem_addr(stages + warp * 32 * 512) + lane * 16;
-    const uint32_t other_part = splits > 1 ? cluster_addr(part, 2 + rank) : 0;
+    const uint32_t other_part = splits > 1 ? cluster_addr(part, 1) : 0;
     const bool wide = width % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+    const int blocks = (width + kGroupSlice - 1) / kGroupSlice, last = n_slices - 1;
+    // The row's scales and those of the weight's two blocks (gated: of gate and up), two
+    // slices ahead: behind the tiles' loads they take more than one.  (Lanes without a
+    // row take the last row's.)
+    const float *xs, *ws, *us;
+    float x[2], w[2], u[2];
+    auto first_scales = [&](const QuantTile& tile) {
+      const int64_t row = tile.lo + min(quad * 32 + lane, tile.rows - 1);
+      const int block = tile.f0 / kGroupSlice;
+      xs = a.scales + row * groups + first_slice;
+      ws = a.weight_scales + first_slice +
+           (static_cast<int64_t>(tile.e) * (kGatedForm ? 2 : 1) * blocks + block) * groups;
+      us = ws + static_cast<int64_t>(kGatedForm ? blocks : block + 1 < blocks) * groups;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = min(i, last);
+        x[i] = load_early(xs + at), w[i] = load_early(ws + at), u[i] = load_early(us + at);
+      }
+    };
     float d0[32], d1[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) d0[i] = d1[i] = 0.f;
-    for (Walk walk(pair, pairs); walk.t < total; walk.next()) {
-      const QuantTile tile = tile_at(walk.t);
-      const int rows = rows_of(tile, rank);
-      const bool any = quad * 32 < rows;
-      const int64_t row = tile.lo + rank * 128 + quad * 32 + lane;
+    Walk walk(worker, workers);
+    QuantTile next = {};
+    if (walk.t < total) {
+      next = tile_at(walk.t);
+      first_scales(next);
+    }
+    while (walk.t < total) {
+      const QuantTile tile = next;
+      walk.next();
+      const int64_t row = tile.lo + quad * 32 + lane;
       float sums[4][32];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < 32; ++i) sums[j][i] = 0.f;
       bool ok = true;
+      const bool any = quad * 32 < tile.rows;
       if (!any) {  // no rows: only makes room
         for (int s = 0; ok && s < n_slices; ++s, ++done) {
           ok = warp_wait_as<kWaitHere>(smem_addr(&s_done[done & 1]), done / 2 & 1, gave_up);
-          if (ok && lane == 0) mbar_arrive_relaxed_cluster(free0 + (done & 1) * 8);
+          if (ok && lane == 0) mbar_arrive_relaxed(smem_addr(&s_free[done & 1]));
         }
       } else {
-        // The row's scales and those of the weight's two blocks (gated: of gate and up),
-        // two slices ahead: behind the tiles' loads they take more than one.  (Lanes
-        // without a row take the last row's.)
-        const int blocks = (width + kGroupSlice - 1) / kGroupSlice, block = tile.f0 / kGroupSlice;
-        const int last = n_slices - 1;
-        const int64_t scaled = min(row, static_cast<int64_t>(tile.lo) + rank * 128 + rows - 1);
-        const float* xs = a.scales + scaled * groups + first_slice;
-        const float* ws =
-            a.weight_scales + first_slice +
-            (static_cast<int64_t>(tile.e) * (kGatedForm ? 2 : 1) * blocks + block) * groups;
-        const float* us = ws + static_cast<int64_t>(kGatedForm ? blocks : block + 1 < blocks) * groups;
-        float x[2], w[2], u[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int at = min(i, last);
-          x[i] = load_early(xs + at), w[i] = load_early(ws + at), u[i] = load_early(us + at);
-        }
         // Two blocks are on their way from tensor memory while two are added.
         // (Behind the last slice what is loaded is not used.)
         ok = warp_wait_as<kWaitHere>(smem_addr(&s_done[done & 1]), done / 2 & 1, gave_up);
         tc_fence_after();
-        tmem_load_row32(lanes + (done & 1) * kMaxN, d0);
-        tmem_load_row32(lanes + (done & 1) * kMaxN + 32, d1);
+        tmem_load_row32(lanes + (done & 1) * kTileFeatures, d0);
+        tmem_load_row32(lanes + (done & 1) * kTileFeatures + 32, d1);
         for (int s = 0; ok && s < n_slices; ++s) {
-          const uint32_t acc = lanes + (done & 1) * kMaxN;
+          const uint32_t acc = lanes + (done & 1) * kTileFeatures;
           const float by_w = x[0] * w[0], by_u = x[0] * u[0];
           x[0] = x[1], w[0] = w[1], u[0] = u[1];
           const int ahead = min(s + 2, last);
@@ -361,11 +387,10 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
           tmem_wait_load(d1);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_relaxed_cluster(free0 + (done & 1) * 8);
+          if (lane == 0) mbar_arrive_relaxed(smem_addr(&s_free[done & 1]));
           ++done;
-          const bool more = s + 1 < n_slices;
           const uint32_t bar = smem_addr(&s_done[done & 1]), parity = done / 2 & 1;
-          const bool over = !more || mbar_test_here(bar, parity);
+          const bool over = s == last || mbar_test_here(bar, parity);
 #pragma unroll
           for (int i = 0; i < 32; ++i) sums[2][i] = fmaf(d0[i], by_u, sums[2][i]);
           if (!__all_sync(kFullMask, over) && !warp_wait_as<kWaitHere>(bar, parity, gave_up)) {
@@ -373,15 +398,19 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
             break;
           }
           tc_fence_after();
-          tmem_load_row32(lanes + (done & 1) * kMaxN, d0);
+          tmem_load_row32(lanes + (done & 1) * kTileFeatures, d0);
 #pragma unroll
           for (int i = 0; i < 32; ++i) sums[3][i] = fmaf(d1[i], by_u, sums[3][i]);
-          tmem_load_row32(lanes + (done & 1) * kMaxN + 32, d1);
+          tmem_load_row32(lanes + (done & 1) * kTileFeatures + 32, d1);
         }
         tmem_wait_load(d0);
         tmem_wait_load(d1);
       }
       if (!ok) break;
+      if (walk.t < total) {
+        next = tile_at(walk.t);
+        first_scales(next);
+      }
       if (splits > 1) {
         if (split > 0) {
           if (any) {
@@ -394,11 +423,11 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
                                         __float_as_uint(sums[j / 8][j % 8 * 4 + 3])));
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&s_parts), rank));
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&s_parts), 0));
           break;
         }
         if (!warp_wait_as<kWaitCluster>(smem_addr(&s_parts), 0, gave_up,
-                              cluster_addr(smem_addr(&s_issued), 2 + rank)))
+                              cluster_addr(smem_addr(&s_issued), 1)))
           break;
         if (any) {
 #pragma unroll
@@ -409,7 +438,7 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
           }
         }
       }
-      if (quad * 32 + lane >= rows) continue;
+      if (quad * 32 + lane >= tile.rows) continue;
       T* out = static_cast<T*>(a.out) + row * width;
       if (kGatedForm) {
 #pragma unroll
@@ -453,11 +482,11 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // the products, loads, arrivals and reads of the cluster are over
+  cluster_sync();  // the arrivals and reads of the cluster are over
   tc_fence_after();
   if (threadIdx.x == 0 && *gave_up != 0 && a.status != nullptr)
     atomicOr(a.status, MOE_FLAG_BARRIER_TIMEOUT);
-  if (warp == kEpiWarps + 1) tmem_free(tmem, 512);
+  if (warp == kEpiWarps + 1) tmem_free_single(tmem, 512);
 }
 
 }  // namespace experts
