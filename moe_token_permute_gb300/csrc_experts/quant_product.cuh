@@ -18,7 +18,8 @@
 //   warps 0-7    tensor memory -> registers, scaled; then the epilogue
 //   warp 8       TMA producer: 128-deep slices into a ring of 4 x 48 KB
 //   warp 9       tcgen05.mma issue, tensor memory allocation
-//   warps 10-11  fill up the warpgroup that gives its registers to warps 0-7
+//   warps 10-11  the scales, four slices at a time, into a ring of 12 slices: behind the
+//                tiles' loads a scale takes longer than a slice
 #pragma once
 
 #include <type_traits>
@@ -35,6 +36,10 @@ constexpr int kRowsBytes = kTileRows * kGroupSlice, kWeightBytes = kTileFeatures
 constexpr int kFp8StageBytes = kRowsBytes + kWeightBytes;
 constexpr int kFp8Stages = 4;
 constexpr int kBuffers = 2;        // of tensor memory, a slice's products each
+constexpr int kScaleChunk = 4;     // slices whose scales are loaded at once
+constexpr int kScaleChunks = 3;    // of the ring
+constexpr int kScaleSlotBytes = kTileRows * 8;  // two numbers a row
+constexpr int kScaleBytes = kScaleChunks * kScaleChunk * kScaleSlotBytes;
 constexpr int kQuantProductThreads = 384;
 constexpr int kQuantEpilogueRegisters = 224, kQuantOtherRegisters = 56;
 static_assert(2 * kQuantEpilogueRegisters + kQuantOtherRegisters <= 65536 / 384 / 8 * 8 * 3,
@@ -56,12 +61,13 @@ struct QuantArgs {
   unsigned* status;
 };
 
-// Dynamic shared memory: stages (1024-byte aligned), then each expert's rows and its
-// first tile.
+// Dynamic shared memory: stages (1024-byte aligned), scales, then each expert's rows and
+// its first tile.
 inline size_t quant_product_smem(int E) {
-  return 1024 + kFp8Stages * kFp8StageBytes + static_cast<size_t>(E) * 12 + 4;
+  return 1024 + kFp8Stages * kFp8StageBytes + kScaleBytes + static_cast<size_t>(E) * 12 + 4;
 }
-static_assert(1024 + kFp8Stages * kFp8StageBytes + MOE_MAX_LOCAL_EXPERTS * 12 + 4 + 1024 <=
+static_assert(1024 + kFp8Stages * kFp8StageBytes + kScaleBytes + MOE_MAX_LOCAL_EXPERTS * 12 + 4 +
+                      1024 <=
                   227 * 1024,
               "shared memory of one block");
 
@@ -115,11 +121,13 @@ __device__ __forceinline__ void store_16(T* row, const float* z, int64_t c, int6
   }
 }
 
-// A load that stays where it is written, ahead of its use.
-__device__ __forceinline__ float load_early(const float* p) {
-  float v;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+__device__ __forceinline__ float2 shared_load_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
+}
+__device__ __forceinline__ void shared_store_f2(uint32_t addr, float x, float y) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
 
 // Each expert's first tile, of 128 rows by f_blocks blocks of features, and their number
@@ -159,14 +167,16 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
   extern __shared__ uint8_t smem_raw[];
   // s_parts is used in the cluster's first block only.
   __shared__ __align__(8) uint64_t s_full[kFp8Stages], s_empty[kFp8Stages], s_done[kBuffers],
-      s_free[kBuffers], s_parts;
+      s_free[kBuffers], s_scaled[kScaleChunks], s_used[kScaleChunks], s_parts;
   __shared__ uint32_t s_tmem;
   __shared__ int s_gave_up;
   __shared__ uint32_t s_issued;  // slices that this block's producer has issued
 
   uint8_t* stages = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Segment* segments = reinterpret_cast<Segment*>(stages + kFp8Stages * kFp8StageBytes);
+  const uint32_t scale_ring = smem_addr(stages + kFp8Stages * kFp8StageBytes);
+  Segment* segments =
+      reinterpret_cast<Segment*>(stages + kFp8Stages * kFp8StageBytes + kScaleBytes);
   int* first = reinterpret_cast<int*>(segments + a.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = static_cast<int>(cluster_rank()), splits = static_cast<int>(cluster_size());
@@ -180,6 +190,10 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
     for (int i = 0; i < kBuffers; ++i) {
       mbar_init(smem_addr(&s_done[i]), 1);
       mbar_init(smem_addr(&s_free[i]), kEpiWarps);
+    }
+    for (int i = 0; i < kScaleChunks; ++i) {
+      mbar_init(smem_addr(&s_scaled[i]), 2);
+      mbar_init(smem_addr(&s_used[i]), kEpiWarps);
     }
     mbar_init(smem_addr(&s_parts), kEpiWarps);
     mbar_init_fence();
@@ -305,11 +319,73 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
         if (*gave_up != 0) drain(ring, issued);
       }
       __syncwarp();
+    } else {
+      // A row's scale times those of the weight's two blocks (gated: of gate and up).
+      // Lane l has rows 64 i + l and 64 i + 32 + l of the tile; kScaleChunk slices of
+      // them are in flight while those before are written.
+      constexpr int kMine = kTileRows / 64;
+      const int r0 = (warp - kEpiWarps - 2) * (kTileRows / 2) + lane;
+      const int blocks = (width + kGroupSlice - 1) / kGroupSlice;
+      const bool whole = groups % kScaleChunk == 0 && first_slice % kScaleChunk == 0 &&
+                         (reinterpret_cast<uintptr_t>(a.scales) & 15) == 0;
+      uint32_t step = 0;  // chunks so far
+      bool ok = true;
+      for (Walk walk(worker, workers); walk.t < total && ok; walk.next()) {
+        const QuantTile tile = tile_at(walk.t);
+        const int block = tile.f0 / kGroupSlice;
+        // Lanes 0-3 load the chunk's four of the first block, 4-7 of the second.
+        const float* ws = a.weight_scales + first_slice + lane % kScaleChunk +
+                          (static_cast<int64_t>(tile.e) * (kGatedForm ? 2 : 1) * blocks + block) *
+                              groups;
+        if (lane / kScaleChunk % 2 == 1)
+          ws += static_cast<int64_t>(kGatedForm ? blocks : block + 1 < blocks) * groups;
+        const float* xs = a.scales + (static_cast<int64_t>(tile.lo) + r0) * groups + first_slice;
+        float x[kMine][kScaleChunk], w;
+        auto fetch = [&](int s) {
+          w = s + lane % kScaleChunk < n_slices ? __ldg(ws + s) : 0.f;
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) {
+            const float* at = xs + static_cast<int64_t>(32 * i) * groups + s;
+            const bool in = r0 + 32 * i < tile.rows;
+            if (whole && s + kScaleChunk <= n_slices) {
+              const float4 v = in ? __ldg(reinterpret_cast<const float4*>(at))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+              x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+            } else {
+#pragma unroll
+              for (int k = 0; k < kScaleChunk; ++k)
+                x[i][k] = in && s + k < n_slices ? __ldg(at + k) : 0.f;
+            }
+          }
+        };
+        fetch(0);
+        for (int s = 0; s < n_slices; s += kScaleChunk, ++step) {
+          const uint32_t chunk = step % kScaleChunks;
+          if (!warp_wait_as<kWaitAwake>(smem_addr(&s_used[chunk]), (step / kScaleChunks & 1) ^ 1,
+                                        gave_up)) {
+            ok = false;
+            break;
+          }
+          const uint32_t to = scale_ring + chunk * kScaleChunk * kScaleSlotBytes + r0 * 8;
+#pragma unroll
+          for (int k = 0; k < kScaleChunk; ++k) {
+            const float by0 = __shfl_sync(kFullMask, w, k);
+            const float by1 = __shfl_sync(kFullMask, w, kScaleChunk + k);
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+              shared_store_f2(to + k * kScaleSlotBytes + i * 256, x[i][k] * by0, x[i][k] * by1);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&s_scaled[chunk]));
+          if (s + kScaleChunk < n_slices) fetch(s + kScaleChunk);
+        }
+      }
     }
   } else {
     more_registers<kQuantEpilogueRegisters>();
     const int quad = warp & 3, half = warp / 4;
     uint32_t done = 0;  // slices so far
+    uint32_t step = 0, scale_pass = 0;  // the chunk of scales, parity of the pass through them
     // The warp's columns: four blocks of 32, two of each 128 rows of the weight.
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 64;
     auto block_column = [](int j) { return (j >> 1) * 128 + (j & 1) * 32; };
@@ -318,37 +394,11 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
     const uint32_t part = smem_addr(stages + warp * 32 * 512) + lane * 16;
     const uint32_t other_part = splits > 1 ? cluster_addr(part, 1) : 0;
     const bool wide = width % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
-    const int blocks = (width + kGroupSlice - 1) / kGroupSlice, last = n_slices - 1;
-    // The row's scales and those of the weight's two blocks (gated: of gate and up), two
-    // slices ahead: behind the tiles' loads they take more than one.  (Lanes without a
-    // row take the last row's.)
-    const float *xs, *ws, *us;
-    float x[2], w[2], u[2];
-    auto first_scales = [&](const QuantTile& tile) {
-      const int64_t row = tile.lo + min(quad * 32 + lane, tile.rows - 1);
-      const int block = tile.f0 / kGroupSlice;
-      xs = a.scales + row * groups + first_slice;
-      ws = a.weight_scales + first_slice +
-           (static_cast<int64_t>(tile.e) * (kGatedForm ? 2 : 1) * blocks + block) * groups;
-      us = ws + static_cast<int64_t>(kGatedForm ? blocks : block + 1 < blocks) * groups;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int at = min(i, last);
-        x[i] = load_early(xs + at), w[i] = load_early(ws + at), u[i] = load_early(us + at);
-      }
-    };
     float d0[32], d1[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) d0[i] = d1[i] = 0.f;
-    Walk walk(worker, workers);
-    QuantTile next = {};
-    if (walk.t < total) {
-      next = tile_at(walk.t);
-      first_scales(next);
-    }
-    while (walk.t < total) {
-      const QuantTile tile = next;
-      walk.next();
+    for (Walk walk(worker, workers); walk.t < total; walk.next()) {
+      const QuantTile tile = tile_at(walk.t);
       const int64_t row = tile.lo + quad * 32 + lane;
       float sums[4][32];
 #pragma unroll
@@ -357,10 +407,17 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
         for (int i = 0; i < 32; ++i) sums[j][i] = 0.f;
       bool ok = true;
       const bool any = quad * 32 < tile.rows;
+      // Frees the scales of slice s, which is through, if its chunk is.
+      auto scales_used = [&](int s) {
+        if (s % kScaleChunk != kScaleChunk - 1 && s != n_slices - 1) return;
+        if (lane == 0) mbar_arrive_relaxed(smem_addr(&s_used[step]));
+        if (++step == kScaleChunks) step = 0, scale_pass ^= 1;
+      };
       if (!any) {  // no rows: only makes room
         for (int s = 0; ok && s < n_slices; ++s, ++done) {
           ok = warp_wait_as<kWaitHere>(smem_addr(&s_done[done & 1]), done / 2 & 1, gave_up);
           if (ok && lane == 0) mbar_arrive_relaxed(smem_addr(&s_free[done & 1]));
+          scales_used(s);
         }
       } else {
         // Two blocks are on their way from tensor memory while two are added.
@@ -371,17 +428,21 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
         tmem_load_row32(lanes + (done & 1) * kTileFeatures + 32, d1);
         for (int s = 0; ok && s < n_slices; ++s) {
           const uint32_t acc = lanes + (done & 1) * kTileFeatures;
-          const float by_w = x[0] * w[0], by_u = x[0] * u[0];
-          x[0] = x[1], w[0] = w[1], u[0] = u[1];
-          const int ahead = min(s + 2, last);
-          x[1] = load_early(xs + ahead), w[1] = load_early(ws + ahead), u[1] = load_early(us + ahead);
+          if (s % kScaleChunk == 0 &&
+              !warp_wait_as<kWaitAwake>(smem_addr(&s_scaled[step]), scale_pass, gave_up)) {
+            ok = false;
+            break;
+          }
+          const float2 by = shared_load_f2(scale_ring +
+                                           (step * kScaleChunk + s % kScaleChunk) * kScaleSlotBytes +
+                                           (quad * 32 + lane) * 8);
           tmem_wait_load(d0);
           tmem_wait_load(d1);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) sums[0][i] = fmaf(d0[i], by_w, sums[0][i]);
+          for (int i = 0; i < 32; ++i) sums[0][i] = fmaf(d0[i], by.x, sums[0][i]);
           tmem_load_row32(acc + block_column(2), d0);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) sums[1][i] = fmaf(d1[i], by_w, sums[1][i]);
+          for (int i = 0; i < 32; ++i) sums[1][i] = fmaf(d1[i], by.x, sums[1][i]);
           tmem_load_row32(acc + block_column(3), d1);
           tmem_wait_load(d0);
           tmem_wait_load(d1);
@@ -390,9 +451,9 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
           if (lane == 0) mbar_arrive_relaxed(smem_addr(&s_free[done & 1]));
           ++done;
           const uint32_t bar = smem_addr(&s_done[done & 1]), parity = done / 2 & 1;
-          const bool over = s == last || mbar_test_here(bar, parity);
+          const bool over = s == n_slices - 1 || mbar_test_here(bar, parity);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) sums[2][i] = fmaf(d0[i], by_u, sums[2][i]);
+          for (int i = 0; i < 32; ++i) sums[2][i] = fmaf(d0[i], by.y, sums[2][i]);
           if (!__all_sync(kFullMask, over) && !warp_wait_as<kWaitHere>(bar, parity, gave_up)) {
             ok = false;
             break;
@@ -400,17 +461,14 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
           tc_fence_after();
           tmem_load_row32(lanes + (done & 1) * kTileFeatures, d0);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) sums[3][i] = fmaf(d1[i], by_u, sums[3][i]);
+          for (int i = 0; i < 32; ++i) sums[3][i] = fmaf(d1[i], by.y, sums[3][i]);
           tmem_load_row32(lanes + (done & 1) * kTileFeatures + 32, d1);
+          scales_used(s);
         }
         tmem_wait_load(d0);
         tmem_wait_load(d1);
       }
       if (!ok) break;
-      if (walk.t < total) {
-        next = tile_at(walk.t);
-        first_scales(next);
-      }
       if (splits > 1) {
         if (split > 0) {
           if (any) {
