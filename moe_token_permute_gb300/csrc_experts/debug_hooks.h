@@ -4,9 +4,16 @@
 
 #include "moe_experts.h"
 
+// The same in the source of the 8-bit operators, whose kernels have variables of their own.
+namespace moe {
+namespace experts {
+bool set_quant_wait(int slices, unsigned long long wait_ns);
+}  // namespace experts
+}  // namespace moe
+
 extern "C" {
 
-// From the next launch on, a wait inside the expert products gives up after
+// From the next launch on, a wait inside the expert products (of 16 and 8 bits) gives up after
 // `wait_ns` nanoseconds without progress, and, with slices > 0, each block's
 // producer stops after that many slices of its contractions, so that the waits for
 // the next one run out: the kernel raises MOE_FLAG_BARRIER_TIMEOUT and returns, its

@@ -159,7 +159,7 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
           for (int s = 0; s < n_slices; ++s, ++issued) {
             const uint32_t st = issued % kRawStages;
             if (withheld(issued) ||
-                !mbar_wait_as<kWaitAwake>(smem_addr(&s_read[st]), (issued / kRawStages & 1) ^ 1, gave_up)) {
+                !mbar_wait_as<kWaitHere>(smem_addr(&s_read[st]), (issued / kRawStages & 1) ^ 1, gave_up)) {
               ok = false;
               break;
             }
@@ -193,10 +193,10 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
           const Tile tile = tile_at(walk.t);
           const uint32_t idesc = instr_desc(false, false, false, 256, mma_n(tile.cols));
           const uint32_t buf = done & 1, acc = tmem + buf * kMaxN;
-          if (!mbar_wait_as<kWaitAwake>(smem_addr(&s_free[buf]), (done / 2 & 1) ^ 1, gave_up, progress)) break;
+          if (!mbar_wait_as<kWaitHere>(smem_addr(&s_free[buf]), (done / 2 & 1) ^ 1, gave_up, progress)) break;
           for (int s = 0; s < 2 * n_slices; ++s, ++issued) {
             const uint32_t st = issued % kWideStages;
-            if (!mbar_wait_as<kWaitAwake>(smem_addr(&s_wide[st]), issued / kWideStages & 1, gave_up)) {
+            if (!mbar_wait_as<kWaitHere>(smem_addr(&s_wide[st]), issued / kWideStages & 1, gave_up)) {
               ok = false;
               break;
             }

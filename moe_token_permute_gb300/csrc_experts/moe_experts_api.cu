@@ -375,7 +375,8 @@ int moe_unpermute_backward(const void* d_out, const void* permuted_rows, int64_t
 int moe_debug_set_expert_wait(int slices, unsigned long long wait_ns) {
   if (slices < 0 || wait_ns == 0) return MOE_ERR_INVALID_ARG;
   if (cudaMemcpyToSymbol(g_debug_slices, &slices, sizeof(slices)) != cudaSuccess ||
-      cudaMemcpyToSymbol(g_debug_wait_ns, &wait_ns, sizeof(wait_ns)) != cudaSuccess) {
+      cudaMemcpyToSymbol(g_debug_wait_ns, &wait_ns, sizeof(wait_ns)) != cudaSuccess ||
+      !set_quant_wait(slices, wait_ns)) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
   }

@@ -3,6 +3,9 @@
 // Argument checks happen before any device is touched; nothing allocates or
 // synchronises.  Each entry point is one launch.
 #include "moe_quant.h"
+#ifdef MOE_DEBUG_HOOKS
+#include "debug_hooks.h"
+#endif
 
 #include <algorithm>
 #include <type_traits>
@@ -141,6 +144,14 @@ int product(const QuantArgs& a, moe_dtype_t code_dtype, moe_dtype_t out_dtype,
 }
 
 }  // namespace
+
+#ifdef MOE_DEBUG_HOOKS
+bool set_quant_wait(int slices, unsigned long long wait_ns) {
+  return cudaMemcpyToSymbol(g_debug_slices, &slices, sizeof(slices)) == cudaSuccess &&
+         cudaMemcpyToSymbol(g_debug_wait_ns, &wait_ns, sizeof(wait_ns)) == cudaSuccess;
+}
+#endif
+
 }  // namespace experts
 }  // namespace moe
 

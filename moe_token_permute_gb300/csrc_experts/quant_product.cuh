@@ -394,9 +394,6 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
     const uint32_t part = smem_addr(stages + warp * 32 * 512) + lane * 16;
     const uint32_t other_part = splits > 1 ? cluster_addr(part, 1) : 0;
     const bool wide = width % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
-    float d0[32], d1[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) d0[i] = d1[i] = 0.f;
     for (Walk walk(worker, workers); walk.t < total; walk.next()) {
       const QuantTile tile = tile_at(walk.t);
       const int64_t row = tile.lo + quad * 32 + lane;
@@ -422,6 +419,9 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
       } else {
         // Two blocks are on their way from tensor memory while two are added.
         // (Behind the last slice what is loaded is not used.)
+        float d0[32], d1[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) d0[i] = d1[i] = 0.f;
         ok = warp_wait_as<kWaitHere>(smem_addr(&s_done[done & 1]), done / 2 & 1, gave_up);
         tc_fence_after();
         tmem_load_row32(lanes + (done & 1) * kTileFeatures, d0);
