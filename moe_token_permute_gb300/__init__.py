@@ -373,17 +373,27 @@ def moe_expert_linear_backward(d_out, rows, weight, expert_first_token_offset, *
         _ptr(d_weight), _ptr(d_bias), _ptr(workspace), _stream(stream)))
 
 
-def _here(*tensors):
-    """The library works on the current device: tensors of another are refused."""
+def _pointers(*tensors):
+    """What _ptr gives, and that the tensors lie on the current device, which is
+    where the library works."""
     device = None
+    out = []
     for t in tensors:
-        if t is None or not t.is_cuda:  # (_ptr refuses the latter)
+        if t is None:
+            out.append(None)
             continue
+        at = t.get_device()
+        if at < 0:
+            raise ValueError("expected a CUDA tensor")
         if device is None:
             device = torch.cuda.current_device() if _raw_device is None else _raw_device()
-        if t.get_device() != device:
+        if at != device:
             raise ValueError(f"expected tensors on the current device (cuda:{device}); "
                              f"one is on {t.device}")
+        if not t.is_contiguous():
+            raise ValueError("expected a contiguous tensor (the library writes in place)")
+        out.append(t.data_ptr())
+    return out
 
 
 def _code_groups(codes_dtype, cols, what):
@@ -416,10 +426,11 @@ def moe_quant_rows(rows, codes, scales, *, expert_first_token_offset=None, works
             raise ValueError("expert_first_token_offset must be int64")
         _need(expert_first_token_offset, 2, "expert_first_token_offset")
         experts = expert_first_token_offset.numel() - 1
-    _here(rows, codes, scales, expert_first_token_offset, workspace)
+    rows_, codes_, scales_, offset_, workspace_ = _pointers(
+        rows, codes, scales, expert_first_token_offset, workspace)
     _b.check("moe_quant_rows", _b.lib().moe_quant_rows(
-        _ptr(rows), _DTYPES[rows.dtype], _ptr(expert_first_token_offset), R, H, experts,
-        _DTYPES[codes.dtype], _ptr(codes), _ptr(scales), _ptr(workspace), _stream(stream)))
+        rows_, _DTYPES[rows.dtype], offset_, R, H, experts, _DTYPES[codes.dtype], codes_, scales_,
+        workspace_, _stream(stream)))
 
 
 def _quant_operands(codes, scales, weight, weight_scales, offset, out, parts):
@@ -466,12 +477,12 @@ def moe_expert_gated_quant(permuted_codes, permuted_scales, weight, weight_scale
                                  expert_first_token_offset, out, 2)
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
-    _here(permuted_codes, permuted_scales, weight, weight_scales, expert_first_token_offset, out,
-          workspace)
+    x, xs, w, ws, offset, out_, workspace_ = _pointers(
+        permuted_codes, permuted_scales, weight, weight_scales, expert_first_token_offset, out,
+        workspace)
     _b.check("moe_expert_gated_quant", _b.lib().moe_expert_gated_quant(
-        _ptr(permuted_codes), _ptr(permuted_scales), _ptr(weight), _ptr(weight_scales),
-        _DTYPES[weight.dtype], _DTYPES[out.dtype], _ptr(expert_first_token_offset), R, H, N // 2,
-        E, _ACTIVATIONS[activation], _ptr(out), _ptr(workspace), _stream(stream)))
+        x, xs, w, ws, _DTYPES[weight.dtype], _DTYPES[out.dtype], offset, R, H, N // 2, E,
+        _ACTIVATIONS[activation], out_, workspace_, _stream(stream)))
 
 
 def moe_expert_linear_quant(codes, scales, weight, weight_scales, expert_first_token_offset, out,
@@ -493,12 +504,12 @@ def moe_expert_linear_quant(codes, scales, weight, weight_scales, expert_first_t
         raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
     _matrix(bias, E, N, out.dtype, "bias")
     _matrix(residual, R, N, out.dtype, "residual")
-    _here(codes, scales, weight, weight_scales, expert_first_token_offset, out, bias, residual,
-          workspace)
+    x, xs, w, ws, offset, out_, bias_, residual_, workspace_ = _pointers(
+        codes, scales, weight, weight_scales, expert_first_token_offset, out, bias, residual,
+        workspace)
     _b.check("moe_expert_linear_quant", _b.lib().moe_expert_linear_quant(
-        _ptr(codes), _ptr(scales), _ptr(weight), _ptr(weight_scales), _DTYPES[weight.dtype],
-        _DTYPES[out.dtype], _ptr(expert_first_token_offset), R, K, N, E, _ptr(bias),
-        _ACTIVATIONS[activation], _ptr(residual), _ptr(out), _ptr(workspace), _stream(stream)))
+        x, xs, w, ws, _DTYPES[weight.dtype], _DTYPES[out.dtype], offset, R, K, N, E, bias_,
+        _ACTIVATIONS[activation], residual_, out_, workspace_, _stream(stream)))
 
 
 def moe_unpermute_backward(d_out, permuted_rows, topk_weights, inv_permuted_idx, d_rows,

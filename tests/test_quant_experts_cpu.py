@@ -162,11 +162,11 @@ def test_binding_refuses_products(code):
 
 def test_tensors_of_another_device_are_refused(monkeypatch):
     class Elsewhere:
-        is_cuda, device = True, "cuda:1"
+        device = "cuda:1"
 
         def get_device(self):
             return 1
 
     monkeypatch.setattr(mp, "_raw_device", lambda: 0)
     with pytest.raises(ValueError, match="current device"):
-        mp._here(None, Elsewhere())
+        mp._pointers(None, Elsewhere())
