@@ -140,11 +140,13 @@ __device__ __forceinline__ void place_in_panels(int local, int m_blocks, int n_b
 
 // Run by one warp: in how many blocks of each size the experts' rows are cut; the
 // choice of the most columns of a tile, returned; and each expert's first tile,
-// first[E] being the number of tiles.  With `widest` tiles have kMaxN columns.
+// first[E] being the number of tiles.  Tiles have cap_of(kFirst) columns at most, with
+// `widest` always.
+template <int kFirst = 0>
 __device__ __forceinline__ int scan_tiles(int E, const Segment* segments, int* first, bool widest,
                                           int m_blocks, int slices, int pairs) {
   const int lane = threadIdx.x & 31;
-  int cap = kMaxN;
+  int cap = cap_of(kFirst);
   if (!widest) {
     int blocks[kCaps] = {}, all = 0;
     for (int e = lane; e < E; e += 32) {
@@ -158,11 +160,12 @@ __device__ __forceinline__ int scan_tiles(int E, const Segment* segments, int* f
 #pragma unroll
     for (int i = 0; i < kCaps; ++i) {
       const int n = __reduce_add_sync(kFullMask, blocks[i]);
-      if (i == 0) most = n;
+      if (i == kFirst) most = n;
       if (lane == i) mine = n;
     }
     float cost = INFINITY;
-    if (lane == 0 || (lane < kCaps && most < (6 * pairs + m_blocks - 1) / m_blocks))
+    if (lane == kFirst ||
+        (lane > kFirst && lane < kCaps && most < (6 * pairs + m_blocks - 1) / m_blocks))
       cost = cap_cost(mine, all, m_blocks, slices, pairs);
     float best = cost;
 #pragma unroll

@@ -6,11 +6,17 @@
 // code is a whole number of 8 bits, which fp16 holds exactly, as it does the products
 // in fp32 (sums are rounded where they pass 2^24).  The tiles and the epilogue are
 // those of expert_product.cuh; between the copies and the products stand eight warps
-// that read 128-byte slices of codes and write them as two slices of fp16, both in the
-// 128-byte swizzle, a lane having a row so that neither access meets in a bank.
+// that read 128-byte slices of codes.  The weights' go to tensor memory as fp16, the
+// rows' to shared memory, whose bandwidth is what bounds the kernel: with both in shared
+// memory a 128-deep slice of 256 columns moves 192 KB through it, 2000 cycles for 1024 of
+// products.  Tensor memory then has two accumulators of 192 columns and four stages of 32.
+// On GB300, weights in shared / in tensor memory, us: one expert, 8191 rows, 4096 -> 4096
+// 235 / 226 (1.2 PFLOP/s); 8 experts, 8192 rows, 14336 -> 4096 792 / 745 (1.3); 128 experts,
+// 512 rows, gated, 2048 -> 2 x 768 131 / 88; 256 experts, 32768 rows, 2048 -> 7168
+// 1852 / 1361.  Twice the converting warps: 226, 89 and 1338, with registers spilled.
 //   warps 0-7    epilogue: tensor memory -> registers, scaled -> shared -> rows
 //   warps 8-15   codes -> fp16
-//   warp 16      TMA producer: 128 codes deep, a ring of 2 x 32 KB
+//   warp 16      TMA producer: 128 codes deep, a ring of 4 x 32 KB
 //   warp 17      tcgen05.mma issue (first block), tensor memory allocation
 //   warps 18-19  fill up a warpgroup (setmaxnreg)
 #pragma once
@@ -20,11 +26,15 @@
 namespace moe {
 namespace experts {
 
-constexpr int kRawStages = 2;
+constexpr int kRawStages = 4;
 constexpr int kRawSlice = 128;     // codes of a raw stage
 constexpr int kWideStages = 4;     // of fp16, 64 deep
+constexpr int kInt8CapIndex = 4;   // cap_of(4) = 192 columns of an accumulator
+constexpr int kInt8Columns = kMaxN - 16 * kInt8CapIndex;
+constexpr int kWideColumns = kSlice / 2;  // of tensor memory
+static_assert(2 * kInt8Columns + kWideStages * kWideColumns == 512, "tensor memory");
 constexpr int kInt8Threads = 640;
-constexpr int kInt8EpilogueRegisters = 144, kInt8ConvertRegisters = 72, kInt8OtherRegisters = 48;
+constexpr int kInt8EpilogueRegisters = 136, kInt8ConvertRegisters = 80, kInt8OtherRegisters = 48;
 static_assert(2 * kInt8EpilogueRegisters + 2 * kInt8ConvertRegisters + kInt8OtherRegisters <=
                   65536 / 640 / 8 * 8 * 5,
               "registers at launch: 96 a thread");
@@ -32,10 +42,10 @@ static_assert(2 * kInt8EpilogueRegisters + 2 * kInt8ConvertRegisters + kInt8Othe
 // Dynamic shared memory: raw and fp16 stages (1024-byte aligned), staging, then each
 // expert's rows and its first tile.
 inline size_t int8_product_smem(int E) {
-  return 1024 + (kRawStages + kWideStages) * kStageBytes + kStagingBytes +
+  return 1024 + kRawStages * kStageBytes + kWideStages * kTileBBytes + kStagingBytes +
          static_cast<size_t>(E) * 12 + 4;
 }
-static_assert(1024 + (kRawStages + kWideStages) * kStageBytes + kStagingBytes +
+static_assert(1024 + kRawStages * kStageBytes + kWideStages * kTileBBytes + kStagingBytes +
                       MOE_MAX_LOCAL_EXPERTS * 12 + 4 + 1024 <= 227 * 1024,
               "shared memory of one block");
 
@@ -69,7 +79,7 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
   uint8_t* raw = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* stages = raw + kRawStages * kStageBytes;
-  uint8_t* staging = stages + kWideStages * kStageBytes;
+  uint8_t* staging = stages + kWideStages * kTileBBytes;
   Segment* segments = reinterpret_cast<Segment*>(staging + kStagingBytes);
   int* first = reinterpret_cast<int*>(segments + a.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -87,7 +97,7 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
       mbar_init(smem_addr(&s_read[i]), kEpiWarps);
     }
     for (int i = 0; i < kWideStages; ++i) {
-      mbar_init(smem_addr(&s_wide[i]), 2 * kEpiWarps);
+      mbar_init(smem_addr(&s_wide[i]), kEpiWarps);  // half the warps of two blocks
       mbar_init(smem_addr(&s_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -119,7 +129,8 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
   __syncthreads();
   if (warp == 0) {
     // (a slice here is two of expert_product.cuh's)
-    const int cap = scan_tiles(a.E, segments, first, splits > 1, m_blocks, 2 * all_slices, pairs);
+    const int cap = scan_tiles<kInt8CapIndex>(a.E, segments, first, splits > 1, m_blocks,
+                                              2 * all_slices, pairs);
     if (lane == 0) s_cap = cap;
   }
   tc_fence_before();
@@ -192,7 +203,7 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
         for (Walk walk(pair, pairs); walk.t < total && ok; walk.next(), ++done) {
           const Tile tile = tile_at(walk.t);
           const uint32_t idesc = instr_desc(false, false, false, 256, mma_n(tile.cols));
-          const uint32_t buf = done & 1, acc = tmem + buf * kMaxN;
+          const uint32_t buf = done & 1, acc = tmem + buf * kInt8Columns;
           if (!mbar_wait_as<kWaitHere>(smem_addr(&s_free[buf]), (done / 2 & 1) ^ 1, gave_up, progress)) break;
           for (int s = 0; s < 2 * n_slices; ++s, ++issued) {
             const uint32_t st = issued % kWideStages;
@@ -201,11 +212,12 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
               break;
             }
             tc_fence_after();
-            const uint32_t pa = smem_addr(stages + st * kStageBytes), pb = pa + kTileABytes;
+            const uint32_t pa = tmem + 2 * kInt8Columns + st * kWideColumns;
+            const uint32_t pb = smem_addr(stages + st * kTileBBytes);
 #pragma unroll
             for (int i = 0; i < kSlice / 16; ++i)
-              tc_mma(acc, smem_desc(pa + i * 32, 16, 1024), smem_desc(pb + i * 32, 16, 1024), idesc,
-                     s > 0 || i > 0);
+              tc_mma_tmem(acc, pa + i * 8, smem_desc(pb + i * 32, 16, 1024), idesc,
+                          s > 0 || i > 0);
             tc_commit(smem_addr(&s_empty[st]), both);
           }
           if (ok) tc_commit(smem_addr(&s_done[buf]), both);
@@ -224,54 +236,63 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
     }
   } else if (warp >= kConvert) {
     fewer_registers<kInt8ConvertRegisters>();
-    // Warps 0-3 have the 128 rows of A, 4-7 those of B, a lane one row: chunk c of 16
-    // codes lies at c ^ (row % 8), and makes the chunks 2 c and 2 c + 1 of 8 numbers.  A
-    // slice is read whole, so that the next copy into its stage starts at once.
-    const int w = warp - kConvert, row = (w & 3) * 32 + lane, turn = lane & 7;
-    const uint32_t offset = (w >> 2) * kTileABytes + row * 128;
+    // Warps 0-3 have the first 64 codes of a slice, 4-7 the others, a lane one row of A and
+    // one of B: chunk c of 16 codes lies at c ^ (row % 8), and makes 8 columns of the row's
+    // lane in tensor memory, or the chunks 2 c and 2 c + 1 of 8 numbers (neither access
+    // meets in a bank).  A slice is read whole, so that the next copy into its stage starts at
+    // once.
+    const int w = warp - kConvert, h = w >> 2, row = (w & 3) * 32 + lane, turn = lane & 7;
+    const uint32_t from0 = smem_addr(raw) + row * 128;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((w & 3) * 32) << 16) + 2 * kInt8Columns;
+    const uint32_t rows = smem_addr(stages) + row * 128;
     const uint32_t wide0 = cluster_addr(smem_addr(&s_wide[0]), leader);
     uint32_t step = 0;  // raw slices so far
     bool ok = true;
     for (Walk walk(pair, pairs); walk.t < total && ok; walk.next()) {
-      const Tile tile = tile_at(walk.t);
-      const bool any = w < 4 || (w & 3) * 32 < mma_n(tile.cols) / 2;
+      const bool any = (w & 3) * 32 < mma_n(tile_at(walk.t).cols) / 2;  // rows of B
       for (int s = 0; s < n_slices && ok; ++s, ++step) {
         const uint32_t st = step % kRawStages;
         if (!warp_wait_as<kWaitAwake>(smem_addr(&s_raw[st]), step / kRawStages & 1, gave_up)) {
           ok = false;
           break;
         }
-        const uint32_t from = smem_addr(raw + st * kStageBytes) + offset;
-        uint4 c[8];
+        const uint32_t from = from0 + st * kStageBytes;
+        uint4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = shared_load16(from + (((4 * h + i) ^ turn) << 4));
         if (any) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) c[i] = shared_load16(from + ((i ^ turn) << 4));
+          for (int i = 0; i < 4; ++i)
+            y[i] = shared_load16(from + kTileABytes + (((4 * h + i) ^ turn) << 4));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&s_read[st]));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t slice = 2 * step + h, at = slice % kWideStages;
-          if (!warp_wait_as<kWaitAwake>(smem_addr(&s_empty[at]), (slice / kWideStages & 1) ^ 1,
-                                        gave_up)) {
-            ok = false;
-            break;
-          }
-          if (any) {
-            const uint32_t to = smem_addr(stages + at * kStageBytes) + offset;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 v = c[4 * h + i];
-              const uint2 x = codes_to_fp16(v.x), y = codes_to_fp16(v.y);
-              const uint2 z = codes_to_fp16(v.z), u = codes_to_fp16(v.w);
-              shared_store16(to + (((2 * i) ^ turn) << 4), make_uint4(x.x, x.y, y.x, y.y));
-              shared_store16(to + (((2 * i + 1) ^ turn) << 4), make_uint4(z.x, z.y, u.x, u.y));
-            }
-            fence_async_shared();
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive_written(wide0 + at * 8);
+        const uint32_t slice = 2 * step + h, at = slice % kWideStages;
+        if (!warp_wait_as<kWaitAwake>(smem_addr(&s_empty[at]), (slice / kWideStages & 1) ^ 1,
+                                      gave_up)) {
+          ok = false;
+          break;
         }
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          tmem_store_row8(lanes + at * kWideColumns + i * 8, codes_to_fp16(x[i].x),
+                          codes_to_fp16(x[i].y), codes_to_fp16(x[i].z), codes_to_fp16(x[i].w));
+        if (any) {
+          const uint32_t to = rows + at * kTileBBytes;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint2 a0 = codes_to_fp16(y[i].x), a1 = codes_to_fp16(y[i].y);
+            const uint2 a2 = codes_to_fp16(y[i].z), a3 = codes_to_fp16(y[i].w);
+            shared_store16(to + (((2 * i) ^ turn) << 4), make_uint4(a0.x, a0.y, a1.x, a1.y));
+            shared_store16(to + (((2 * i + 1) ^ turn) << 4), make_uint4(a2.x, a2.y, a3.x, a3.y));
+          }
+          fence_async_shared();
+        }
+        tmem_wait_store();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_written(wide0 + at * 8);
       }
     }
     __syncwarp();
@@ -283,10 +304,10 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
     T* residual = kGatedForm ? nullptr : static_cast<T*>(const_cast<void*>(a.residual));
     uint32_t done = 0;
     const uint32_t free0 = cluster_addr(smem_addr(&s_free[0]), leader);
-    // Pairs that share a tile have one tile at most: its sums may lie over the fp16
+    // Pairs that share a tile have one tile at most: its sums may lie over the raw
     // stages, which are through.  A lane's 32 values of the warp's columns c: 8 steps
     // of 512 bytes from part + 64 c on.
-    const uint32_t part = smem_addr(stages + warp * 4 * 4096) + lane * 16;
+    const uint32_t part = smem_addr(raw + warp * 4 * 4096) + lane * 16;
     const uint32_t other_part = splits > 1 ? cluster_addr(part, 2 + rank) : 0;
     for (Walk walk(pair, pairs); walk.t < total; walk.next(), ++done) {
       const Tile tile = tile_at(walk.t);
@@ -306,7 +327,7 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
       const uint32_t buf = done & 1;
       if (!warp_wait_as<kWaitNap>(smem_addr(&s_done[buf]), done / 2 & 1, gave_up, progress)) break;
       tc_fence_after();
-      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kMaxN;
+      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kInt8Columns;
       if (splits > 1) {
         if (split > 0) {
           for (int c = c0; c < cols; c += 64) {

@@ -78,8 +78,9 @@ cudaError_t launch_int8(const QuantArgs& a, int sms, cudaStream_t s) {
       !make_map<uint8_t>(&map_b, a.codes, 0, a.num_rows, a.K, 64))
     return cudaErrorInvalidValue;
   const int64_t pairs = sms / 2;
-  const int splits = tile_splits(most_tiles<kUse>(a, kMaxN), ceil_div(a.K, kRawSlice), pairs);
-  const int64_t tiles = most_tiles<kUse>(a, splits > 1 ? kMaxN : kLeastCap);
+  const int splits =
+      tile_splits(most_tiles<kUse>(a, kInt8Columns), ceil_div(a.K, kRawSlice), pairs);
+  const int64_t tiles = most_tiles<kUse>(a, splits > 1 ? kInt8Columns : kLeastCap);
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
   const unsigned blocks = 2 * splits * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
   return launch_clusters(k_int8_product<T, kUse>, dim3(blocks), dim3(2 * splits), kInt8Threads,
@@ -104,7 +105,7 @@ cudaError_t launch_fp8(const QuantArgs& a, int sms, cudaStream_t s) {
 
 template <typename T, bool kFp8, bool kGatedForm>
 cudaError_t launch_quant_product(const QuantArgs& a, int sms, cudaStream_t s) {
-  if (!quant_decode_pays(kGatedForm, a.num_rows, a.E, a.K))
+  if (!quant_decode_pays(kFp8, kGatedForm, a.num_rows, a.E, a.K, kGatedForm ? a.N / 2 : a.N))
     return kFp8 ? launch_fp8<T, kGatedForm>(a, sms, s) : launch_int8<T, kGatedForm>(a, sms, s);
   // Tasks at most: every expert with rows has one group, and each further
   // kDecodeGroup rows one more.

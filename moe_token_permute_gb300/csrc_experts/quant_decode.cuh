@@ -21,14 +21,41 @@ namespace moe {
 namespace experts {
 
 constexpr int kDecodeCodes = kDecodeBlocks * 128;  // of a stage
+constexpr int kQuantDecodeGroups = 128;            // of rows; a call has no more than rows
 
-// Which calls: see decode_pays.
-inline bool quant_decode_pays(bool gated, int64_t rows, int64_t E, int64_t K) {
-  const int64_t task_bytes = (gated ? 2 : 1) * kDecodeFeatures * K;
-  const int64_t most = task_bytes >= 64 * 1024   ? kDecodeMaxRows
-                       : task_bytes >= 32 * 1024 ? kDecodeMaxRows / 2
-                                                 : 0;
-  return rows <= std::min<int64_t>(most, kDecodeGroup * E) && K % 128 == 0;
+// Which calls.  us from a graph, this kernel / tiles, on GB300 (experts x in -> features; the
+// rows go to as many experts as there are; weights not in L2):
+//   fp8   gated 128 x 2048 -> 768, 8 / 16 / 32 rows     13.6 / 14.9   21.6 / 16.1   35 / 30
+//         gated 64 x 7168 -> 2048, 8 / 32 rows          44 / 44       125 / 123
+//         gated 8 x 4096 -> 14336, 2 / 8 / 32 rows      47 / 50       96 / 88       186 / 145
+//         linear 8 x 14336 -> 4096, 2 / 8 / 32 rows     27 / 37       47 / 59       78 / 78
+//         linear 8 x 4096 -> 4096, 2 / 8 / 32 rows      13.5 / 17.5   23.7 / 22.8   44 / 29
+//         linear 1 x 4096 -> 4096, 1 / 8 / 16 rows      9.3 / 17.0    10.4 / 17.6   14.5 / 17.6
+//         linear 128 x 768 -> 2048, 64 x 2048 -> 7168, 8 rows   17.5 / 10.4   51 / 29
+//   int8  gated 128 x 1024 / 2048 -> 768, 8 rows        13.5 / 14.4   13.8 / 18.6
+//         gated 128 x 2048 -> 768, 32 / 64 rows         38 / 39       60 / 49
+//         gated 8 x 4096 -> 14336, 8 / 32 / 64 rows     101 / 139     190 / 233     271 / 233
+//         gated 64 x 4096 -> 2048, 32 / 64 rows         76 / 103      128 / 170
+//         gated 64 x 7168 -> 2048, 8 / 32 / 128 rows    46 / 73       129 / 199     252 / 376
+//         gated 8 x 7168 -> 2048, 16 x 14336 -> 2048, 8 rows of each    60 / 72     205 / 257
+//         linear 8 x 14336 -> 4096, 2 / 32 / 64 rows    28 / 43       79 / 137      109 / 137
+//         linear 16 x 7168 -> 4096, 128 rows            115 / 140
+//         linear 8 x 4096 -> 4096, 2 / 8 / 32 rows      12.4 / 18.6   23.7 / 38     42 / 47
+//         linear 1 x 4096 -> 4096, 1 / 16 rows, -> 14336, 32 rows   9.3 / 17.9   13.4 / 18.5   64 / 29
+//         linear 64 x 2048 -> 7168, 128 x 768 -> 2048, 8 rows    55 / 40    17.5 / 13.4
+// fp8 tiles stream as fast once there are enough of them for the SMs: few tiles, or, of a
+// long contraction, fewer than SMs.  int8 tiles spend their time on the codes, whatever the
+// rows: up to 8 rows of an expert on average, which are one reading of its weights; each
+// group of rows has its own pass of short lines, and more than 32 pay from long ones on.
+inline bool quant_decode_pays(bool fp8, bool gated, int64_t rows, int64_t E, int64_t K,
+                              int64_t features) {
+  if (K % 128 != 0) return false;
+  if (rows > std::max<int64_t>(2 * kDecodeGroup, kDecodeGroup * E)) return false;
+  if (!fp8)
+    return (gated ? 2 : 1) * K >= 4096 && rows <= (K >= 7168 ? kQuantDecodeGroups : kDecodeMaxRows);
+  const int64_t tiles = std::min(E, rows) * ((features + 255) / 256) * (gated ? 2 : 1);
+  return rows <= kDecodeMaxRows &&
+         ((tiles <= 48 && K >= 2048) || (tiles <= 128 && K >= 8192));
 }
 
 __device__ __forceinline__ void mma_16832(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -60,7 +87,7 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
   __shared__ __align__(8) uint64_t s_full[kRing], s_empty[kRing], s_sums[2], s_read[2];
   __shared__ int s_gave_up, s_scan[32];
   __shared__ uint32_t s_issued;  // stages that the producer has issued
-  __shared__ DecodeGroup s_groups[kDecodeMaxRows];
+  __shared__ DecodeGroup s_groups[kQuantDecodeGroups];
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Sum* parts = reinterpret_cast<Sum*>(ring + kRing * Shape::kStageBytes);
@@ -95,11 +122,11 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
     int at = groups + block_exclusive_sum((s.hi - s.lo + kDecodeGroup - 1) / kDecodeGroup, s_scan,
                                           &part);
     // Segments that overlap (bad offsets) could make more groups than rows.
-    for (int lo = s.lo; lo < s.hi && at < kDecodeMaxRows; lo += kDecodeGroup, ++at)
+    for (int lo = s.lo; lo < s.hi && at < kQuantDecodeGroups; lo += kDecodeGroup, ++at)
       s_groups[at] = {e, lo, min(kDecodeGroup, s.hi - lo)};
     groups += part;
   }
-  groups = min(groups, kDecodeMaxRows);
+  groups = min(groups, kQuantDecodeGroups);
   if (bad && a.status != nullptr && blockIdx.x == 0)
     atomicOr(a.status, MOE_FLAG_OFFSET_OUT_OF_RANGE);
   __syncthreads();

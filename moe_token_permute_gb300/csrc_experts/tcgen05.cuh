@@ -390,6 +390,26 @@ __device__ __forceinline__ void tc_commit_single(uint32_t bar) {
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
       : "memory");
 }
+// tc_mma with A in tensor memory: a block's 128 rows in its lanes, 16 bits in half a
+// column.
+__device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1 : 0)
+      : "memory");
+}
+// 8 columns of the lane's own row of tensor memory.
+__device__ __forceinline__ void tmem_store_row8(uint32_t addr, uint2 a, uint2 b, uint2 c, uint2 d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                   addr),
+               "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y), "r"(c.x), "r"(c.y), "r"(d.x), "r"(d.y)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_store() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
 // The barrier at this address in the cluster's blocks of `mask` (the pair) gets one
 // arrival when every tcgen05.mma issued before is done.
 __device__ __forceinline__ void tc_commit(uint32_t bar, uint16_t mask) {

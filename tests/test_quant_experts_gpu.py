@@ -119,6 +119,16 @@ def test_few_rows_over_long_contractions(K, N, rows, code):
 
 
 @FORMS
+@pytest.mark.parametrize("rows", [127, 128, 129])
+@pytest.mark.parametrize("E", [16, 130])
+def test_rows_of_many_experts(E, rows, code):
+    """As many groups of rows as a short call can have, and one more."""
+    counts = [rows // E + (e < rows % E) for e in range(E)]
+    run_gated(counts, 7168, 40, code, BF, "silu", rows, tail=1)
+    run_linear(counts, 7296, 72, code, HF, "none", rows, False, True, tail=2)
+
+
+@FORMS
 @pytest.mark.parametrize("rows", [1, 15, 64, 130, 300, 1000])
 @pytest.mark.parametrize("K,N", [(4096, 512), (2064, 4096)])
 def test_one_expert(K, N, rows, code):
