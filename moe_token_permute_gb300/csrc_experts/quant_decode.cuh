@@ -230,11 +230,12 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
         if (kFp8) {
 #pragma unroll
           for (int i = 0; i < kDecodeStep / 2; ++i) {
-            const int k = min(s * kDecodeBlocks + i * kDecodeSet + warp % kDecodeSet, scale_groups - 1);
+            const int b = s * kDecodeBlocks + i * kDecodeSet + warp % kDecodeSet;
+            const int k = min(b, scale_groups - 1);
             const float w = __ldg(ws + k), u = __ldg(us + k);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float v = __ldg(xs[j] + k);
+              const float v = b < scale_groups ? __ldg(xs[j] + k) : 0.f;
               by[i][j] = v * w, by[i][2 + j] = v * u;
             }
           }
@@ -268,7 +269,7 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
               mma_16832(part[j], v[i + j].x, w[i + j].x, v[i + j].y, w[i + j].y, u[i + j].x, u[i + j].y);
               mma_16832(part[j], v[i + j].z, w[i + j].z, v[i + j].w, w[i + j].w, u[i + j].z, u[i + j].w);
             }
-            // (a block behind K has zeros and the last block's scales)
+            // (a block behind K has zeros)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] += (part[0][j] + part[1][j]) * by[i / 2][j];
           }

@@ -189,6 +189,18 @@ def test_infinities_and_nan_stay_in_their_row(counts, code):
     assert torch.equal(out[~bad], clean[~bad])
 
 
+@pytest.mark.parametrize("counts", [[3, 4], [140, 90]], ids=["few", "many"])
+@pytest.mark.parametrize("K", [2048, 2176, 14336 + 128])
+def test_an_infinite_last_scale(K, counts):
+    """What a ring's last stage has behind the contraction adds nothing, not even NaN."""
+    _, n, offset, x, xs, w, ws = setup(counts, K, 256, E4M3, 1, 6)
+    x.copy_(x.float().abs().clamp(min=1).to(E4M3)), w.copy_(w.float().abs().clamp(min=1).to(E4M3))
+    xs[:, -1] = float("inf")
+    out = blank(n, 256, dtype=BF)
+    mp.moe_expert_linear_quant(x, xs, w, ws, offset, out)
+    assert (out == float("inf")).all()
+
+
 @FORMS
 def test_other_experts_cannot_be_seen(code):
     """Segments that end inside a tile, the next expert's rows being NaN."""
