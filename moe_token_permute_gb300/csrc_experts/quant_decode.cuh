@@ -7,9 +7,13 @@
 // own, which then join the task's, scaled.  int8 sums are whole numbers until the end.
 // The 8-bit forms of mma.sync are slow on GB300, so all 16 rows of their A tile are used:
 // a task of the linear product has two tiles of 8 features where it can, and an SM an
-// even share of the tiles, one after another.  (2 rows of 8 x [14336 -> 4096], int8: with 8 features
-// a task 34 us, at 81% of that pipe; with the codes made fp16 for m16n8k16 32, bound by
-// the instructions.)
+// even share of the tiles, one after another.  (2 rows of 8 x [14336 -> 4096], int8: with 8
+// features a task 34 us, with the codes made fp16 for m16n8k16 32, here 27; 4.3 TB/s, and 6.1
+// of 16384 features.  4-way dot products in the place of mma.sync: 26, but 12.4 instead of 11.4 from
+// 4096.)  What bounds short contractions is the way of a task's sums to their results, so
+// the warp that adds them up loads the next task's scales meanwhile and never sleeps (8 rows
+// of 128 x [2048 -> 2 x 768] 14.4 -> 11.4 us, of 64 x [2048 -> 7168] 55 -> 35; with two such
+// warps no better).
 #pragma once
 
 #include <type_traits>
@@ -21,41 +25,41 @@ namespace moe {
 namespace experts {
 
 constexpr int kDecodeCodes = kDecodeBlocks * 128;  // of a stage
-constexpr int kQuantDecodeGroups = 128;            // of rows; a call has no more than rows
+constexpr int kQuantDecodeGroups = 256;            // of rows; a call has no more than rows
 
 // Which calls.  us from a graph, this kernel / tiles, on GB300 (experts x in -> features; the
 // rows go to as many experts as there are; weights not in L2):
-//   fp8   gated 128 x 2048 -> 768, 8 / 16 / 32 rows     13.6 / 14.9   21.6 / 16.1   35 / 30
-//         gated 64 x 7168 -> 2048, 8 / 32 rows          44 / 44       125 / 123
-//         gated 8 x 4096 -> 14336, 2 / 8 / 32 rows      47 / 50       96 / 88       186 / 145
-//         linear 8 x 14336 -> 4096, 2 / 8 / 32 rows     27 / 37       47 / 59       78 / 78
-//         linear 8 x 4096 -> 4096, 2 / 8 / 32 rows      13.5 / 17.5   23.7 / 22.8   44 / 29
-//         linear 1 x 4096 -> 4096, 1 / 8 / 16 rows      9.3 / 17.0    10.4 / 17.6   14.5 / 17.6
-//         linear 128 x 768 -> 2048, 64 x 2048 -> 7168, 8 rows   17.5 / 10.4   51 / 29
-//   int8  gated 128 x 1024 / 2048 -> 768, 8 rows        13.5 / 14.4   13.8 / 18.6
-//         gated 128 x 2048 -> 768, 32 / 64 rows         38 / 39       60 / 49
-//         gated 8 x 4096 -> 14336, 8 / 32 / 64 rows     101 / 139     190 / 233     271 / 233
-//         gated 64 x 4096 -> 2048, 32 / 64 rows         76 / 103      128 / 170
-//         gated 64 x 7168 -> 2048, 8 / 32 / 128 rows    46 / 73       129 / 199     252 / 376
-//         gated 8 x 7168 -> 2048, 16 x 14336 -> 2048, 8 rows of each    60 / 72     205 / 257
-//         linear 8 x 14336 -> 4096, 2 / 32 / 64 rows    28 / 43       79 / 137      109 / 137
-//         linear 16 x 7168 -> 4096, 128 rows            115 / 140
-//         linear 8 x 4096 -> 4096, 2 / 8 / 32 rows      12.4 / 18.6   23.7 / 38     42 / 47
-//         linear 1 x 4096 -> 4096, 1 / 16 rows, -> 14336, 32 rows   9.3 / 17.9   13.4 / 18.5   64 / 29
-//         linear 64 x 2048 -> 7168, 128 x 768 -> 2048, 8 rows    55 / 40    17.5 / 13.4
-// fp8 tiles stream as fast once there are enough of them for the SMs: few tiles, or, of a
-// long contraction, fewer than SMs.  int8 tiles spend their time on the codes, whatever the
-// rows: up to 8 rows of an expert on average, which are one reading of its weights; each
-// group of rows has its own pass of short lines, and more than 32 pay from long ones on.
+//                                                     fp8            int8
+//   gated  128 x 1024 -> 768, 8 rows                  12.4 / 13.4    11.4 / 14.5
+//          128 x 2048 -> 768, 8 rows                  12.4 / 14.5    11.5 / 18.6
+//            16, 32 rows                    18.7 / 15.8, 30 / 30     17.7 / 28.8, 27 / 39
+//            256 rows, the same by a Zipf law                        79 / 98, 59 / 69
+//            512 rows, the same by a Zipf law                        91 / 113, 88 / 88
+//          64 x 7168 -> 2048, 8, 32, 256 rows  44 / 45, 125 / 126    46 / 73, 129 / 199, 304 / 451
+//          8 x 4096 -> 14336, 2, 8 rows       43 / 54, 87 / 90       43 / 65, 86 / 140
+//            32, 64 rows                      150 / 148, 212 / 149   148 / 233, 208 / 233
+//   linear 8 x 14336 -> 4096, 2, 8 rows       27 / 37, 48 / 70       27 / 43, 49 / 108
+//            32, 64 rows                      78 / 80, 109 / 80      79 / 137, 109 / 138
+//          8 x 4096 -> 4096, 2, 8 rows    12.1 / 17.5, 20.5 / 25.3   11.4 / 18.9, 19.8 / 38.1
+//            32, 64 rows                      30 / 29, 39 / 29       29 / 47, 37 / 47
+//          1 x 4096 -> 4096, 1, 16 rows   8.3 / 17.2, 12.4 / 17.6    8.4 / 18.5, 11.4 / 18.5
+//            32, 64 rows                      17.5 / 17.6            15.6 / 18.5, 24.7 / 18.6
+//          1 x 4096 -> 14336, 16 rows         26.6 / 21.6            23.9 / 27.9
+//          64 x 2048 -> 7168, 8, 256 rows     33 / 31                35 / 40, 245 / 247
+//          128 x 768 -> 2048, 8, 256 rows     13.5 / 10.4            12.4 / 13.5, 122 / 63
+// int8 tiles spend their time on the codes, whatever the rows: up to 8 rows of an expert on
+// average, which are one reading of its weights.  fp8 tiles stream as fast where there are
+// enough of them for the SMs, and contractions are short, or rows many.
 inline bool quant_decode_pays(bool fp8, bool gated, int64_t rows, int64_t E, int64_t K,
                               int64_t features) {
   if (K % 128 != 0) return false;
-  if (rows > std::max<int64_t>(2 * kDecodeGroup, kDecodeGroup * E)) return false;
   if (!fp8)
-    return (gated ? 2 : 1) * K >= 4096 && rows <= (K >= 7168 ? kQuantDecodeGroups : kDecodeMaxRows);
+    return (gated ? 2 : 1) * K >= 2048 &&
+           rows <= std::min<int64_t>(kQuantDecodeGroups,
+                                     std::max<int64_t>(kDecodeMaxRows, kDecodeGroup * E));
   const int64_t tiles = std::min(E, rows) * ((features + 255) / 256) * (gated ? 2 : 1);
-  return rows <= kDecodeMaxRows &&
-         ((tiles <= 48 && K >= 2048) || (tiles <= 128 && K >= 8192));
+  return (K >= 4096 && rows <= std::min<int64_t>(kDecodeMaxRows, std::max<int64_t>(8, 4 * E))) ||
+         (K >= 1024 && tiles <= 48 && rows <= 16);
 }
 
 __device__ __forceinline__ void mma_16832(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -299,28 +303,38 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
   } else {
     T* out = static_cast<T*>(a.out);
     int turn = 0;
-    for (Task t = start; t.left > 0; advance(t), ++turn) {
+    // Value j of the lane: feature and row (j * 32 + lane) of the task.
+    constexpr int kValues = kDecodeFeatures * kDecodeGroup / 32;
+    const int f = lane % kDecodeFeatures, r0 = lane / kDecodeFeatures;
+    // int8: scales of a task's two channels and of its rows; a task's are loaded while the
+    // one before is summed.
+    float w = 0.f, u = 0.f, xs[kValues] = {};
+    auto fetch = [&](const Task& t) {
+      if (kFp8 || t.left <= 0) return;
+      const DecodeGroup task = s_groups[t.group];
+      const float* ws = a.weight_scales + static_cast<int64_t>(task.e) * a.N +
+                        t.part * kDecodeFeatures + f;
+      w = __ldg(ws);
+      u = kGatedForm ? __ldg(ws + F) : t.tiles > 1 ? __ldg(ws + kDecodeFeatures) : 0.f;
+#pragma unroll
+      for (int j = 0; j < kValues; ++j)
+        xs[j] = __ldg(a.scales + task.lo + min(r0 + j * (32 / kDecodeFeatures), task.rows - 1));
+    };
+    fetch(start);
+    for (Task t = start, next; t.left > 0; t = next, ++turn) {
+      next = t;
+      advance(next);
       const DecodeGroup task = s_groups[t.group];
       const int buf = turn & 1;
-      // Value j of the lane: feature and row (j * 32 + lane) of the task.
-      constexpr int kValues = kDecodeFeatures * kDecodeGroup / 32;
-      const int f = lane % kDecodeFeatures, r0 = lane / kDecodeFeatures;
       const int c = t.part * kDecodeFeatures + f;
-      float by[kValues], by_up[kValues];
-      if (!kFp8) {
-        const float* ws = a.weight_scales + static_cast<int64_t>(task.e) * a.N + c;
-        const float w = __ldg(ws), u = kGatedForm    ? __ldg(ws + F)
-                                         : t.tiles > 1 ? __ldg(ws + kDecodeFeatures)
-                                                       : 0.f;
-#pragma unroll
-        for (int j = 0; j < kValues; ++j) {
-          const int r = min(r0 + j * (32 / kDecodeFeatures), task.rows - 1);
-          const float v = __ldg(a.scales + task.lo + r);
-          by[j] = v * w, by_up[j] = v * u;
-        }
-      }
       // (spans a task's contraction)
-      if (!warp_wait(smem_addr(&s_sums[buf]), turn / 2 & 1, gave_up, smem_addr(&s_issued))) break;
+      if (!warp_wait_as<kWaitAwake>(smem_addr(&s_sums[buf]), turn / 2 & 1, gave_up,
+                                    smem_addr(&s_issued)))
+        break;
+      float by[kValues], by_up[kValues];
+#pragma unroll
+      for (int j = 0; j < kValues; ++j) by[j] = xs[j] * w, by_up[j] = xs[j] * u;
+      fetch(next);
       Sum z[kValues], up[kValues];
 #pragma unroll
       for (int j = 0; j < kValues; ++j) {
