@@ -119,8 +119,8 @@ def test_few_rows_over_long_contractions(K, N, rows, code):
 
 
 @FORMS
-@pytest.mark.parametrize("rows", [127, 128, 129])
-@pytest.mark.parametrize("E", [16, 130])
+@pytest.mark.parametrize("E,rows", [(16, 127), (16, 128), (16, 129), (130, 129), (130, 255),
+                                    (130, 256), (130, 257)])
 def test_rows_of_many_experts(E, rows, code):
     """As many groups of rows as a short call can have, and one more."""
     counts = [rows // E + (e < rows % E) for e in range(E)]
@@ -221,14 +221,16 @@ def test_other_experts_cannot_be_seen(code):
 
 
 @FORMS
-def test_malformed_offsets(code):
-    K, N, R = 256, 136, 70
+@pytest.mark.parametrize("K,R,from0,to0,c", [(256, 70, 50, 60, 10), (4096, 12, 7, 9, 4)],
+                         ids=["tiles", "streamed"])
+def test_malformed_offsets(K, R, from0, to0, c, code):
+    N = 136
     _, _, _, x, xs, w, ws = setup([R, 0, 0], K, N, code, 1, 6)
     status = torch.zeros(mp.moe_permute_workspace_size(1, 1, 1), dtype=torch.uint8, device=DEV)
     mp.moe_permute_workspace_init(status)
-    for ends, cut in (([50, 60, 0, 10], [(50, 60), (60, 60), (0, 10)]),
-                      ([-3, 20, 10, 2 ** 40], [(0, 20), (20, 20), (10, 70)]),
-                      ([80, 90, 2 ** 33, -1], [(70, 70)] * 3)):
+    for ends, cut in (([from0, to0, 0, c], [(from0, to0), (to0, to0), (0, c)]),
+                      ([-3, c + 2, c, 2 ** 40], [(0, c + 2), (c + 2, c + 2), (c, R)]),
+                      ([R + 1, R + 9, 2 ** 33, -1], [(R, R)] * 3)):
         offset = torch.tensor(ends, device=DEV)
         out = blank(R, N, dtype=BF)
         mp.moe_clear_status(status)
@@ -243,6 +245,21 @@ def test_malformed_offsets(code):
                 want = qref.product(x[lo:hi], xs[lo:hi], w[e], ws[e], 1)
                 ref.check(out[lo:hi], want, BF, f"expert {e}")
         assert (out[~used] == SENTINEL).all()
+
+
+@FORMS
+@pytest.mark.parametrize("K,R", [(256, 70), (4096, 12)], ids=["tiles", "streamed"])
+def test_segments_that_all_overlap(K, R, code):
+    """Far more groups of rows than rows: the outputs are undefined, but only they."""
+    E, N = 600, 136
+    _, _, _, x, xs, w, ws = setup([R] + [0] * (E - 1), K, N, code, 1, 10)
+    status = torch.zeros(mp.moe_permute_workspace_size(1, 1, 1), dtype=torch.uint8, device=DEV)
+    mp.moe_permute_workspace_init(status)
+    offset = torch.tensor([R * (e % 2) for e in range(E + 1)], device=DEV)
+    out = blank(R + 64, N, dtype=BF)
+    mp.moe_expert_linear_quant(x, xs, w, ws, offset, out[:R], workspace=status)
+    assert mp.moe_read_status(status) == b.MOE_FLAG_OFFSET_OUT_OF_RANGE
+    untouched(out, R)
 
 
 @FORMS
@@ -293,7 +310,7 @@ def test_elements_beyond_32_bits(code):
     w = torch.zeros(E, N, K, dtype=torch.int8, device=DEV)
     w[-1] = make_codes(g, code, N, K).view(torch.int8)
     w = w.view(code)
-    for rows in (5, 70):
+    for rows in (5, 70, 300):
         x = make_codes(g, code, rows, K)
         shapes = qref.scale_shapes(code, rows, E, N, K, 1)
         xs, ws = (torch.rand(*s, generator=g, device=DEV) / 128 for s in shapes)

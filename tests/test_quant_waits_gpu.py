@@ -49,10 +49,11 @@ def operands(code, counts, K, N, parts, seed):
     return codes(R, K), xs, codes(E, N, K), ws, offset, status
 
 
-def test_fp8_contraction_longer_than_the_limit(debug_library):
+@pytest.mark.parametrize("R,limit", [(40, SHORT_NS), (8, SHORT_NS // 4)], ids=["tiles", "streamed"])
+def test_fp8_contraction_longer_than_the_limit(debug_library, R, limit):
     """int8's are at most MOE_INT8_MAX_IN long, which no limit of this size reaches.  The
     rows are zero but for a thousand columns, so that the sums' bound counts few groups."""
-    K, N, R = 1 << 22, 8, 40
+    K, N = 1 << 22, 8
     _, _, _, _, _, status = operands(E4M3, [1], 16, 8, 1, 1)
     g = torch.Generator(DEV).manual_seed(2)
     at = torch.randint(0, K, (1000,), generator=g, device=DEV)
@@ -64,7 +65,7 @@ def test_fp8_contraction_longer_than_the_limit(debug_library):
     w = torch.randint(0, 100, (1, N, K), generator=g, device=DEV, dtype=torch.int8).view(E4M3)
     xs, ws = torch.ones(R, K // 128, device=DEV), torch.ones(1, 1, K // 128, device=DEV)
     offset, out = torch.tensor([0, R], device=DEV), torch.empty(R, N, dtype=BF, device=DEV)
-    assert debug_library.moe_debug_set_expert_wait(0, SHORT_NS) == b.MOE_OK
+    assert debug_library.moe_debug_set_expert_wait(0, limit) == b.MOE_OK
 
     def call():
         mp.moe_expert_linear_quant(x, xs, w, ws, offset, out, workspace=status)
@@ -76,7 +77,7 @@ def test_fp8_contraction_longer_than_the_limit(debug_library):
     end.record()
     end.synchronize()
     assert mp.moe_read_status(status) == 0, "a wait gave up although the work went on"
-    assert start.elapsed_time(end) > 1.5 * SHORT_NS / 1e6, "too short to show anything"
+    assert start.elapsed_time(end) > 1.5 * limit / 1e6, "too short to show anything"
     a, c = x.view(torch.int8)[:, at].view(E4M3).double(), w.view(torch.int8)[0][:, at].view(E4M3)
     want, mag = a @ c.double().t(), a.abs() @ c.double().abs().t()
     # at most a thousand groups have terms, and each is added once
