@@ -141,10 +141,11 @@ __device__ __forceinline__ void place_in_panels(int local, int m_blocks, int n_b
 // Run by one warp: in how many blocks of each size the experts' rows are cut; the
 // choice of the most columns of a tile, returned; and each expert's first tile,
 // first[E] being the number of tiles.  Tiles have cap_of(kFirst) columns at most, with
-// `widest` always.
-template <int kFirst = 0>
+// `widest` always, and else what costs least by cost_of(cap, blocks, rows); kFewWaves: if
+// they are fewer than six waves of `workers`.
+template <int kFirst, bool kFewWaves, typename Cost>
 __device__ __forceinline__ int scan_tiles(int E, const Segment* segments, int* first, bool widest,
-                                          int m_blocks, int slices, int pairs) {
+                                          int m_blocks, int workers, Cost cost_of) {
   const int lane = threadIdx.x & 31;
   int cap = cap_of(kFirst);
   if (!widest) {
@@ -165,8 +166,9 @@ __device__ __forceinline__ int scan_tiles(int E, const Segment* segments, int* f
     }
     float cost = INFINITY;
     if (lane == kFirst ||
-        (lane > kFirst && lane < kCaps && most < (6 * pairs + m_blocks - 1) / m_blocks))
-      cost = cap_cost(mine, all, m_blocks, slices, pairs);
+        (lane > kFirst && lane < kCaps &&
+         (!kFewWaves || most < (6 * workers + m_blocks - 1) / m_blocks)))
+      cost = cost_of(cap_of(lane), mine, all);
     float best = cost;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) best = fminf(best, __shfl_xor_sync(kFullMask, best, d));
@@ -481,7 +483,10 @@ k_expert_product(const __grid_constant__ CUtensorMap map_a,
       first[before] = e;
     }
   } else if (warp == 0) {
-    const int cap = scan_tiles(a.E, segments, first, splits > 1, m_blocks, all_slices, pairs);
+    const int cap = scan_tiles<0, true>(
+        a.E, segments, first, splits > 1, m_blocks, pairs, [&](int, int blocks, int rows) {
+          return cap_cost(blocks, rows, m_blocks, all_slices, pairs);
+        });
     if (lane == 0) s_cap = cap;
   }
   tc_fence_before();

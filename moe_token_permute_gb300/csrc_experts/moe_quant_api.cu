@@ -69,6 +69,20 @@ cudaError_t launch_quant_int8(const QuantRowsArgs& a, int sms, cudaStream_t s) {
   return launch(kern, dim3(static_cast<unsigned>(grid)), kQuantThreads, 0, s, a);
 }
 
+template <typename T, int kUse, int kHalves>
+cudaError_t launch_int8_tiles(const CUtensorMap& map_a, const CUtensorMap& map_b,
+                              const QuantArgs& a, int sms, cudaStream_t s) {
+  constexpr int kStep = m_step<kUse>() / 2 * kHalves;
+  const int splits = kHalves == 1 ? tile_splits(most_tiles<kUse>(a, kInt8Columns, kStep),
+                                                ceil_div(a.K, kRawSlice), sms)
+                                  : 1;
+  const int64_t tiles = most_tiles<kUse>(a, splits > 1 ? kInt8Columns : kLeastCap, kStep);
+  if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
+  const unsigned blocks = splits * static_cast<unsigned>(std::min<int64_t>(tiles, sms / splits));
+  return launch_clusters(k_int8_product<T, kUse, kHalves>, dim3(blocks), dim3(splits),
+                         kInt8Threads, int8_product_smem(a.E), s, map_a, map_b, a);
+}
+
 template <typename T, bool kGatedForm>
 cudaError_t launch_int8(const QuantArgs& a, int sms, cudaStream_t s) {
   constexpr int kUse = kGatedForm ? kGated : kForward;
@@ -77,14 +91,9 @@ cudaError_t launch_int8(const QuantArgs& a, int sms, cudaStream_t s) {
                    : make_map<uint8_t>(&map_a, a.weight, a.E, a.N, a.K, 128)) ||
       !make_map<uint8_t>(&map_b, a.codes, 0, a.num_rows, a.K, 64))
     return cudaErrorInvalidValue;
-  const int64_t pairs = sms / 2;
-  const int splits =
-      tile_splits(most_tiles<kUse>(a, kInt8Columns), ceil_div(a.K, kRawSlice), pairs);
-  const int64_t tiles = most_tiles<kUse>(a, splits > 1 ? kInt8Columns : kLeastCap);
-  if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
-  const unsigned blocks = 2 * splits * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
-  return launch_clusters(k_int8_product<T, kUse>, dim3(blocks), dim3(2 * splits), kInt8Threads,
-                         int8_product_smem(a.E), s, map_a, map_b, a);
+  return int8_two_halves(most_tiles<kUse>(a, kInt8Columns), sms)
+             ? launch_int8_tiles<T, kUse, 2>(map_a, map_b, a, sms, s)
+             : launch_int8_tiles<T, kUse, 1>(map_a, map_b, a, sms, s);
 }
 
 template <typename T, bool kGatedForm>

@@ -97,14 +97,15 @@ bool make_gated_map(CUtensorMap* map, const void* base, int64_t E, int64_t F, in
                            {kLineValues<T>, 8, 2, 8, 1});
 }
 
-// The most tiles a product may have, of at most `columns` columns each.
+// The most tiles a product may have, of `step` features and at most `columns` columns
+// each.
 template <int kUse, typename Args>
-int64_t most_tiles(const Args& a, int columns) {
+int64_t most_tiles(const Args& a, int columns, int step = m_step<kUse>()) {
   const int64_t m = kUse == kForward || kUse == kWeightGrad ? a.N : kUse == kGated ? a.N / 2 : a.K;
   const int64_t blocks = kUse == kWeightGrad ? a.E * ceil_div(a.K, kMaxN)
                          : a.E == 1          ? ceil_div(a.num_rows, columns)
                                     : a.num_rows / columns + std::min<int64_t>(a.E, a.num_rows);
-  return ceil_div(m, m_step<kUse>()) * blocks;
+  return ceil_div(m, step) * blocks;
 }
 
 // Pairs that share a tile, each with 4 slices at least.

@@ -55,13 +55,6 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
-// Behind writes to this block's shared memory and fence_async_shared: what the peer then
-// starts are products, which read them where they lie.  The cluster's release waits until
-// all that went before is performed everywhere, which here is nothing (an int8 product's
-// slice took 2800 cycles so).
-__device__ __forceinline__ void mbar_arrive_written(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 // Says only that this warp is through with reading, its values being in
 // registers: unlike a release it does not wait until the global stores before it
 // are performed, 1500 cycles.
@@ -317,6 +310,14 @@ __device__ __forceinline__ void tma_load_4d_single(uint32_t dst, const CUtensorM
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_5d_single(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, int w, int v, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
+      : "memory");
+}
 
 // A plain copy of `bytes` (a multiple of 16, both sides 16-byte aligned) to
 // this block's shared memory.
@@ -390,22 +391,25 @@ __device__ __forceinline__ void tc_commit_single(uint32_t bar) {
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
       : "memory");
 }
-// tc_mma with A in tensor memory: a block's 128 rows in its lanes, 16 bits in half a
-// column.
-__device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                            bool accumulate) {
+// 16-bit operands in one block, A in tensor memory: 128 rows in its lanes, 16 bits in
+// half a column.
+__device__ __forceinline__ void tc_mma_tmem_single(uint32_t d, uint32_t a, uint64_t b,
+                                                   uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1 : 0)
       : "memory");
 }
-// 8 columns of the lane's own row of tensor memory.
-__device__ __forceinline__ void tmem_store_row8(uint32_t addr, uint2 a, uint2 b, uint2 c, uint2 d) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
-                   addr),
-               "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y), "r"(c.x), "r"(c.y), "r"(d.x), "r"(d.y)
-               : "memory");
+// 16 columns of the lane's own row of tensor memory.
+__device__ __forceinline__ void tmem_store_row16(uint32_t addr, const uint2 (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, "
+      "%9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(v[0].x), "r"(v[0].y), "r"(v[1].x), "r"(v[1].y), "r"(v[2].x), "r"(v[2].y),
+      "r"(v[3].x), "r"(v[3].y), "r"(v[4].x), "r"(v[4].y), "r"(v[5].x), "r"(v[5].y),
+      "r"(v[6].x), "r"(v[6].y), "r"(v[7].x), "r"(v[7].y)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_wait_store() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
