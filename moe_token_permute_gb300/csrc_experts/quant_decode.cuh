@@ -236,10 +236,11 @@ k_quant_decode(const __grid_constant__ CUtensorMap map, const QuantArgs a) {
           for (int i = 0; i < kDecodeStep / 2; ++i) {
             const int b = s * kDecodeBlocks + i * kDecodeSet + warp % kDecodeSet;
             const int k = min(b, scale_groups - 1);
-            const float w = __ldg(ws + k), u = __ldg(us + k);
+            const bool in = b < scale_groups;  // (no scale but 0 behind: it may be infinite)
+            const float w = in ? __ldg(ws + k) : 0.f, u = in ? __ldg(us + k) : 0.f;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float v = b < scale_groups ? __ldg(xs[j] + k) : 0.f;
+              const float v = in ? __ldg(xs[j] + k) : 0.f;
               by[i][j] = v * w, by[i][2 + j] = v * u;
             }
           }

@@ -326,3 +326,22 @@ def test_elements_beyond_32_bits(code):
 def test_no_rows(code):
     _, _, offset, x, xs, w, ws = setup([0, 0], 64, 32, code, 2, 9)
     mp.moe_expert_gated_quant(x, xs, w, ws, offset, blank(0, 16, dtype=BF))
+
+
+@pytest.mark.parametrize("counts", [[3, 4], [140, 90]], ids=["few", "many"])
+@pytest.mark.parametrize("K", [2048, 2176, 4096 + 384, 14336 + 128])
+def test_an_infinite_last_weight_scale(K, counts):
+    """The same where the scales of the weights' last blocks are infinite: in the linear
+    product, and of the gate rows, the up rows or both."""
+    _, n, offset, x, xs, w, ws = setup(counts, K, 256, E4M3, 2, 6)
+    x.copy_(x.float().abs().clamp(min=1).to(E4M3)), w.copy_(w.float().abs().clamp(min=1).to(E4M3))
+    out, h = blank(n, 256, dtype=BF), blank(n, 128, dtype=BF)
+    for blocks in ([0], [1], [0, 1]):  # of 128 features: gate and up rows, if gated
+        scales = ws.clone()
+        scales[:, blocks, -1] = float("inf")
+        mp.moe_expert_linear_quant(x, xs, w, scales, offset, out)
+        mp.moe_expert_gated_quant(x, xs, w, scales, offset, h)
+        for block in (0, 1):
+            part = out[:, 128 * block:128 * block + 128]
+            assert (part == float("inf")).all() if block in blocks else part.isfinite().all()
+        assert (h == float("inf")).all()
