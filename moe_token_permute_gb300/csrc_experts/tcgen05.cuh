@@ -144,7 +144,12 @@ __device__ __forceinline__ bool mbar_test_here(uint32_t bar, uint32_t parity) {
 // rows may be counted up to 2^31) names the count of what a producer has issued,
 // which moves with every slice: only where that stands still too has something gone
 // wrong.  The count is in shared memory of this block or of another of the cluster.
+// The clock decides; the count of polls only ends a wait if the clock should stand still, and
+// takes longer than kWaitNs however a wait polls: a poll is a test of the barrier and a
+// load from shared memory behind it, more than 8 cycles at 2.07 GHz.
 constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr unsigned kMostPolls = 1u << 30;
+static_assert(kMostPolls * 4ull > 2 * kWaitNs, "a wait that makes progress outlasts the polls");
 constexpr uint32_t kNoProgress = 0xffffffffu;
 
 #ifdef MOE_DEBUG_HOOKS
@@ -194,7 +199,7 @@ __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, vo
                                                uint32_t progress) {
   unsigned long long t0 = now_ns();
   uint32_t seen = progress_at(progress);
-  for (unsigned i = 0; i < (1u << 26); ++i) {
+  for (unsigned i = 0; i < kMostPolls; ++i) {
     if (mbar_poll<kHow>(bar, parity)) return true;
     if (*gave_up != 0) return false;
     if ((i & 63u) == 63u && now_ns() - t0 > wait_ns()) {
