@@ -409,7 +409,7 @@ k_quant_product(const __grid_constant__ CUtensorMap map_rows,
       // Frees the scales of slice s, which is through, if its chunk is.
       auto scales_used = [&](int s) {
         if (s % kScaleChunk != kScaleChunk - 1 && s != n_slices - 1) return;
-        if (lane == 0) mbar_arrive_relaxed(smem_addr(&s_used[step]));
+        if (lane == 0) mbar_arrive(smem_addr(&s_used[step]));  // behind a __syncwarp
         if (++step == kScaleChunks) step = 0, scale_pass ^= 1;
       };
       if (!any) {  // no rows: only makes room

@@ -36,7 +36,8 @@ __device__ __forceinline__ void mbar_init_fence() {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Says only that this warp is through with reading (see mbar_arrive_relaxed_cluster).
+// Behind tc_fence_before: says only that this warp has read its tensor memory (see
+// mbar_arrive_relaxed_cluster).
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
