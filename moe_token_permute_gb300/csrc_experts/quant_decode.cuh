@@ -28,38 +28,51 @@ constexpr int kDecodeCodes = kDecodeBlocks * 128;  // of a stage
 constexpr int kQuantDecodeGroups = 256;            // of rows; a call has no more than rows
 
 // Which calls.  us from a graph, this kernel / tiles, on GB300 (experts x in -> features; the
-// rows go to as many experts as there are; weights not in L2):
-//                                                     fp8            int8
-//   gated  128 x 1024 -> 768, 8 rows                  12.4 / 13.4    11.4 / 14.5
-//          128 x 2048 -> 768, 8 rows                  12.4 / 14.5    11.5 / 18.6
-//            16, 32 rows                    18.7 / 15.8, 30 / 30     17.7 / 28.8, 27 / 39
-//            256 rows, the same by a Zipf law                        79 / 98, 59 / 69
-//            512 rows, the same by a Zipf law                        91 / 113, 88 / 88
-//          64 x 7168 -> 2048, 8, 32, 256 rows  44 / 45, 125 / 126    46 / 73, 129 / 199, 304 / 451
-//          8 x 4096 -> 14336, 2, 8 rows       43 / 54, 87 / 90       43 / 65, 86 / 140
-//            32, 64 rows                      150 / 148, 212 / 149   148 / 233, 208 / 233
-//   linear 8 x 14336 -> 4096, 2, 8 rows       27 / 37, 48 / 70       27 / 43, 49 / 108
-//            32, 64 rows                      78 / 80, 109 / 80      79 / 137, 109 / 138
-//          8 x 4096 -> 4096, 2, 8 rows    12.1 / 17.5, 20.5 / 25.3   11.4 / 18.9, 19.8 / 38.1
-//            32, 64 rows                      30 / 29, 39 / 29       29 / 47, 37 / 47
-//          1 x 4096 -> 4096, 1, 16 rows   8.3 / 17.2, 12.4 / 17.6    8.4 / 18.5, 11.4 / 18.5
-//            32, 64 rows                      17.5 / 17.6            15.6 / 18.5, 24.7 / 18.6
-//          1 x 4096 -> 14336, 16 rows         26.6 / 21.6            23.9 / 27.9
-//          64 x 2048 -> 7168, 8, 256 rows     33 / 31                35 / 40, 245 / 247
-//          128 x 768 -> 2048, 8, 256 rows     13.5 / 10.4            12.4 / 13.5, 122 / 63
-// int8 tiles spend their time on the codes, whatever the rows: up to 8 rows of an expert on
-// average, which are one reading of its weights.  fp8 tiles stream as fast where there are
-// enough of them for the SMs, and contractions are short, or rows many.
+// rows go to as many experts as there are, evenly, or z: by a Zipf law; weights not in L2):
+//                                                  fp8                  int8
+//   gated  128 x 1024 -> 768, 8, 32 rows           11.1 / 12.5          10.8 / 13.4, 27 / 26
+//            256 rows, z                                                85 / 60, 55 / 35
+//          128 x 2048 -> 768, 8, 16 rows           12.1 / 14.7, 19 / 16 11.9 / 19.1, 17 / 24
+//            10, 12, 13 rows               14.2 / 15.3, 15.5 / 16.1, 16.3 / 15.1
+//            32, 256 rows, z              32 / 30, 105 / 76, 69 / 43    28 / 41, 86 / 102, 57 / 57
+//          128 x 2048 -> 1024, 1280, 8 rows        14.3 / 15.4, 16.5 / 15.2
+//          64 x 7168 -> 2048, 8, 32 rows           44 / 44, 146 / 156   45 / 60, 151 / 212
+//            256 rows, z                           287 / 279, 301 / 232 295 / 364, 306 / 312
+//          8 x 4096 -> 14336, 2, 8, 64 rows   44 / 53, 149 / 147, 152 / 146   42 / 68, 143 / 186, 147 / 187
+//          1 x 4096 -> 14336, 8, 16, 17 rows  26 / 26, 43 / 26, 62 / 27       25 / 38, 38 / 38, 59 / 38
+//          1 x 2048 -> 6144, 8, 16, 24 rows   12.5 / 15.4, 18 / 15            11.6 / 17.6, 16 / 18, 21 / 18
+//   linear 8 x 14336 -> 4096, 2, 8, 64 rows   26 / 36, 77 / 77, 79 / 77       27 / 52, 78 / 107, 79 / 108
+//          8 x 4096 -> 4096, 2, 8, 64 rows    12.6 / 17, 30 / 28, 30 / 29     11.9 / 20, 28 / 38, 29 / 38
+//          1 x 4096 -> 4096, 1, 16 rows       8.9 / 15.8, 11.5 / 16.7         8.8 / 18.8, 10.8 / 18.8
+//            32, 64 rows                      16.4 / 16.8, 28 / 18            14.8 / 18.9, 24 / 20
+//          1 x 4096 -> 14336, 8, 16, 24 rows  17 / 20, 26 / 20, 36 / 20       16 / 29, 22 / 29, 32 / 29
+//          1 x 14336 -> 4096, 16, 32 rows     24 / 35, 37 / 35                23 / 50, 34 / 50
+//          2 x 4096 -> 14336, 16, 24 rows     27 / 26, 46 / 26                26 / 38, 39 / 38
+//          3 x 4096 -> 14336, 24, 32 rows     37 / 48, 66 / 48                35 / 67, 60 / 67
+//          64 x 2048 -> 7168, 8, 16, 256 rows 35 / 30, 234 / 147              34 / 40, 61 / 56, 212 / 192
+//          64 x 2048 -> 2048, 8, 10 rows      14.2 / 15.1, 16.8 / 14.7
+//          128 x 2048 -> 2048, 32, 128 rows                                   38 / 41, 127 / 116
+//          64 x 2816 -> 2048, 64 rows, 256 z                                  81 / 91, 83 / 71
+//          128 x 768 -> 2048, 8, 256 rows     13.0 / 9.8, 127 / 44            12.1 / 12.6, 123 / 56
+// A group of rows is one reading of its expert's weights, and a task costs about 0.7 us beside
+// its loads.  int8 tiles spend their time on the codes, whatever the rows, so that int8 streams
+// while rows are one reading of the weights on average, and contractions long; fp8 tiles
+// stream as fast where there are enough of them for the SMs.
 inline bool quant_decode_pays(bool fp8, bool gated, int64_t rows, int64_t E, int64_t K,
                               int64_t features) {
-  if (K % 128 != 0) return false;
-  if (!fp8)
-    return (gated ? 2 : 1) * K >= 2048 &&
-           rows <= std::min<int64_t>(kQuantDecodeGroups,
-                                     std::max<int64_t>(kDecodeMaxRows, kDecodeGroup * E));
-  const int64_t tiles = std::min(E, rows) * ((features + 255) / 256) * (gated ? 2 : 1);
-  return (K >= 4096 && rows <= std::min<int64_t>(kDecodeMaxRows, std::max<int64_t>(8, 4 * E))) ||
-         (K >= 1024 && tiles <= 48 && rows <= 16);
+  if (K % 128 != 0 || rows > kQuantDecodeGroups) return false;
+  const int64_t used = std::min(E, rows);
+  const int64_t groups = used + (rows - used) / kDecodeGroup;  // about
+  // Of the tiled kernel, if every group had its own.
+  const int64_t tiles = groups * ((features + (gated ? 127 : 255)) / (gated ? 128 : 256));
+  if (fp8)
+    return rows <= kDecodeMaxRows && ((K >= 4096 && rows <= std::max<int64_t>(8, 4 * E)) ||
+                                      (K >= 1024 && tiles <= 64));
+  const int64_t contraction = (gated ? 2 : 1) * K;  // of a task
+  if (contraction < 2048) return false;
+  if (rows > kDecodeGroup * E)
+    return rows <= kDecodeMaxRows && (tiles <= 96 || (K >= 4096 && rows <= 2 * kDecodeGroup));
+  return contraction >= 2816 || tiles <= 256;
 }
 
 __device__ __forceinline__ void mma_16832(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
