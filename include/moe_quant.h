@@ -24,7 +24,13 @@
  *    rows (ffn_size, out_size) multiples of 8; matrix bases are 16-byte aligned,
  *    scales 4-byte aligned.
  *  - int8: in_size is at most MOE_INT8_MAX_IN, so that a sum of products of any codes
- *    fits 32 bits.
+ *    fits 32 bits.  Calls of few rows add whole numbers, which is exact.  Others add in
+ *    fp32: exact while the sums of a result's products, in any order, stay within 2^24 in
+ *    magnitude, and rounded beyond, by at most in_size * 2^-23 of the sum of the products'
+ *    magnitudes.  The same row may then give different results in calls of different
+ *    num_rows.
+ *  - A sum is multiplied by the fp32 product of its two scales, which should be neither
+ *    subnormal nor infinite where the scales are not.
  */
 #ifndef MOE_QUANT_H
 #define MOE_QUANT_H

@@ -12,6 +12,7 @@ import torch
 
 import expert_ref as ref
 import moe_token_permute_gb300 as mp
+import quant_ref as qref
 from moe_token_permute_gb300 import _binding as b
 
 pytestmark = pytest.mark.gpu
@@ -104,3 +105,27 @@ def test_a_wait_that_runs_out_is_flagged(monkeypatch, form, K, N):
     mp.moe_clear_status(status)
     assert torch.equal(call(), want)
     assert mp.moe_read_status(status) == 0
+
+
+@pytest.mark.parametrize("rows", [3, 8, 200, 3000], ids=["streamed", "streamed8", "tiles", "tiles2"])
+@pytest.mark.parametrize("K,N", [(4096, 512), (14336, 264)])
+def test_sums_that_pass_24_bits_and_cancel(rows, K, N):
+    """Few rows are added in whole numbers: exact.  More are added in fp32, whose roundings
+    beyond 2^24 stay within the bound of the sums' size, whatever is left of them."""
+    g = torch.Generator(DEV).manual_seed(K + rows)
+    half = torch.randint(100, 128, (rows, K // 2), generator=g, device=DEV)
+    x = torch.cat([half, -half.flip(1)], 1)
+    x[:, ::97] += torch.randint(-9, 1, (rows, len(range(0, K, 97))), generator=g, device=DEV)
+    w = torch.randint(100, 128, (1, N, K // 2), generator=g, device=DEV)
+    w = torch.cat([w, w.flip(2)], 2).to(torch.int8)
+    x = x.clamp(-128, 127).to(torch.int8)
+    assert (x[:, :K // 2].double() @ w[0, :, :K // 2].double().t()).min() > 2 ** 24
+    xs, ws = torch.full((rows, 1), 2.0 ** -6, device=DEV), torch.full((1, N), 2.0 ** -6, device=DEV)
+    offset = torch.tensor([0, rows], device=DEV)
+    out = torch.empty(rows, N, dtype=BF, device=DEV)
+    mp.moe_expert_linear_quant(x, xs, w, ws, offset, out)
+    sums = x.double() @ w[0].double().t() * 2.0 ** -12
+    if rows <= 8:
+        assert torch.equal(out, sums.to(BF))
+    else:
+        ref.check(out, qref.product(x, xs, w[0], ws[0], 1), BF, "out")
