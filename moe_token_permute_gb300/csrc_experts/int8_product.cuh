@@ -14,13 +14,15 @@
 // start only when both blocks' codes are written, and a release that orders them across
 // the blocks takes longer than the conversion of a slice (one expert, 8191 rows, 4096 ->
 // 4096: 343 us; with tiles of 128 columns and twice the stages 320).
-// What bounds the kernel is shared memory: copies, reads and the products of both halves
-// move 131 KB for 64 codes of 192 columns, 1024 of the 1170 cycles that they take (768 of
-// products).  Beyond 96 columns tensor memory has no room for two tiles' accumulators, and
-// the products wait for a tile's results: 60 us of that layer's with gelu and residual.
-// On GB300, us: that layer 262 (1.05 PFLOP/s); 8 experts, 8192 rows, 14336 -> 4096 741 (1.3);
+// 64 codes deep and 176 columns wide a tile takes 1090 cycles, 700 of products.  No unit is at
+// its limit (4096 rows of that layer: tensor pipe 39% of the time, issue slots 50, shared
+// memory's pipe 38), but a stage's way from the converting warps to its products and back
+// takes two stages' time, and tensor memory has room for no more.  Beyond 96 columns it has none either for two tiles'
+// accumulators, and the products wait for a tile's results: 60 us of that layer's with
+// gelu and residual.
+// On GB300, us: that layer 249 (1.10 PFLOP/s); 8 experts, 8192 rows, 14336 -> 4096 750 (1.28);
 // 128 experts, 512 rows by a Zipf law, gated, 2048 -> 2 x 768 71; 256 experts, 32768 rows,
-// 2048 -> 7168 1333.
+// 2048 -> 7168 1301.
 //   warps 0-7    epilogue: tensor memory -> registers, scaled -> shared -> rows
 //   warps 8-15   codes -> fp16
 //   warp 16      TMA producer: 128 codes deep
@@ -42,10 +44,19 @@ constexpr int kInt8Widest = 4;     // of cap_of: columns of a tile at most
 constexpr int kInt8Columns = kMaxN - 16 * kInt8Widest;
 constexpr int kInt8DataBytes = 192 * 1024;  // of stages
 constexpr int kInt8Threads = 640;
-constexpr int kInt8EpilogueRegisters = 136, kInt8ConvertRegisters = 80, kInt8OtherRegisters = 48;
-static_assert(2 * kInt8EpilogueRegisters + 2 * kInt8ConvertRegisters + kInt8OtherRegisters <=
-                  65536 / 640 / 8 * 8 * 5,
-              "registers at launch: 96 a thread");
+// Registers of a thread, and whether the weights' codes are converted ahead of the wait for
+// room, which takes 16 more: linear products in two halves, whose tiles of more than 160
+// columns have two stages (one expert, 8191 rows, 4096 -> 4096 262 -> 248 us; gated ones, whose
+// epilogue needs the registers, 141 -> 144 at 16 experts, 12288 rows, 2048 -> 2 x 1408).
+template <int kUse, int kHalves>
+struct Int8Registers {
+  static constexpr bool kEarly = kUse == kForward && kHalves == 2;
+  static constexpr int kEpilogue = kEarly ? 120 : 128, kConvert = kEarly ? 88 : 80, kOther = 64;
+  static constexpr int kLaunch = 65536 / kInt8Threads / 8 * 8;
+  static_assert(2 * kEpilogue + 2 * kConvert + kOther <= 5 * kLaunch, "what the block has");
+  static_assert(kEpilogue >= kLaunch && kConvert <= kLaunch && kOther <= kLaunch,
+                "setmaxnreg.inc gives no fewer than a thread has, .dec no more");
+};
 
 // Dynamic shared memory: stages (1024-byte aligned), staging, then each expert's rows and
 // its first tile.
@@ -119,6 +130,20 @@ __device__ __forceinline__ uint2 codes_to_fp16(uint32_t c) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
+// 16 codes as fp16.
+struct Wide16 {
+  uint2 v[4];
+  Wide16() = default;
+  __device__ __forceinline__ explicit Wide16(uint4 c)
+      : v{codes_to_fp16(c.x), codes_to_fp16(c.y), codes_to_fp16(c.z), codes_to_fp16(c.w)} {}
+  // Computed ahead of what stands behind this.
+  __device__ __forceinline__ void keep() {
+    asm volatile(""
+                 : "+r"(v[0].x), "+r"(v[0].y), "+r"(v[1].x), "+r"(v[1].y), "+r"(v[2].x),
+                   "+r"(v[2].y), "+r"(v[3].x), "+r"(v[3].y));
+  }
+};
+
 // map_a: the weight's codes as TMA tiles of 128 bytes by 128 rows (gated: make_gated_map);
 // map_b: the rows' by 64 rows.  A block, or (kHalves = 1) two in a cluster, which share a
 // tile's contraction.
@@ -126,6 +151,7 @@ template <typename T, int kUse, int kHalves>
 __global__ void __launch_bounds__(kInt8Threads, 1)
 k_int8_product(const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b, const QuantArgs a) {
+  using Registers = Int8Registers<kUse, kHalves>;
   constexpr bool kGatedForm = kUse == kGated;
   constexpr int kHalfStep = m_step<kUse>() / 2;  // features of 128 rows of A
   extern __shared__ uint8_t smem_raw[];
@@ -214,7 +240,7 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
   auto mma_n = [](int cols) { return (cols + 15) / 16 * 16; };
 
   if (warp >= kProducer) {
-    fewer_registers<kInt8OtherRegisters>();
+    fewer_registers<Registers::kOther>();
     if (warp == kProducer) {
       if (elect_one()) {
         Int8Ring ring = {0, 0};
@@ -311,7 +337,7 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
       __syncwarp();
     }
   } else if (warp >= kConvert) {
-    fewer_registers<kInt8ConvertRegisters>();
+    fewer_registers<Registers::kConvert>();
     // A lane has one row of A, and chunks of 16 codes of B.  Two halves: warps 0-3 have the
     // first's rows, 4-7 the second's, and all work on one stage of 64 codes.  One half: warps
     // 0-3 have the first 64 codes of a slice, 4-7 the others.  Chunk c of a row lies at
@@ -357,6 +383,11 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&s_read[from.at]));
           }
+          Wide16 v[4];
+          if (Registers::kEarly) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = Wide16(x[j]), v[j].keep();
+          }
           if (!warp_wait_as<kWaitAwake>(smem_addr(&s_empty[ring.at]), ring.pass ^ 1, gave_up)) {
             ok = false;
             break;
@@ -365,22 +396,19 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
           const uint32_t at_a = a_to + ring.at * kHalves * kWideColumns;
 #pragma unroll
           for (int j = 0; j < 4; j += 2) {
-            const uint2 v[8] = {codes_to_fp16(x[j].x),     codes_to_fp16(x[j].y),
-                                codes_to_fp16(x[j].z),     codes_to_fp16(x[j].w),
-                                codes_to_fp16(x[j + 1].x), codes_to_fp16(x[j + 1].y),
-                                codes_to_fp16(x[j + 1].z), codes_to_fp16(x[j + 1].w)};
-            tmem_store_row16(at_a + j * 8, v);
+            if (!Registers::kEarly) v[j] = Wide16(x[j]), v[j + 1] = Wide16(x[j + 1]);
+            tmem_store_row16(at_a + j * 8, v[j].v, v[j + 1].v);
           }
           const uint32_t at_b = b_to + ring.at * shape.wide_bytes;
 #pragma unroll
           for (int j = 0; j < kMost; ++j)
             if (j * kRowStep < rows) {
-              const uint2 a0 = codes_to_fp16(y[j].x), a1 = codes_to_fp16(y[j].y);
-              const uint2 a2 = codes_to_fp16(y[j].z), a3 = codes_to_fp16(y[j].w);
+              const Wide16 b(y[j]);
               const uint32_t to = at_b + j * kRowStep * 128;
-              shared_store16(to + (((2 * b_chunk) ^ turn) << 4), make_uint4(a0.x, a0.y, a1.x, a1.y));
+              shared_store16(to + (((2 * b_chunk) ^ turn) << 4),
+                             make_uint4(b.v[0].x, b.v[0].y, b.v[1].x, b.v[1].y));
               shared_store16(to + (((2 * b_chunk + 1) ^ turn) << 4),
-                             make_uint4(a2.x, a2.y, a3.x, a3.y));
+                             make_uint4(b.v[2].x, b.v[2].y, b.v[3].x, b.v[3].y));
             }
           fence_async_shared();
           tmem_wait_store();
@@ -394,7 +422,7 @@ k_int8_product(const __grid_constant__ CUtensorMap map_a,
     }
     __syncwarp();
   } else {
-    more_registers<kInt8EpilogueRegisters>();
+    more_registers<Registers::kEpilogue>();
     const int quad = warp & 3, g = lane >> 2, q = lane & 3;
     const uint32_t stage = smem_addr(staging + warp * kStagingWarpBytes);
     T* out = static_cast<T*>(a.out);

@@ -408,13 +408,14 @@ __device__ __forceinline__ void tc_mma_tmem_single(uint32_t d, uint32_t a, uint6
       : "memory");
 }
 // 16 columns of the lane's own row of tensor memory.
-__device__ __forceinline__ void tmem_store_row16(uint32_t addr, const uint2 (&v)[8]) {
+__device__ __forceinline__ void tmem_store_row16(uint32_t addr, const uint2 (&a)[4],
+                                                 const uint2 (&b)[4]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, "
       "%9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
-      "r"(v[0].x), "r"(v[0].y), "r"(v[1].x), "r"(v[1].y), "r"(v[2].x), "r"(v[2].y),
-      "r"(v[3].x), "r"(v[3].y), "r"(v[4].x), "r"(v[4].y), "r"(v[5].x), "r"(v[5].y),
-      "r"(v[6].x), "r"(v[6].y), "r"(v[7].x), "r"(v[7].y)
+      "r"(a[0].x), "r"(a[0].y), "r"(a[1].x), "r"(a[1].y), "r"(a[2].x), "r"(a[2].y),
+      "r"(a[3].x), "r"(a[3].y), "r"(b[0].x), "r"(b[0].y), "r"(b[1].x), "r"(b[1].y),
+      "r"(b[2].x), "r"(b[2].y), "r"(b[3].x), "r"(b[3].y)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_store() {
