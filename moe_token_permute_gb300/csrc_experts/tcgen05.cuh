@@ -184,14 +184,13 @@ __device__ __forceinline__ uint32_t progress_at(uint32_t addr) {
 //   kWaitCluster, kWaitHere  asleep for kNapNs, with the cluster's acquire or this block's;
 //                            a warp that fell asleep takes up to 1000 cycles to wake up
 //   kWaitAwake               all the time
-//   kWaitNap                 twice a microsecond
-enum Wait { kWaitCluster, kWaitHere, kWaitAwake, kWaitNap };
+enum Wait { kWaitCluster, kWaitHere, kWaitAwake };
 template <Wait kHow>
 __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
   if (kHow == kWaitCluster) return mbar_try(bar, parity);
   if (kHow == kWaitHere) return mbar_try_here(bar, parity);
   if (mbar_test_here(bar, parity)) return true;
-  __nanosleep(kHow == kWaitNap ? 500 : 20);
+  __nanosleep(20);
   return false;
 }
 
@@ -250,7 +249,7 @@ __device__ __forceinline__ bool warp_wait_as(uint32_t bar, uint32_t parity, vola
                                              uint32_t progress = kNoProgress) {
   // The whole warp asks once: without the split into lanes, a wait that is over costs a
   // third.
-  if (kHow >= kWaitAwake && __all_sync(0xffffffffu, mbar_test_here(bar, parity))) return true;
+  if (kHow == kWaitAwake && __all_sync(0xffffffffu, mbar_test_here(bar, parity))) return true;
   bool ok = true;
   if ((threadIdx.x & 31) == 0) ok = mbar_wait_as<kHow>(bar, parity, gave_up, progress);
   return __all_sync(0xffffffffu, ok);
