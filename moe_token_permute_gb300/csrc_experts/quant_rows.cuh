@@ -19,8 +19,9 @@ namespace experts {
 
 constexpr int kQuantThreads = 256;
 // Blocks of an SM, which run all at the same time.  8192 x 14336 bf16 to fp8, with 1 piece in
-// flight and 8 blocks 69 us, 2 and 5 59, 2 and 6 68 (spilled registers), 3 and 4 61, 4 and 4 62;
-// to int8, with 3 blocks 61, 4 59, 5 66 (spilled).  At the copy bandwidth it would be 52.
+// flight and 8 blocks 69 us, 2 and 5 59 (one register spilled), 2 and 6 68 (more), 3 and 4 61, 4 and
+// 4 62; to int8, with 3 blocks 61, 4 59 (12 spilled), 5 66 (more).  At the copy bandwidth it
+// would be 52.
 constexpr int kFp8Blocks = 5, kInt8Blocks = 4;
 constexpr float kInt8Max = 127.0f;
 

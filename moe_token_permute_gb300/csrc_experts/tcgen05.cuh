@@ -147,7 +147,7 @@ __device__ __forceinline__ bool mbar_test_here(uint32_t bar, uint32_t parity) {
 // wrong.  The count is in shared memory of this block or of another of the cluster.
 // The clock decides; the count of polls only ends a wait if the clock should stand still, and
 // takes longer than kWaitNs however a wait polls: a poll is a test of the barrier and a
-// load from shared memory behind it, more than 8 cycles at 2.07 GHz.
+// load from shared memory behind it, more than 9 cycles at 2.07 GHz.
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr unsigned kMostPolls = 1u << 30;
 static_assert(kMostPolls * 4ull > 2 * kWaitNs, "a wait that makes progress outlasts the polls");
